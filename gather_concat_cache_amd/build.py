@@ -21,10 +21,14 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgcache.so")
 SOURCES = ["ds_mla_kernels.hip", "nvfp4_kv_kernels.hip", "sparse_index.hip", "gcache_abi.hip"]
+# the operators around the cache (include/gcache_attention.h, include/gcache_pages.h)
+OPERATOR_SOURCES = ["attention_kernels.hip", "qk_norm_rope.hip", "page_kernels.hip", "operators_abi.hip"]
 # measurement helper beside the library (include/gcache_bench.h), loaded by bench.py only
 BENCH_LIB = os.path.join(PKG, "libgcache_bench.so")
 BENCH_SOURCES = ["bench_ceiling.hip"]
 HEADERS = ["gcache_device.h", "gcache_internal.h"]
+OPERATOR_HEADERS = ["gcache_operators.h"]
+PUBLIC_HEADERS = ["gcache.h", "gcache_attention.h", "gcache_pages.h"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
@@ -62,18 +66,20 @@ def build(verbose: bool = False) -> str:
     measurement helper libgcache_bench.so)."""
     objdir = os.path.join(ROOT, "_build", "gcache")
     os.makedirs(objdir, exist_ok=True)
-    srcs = SOURCES + BENCH_SOURCES
+    srcs = SOURCES + OPERATOR_SOURCES + BENCH_SOURCES
+    n = len(SOURCES) + len(OPERATOR_SOURCES)
     objs = [os.path.join(objdir, s.replace(".hip", ".o")) for s in srcs]
     with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         list(ex.map(lambda so: _compile(*so, verbose), zip(srcs, objs)))
-    _link(LIB, objs[:len(SOURCES)], verbose)
-    _link(BENCH_LIB, objs[len(SOURCES):], verbose)
+    _link(LIB, objs[:n], verbose)
+    _link(BENCH_LIB, objs[n:], verbose)
     return LIB
 
 
 def source_digest() -> str:
-    """sha256 of every source and header the library is built from (the
-    kernels, their headers and the C ABI header)."""
+    """sha256 of every source and header the cache writes and gathers are built
+    from (the kernels, their headers and the C ABI header); the operators'
+    files, which those kernels do not include, are not in it."""
     import hashlib
     h = hashlib.sha256()
     for path in [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "gcache.h")]:
@@ -87,7 +93,8 @@ def stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "gcache.h")]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + OPERATOR_SOURCES + HEADERS + OPERATOR_HEADERS]
+    deps += [os.path.join(ROOT, "include", f) for f in PUBLIC_HEADERS]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

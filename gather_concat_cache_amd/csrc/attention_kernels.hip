@@ -1,0 +1,717 @@
+// attention_kernels.hip -- attention over the quantized paged caches, read in
+// place: the per-head NVFP4 K/V cache (any byte layout) and the 352-byte
+// nvfp4_ds_mla entry in absorbed form (all heads share the latent; scores
+// over 576 values, values over 512).
+//
+// Mathematics.  For a query row with logits s_j = scale * q . k_j over its
+// visible keys, o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m) for any m.
+// One pass over the keys keeps a running m, l = sum exp2(s - m) and
+// o = sum exp2(s - m) v in binary32, in units of log2; partial triples
+// (m, l, o) of disjoint key sets join by rescaling to the larger m.
+//
+// Rounding.  An NVFP4 value e2m1 * e4m3 has at most 6 significant bits and a
+// magnitude of 2^-10 .. 2688, so it is exact in binary16; the per-tensor
+// scales stay outside (in the logit factor and in the output).  A query row
+// is scaled by the power of two that puts its largest magnitude in
+// [2^10, 2^11) and is then exact in binary16 down to 2^-24 of that maximum.
+// So scores are binary32 sums of exact products; only the weights
+// exp2(s - m) are rounded, to binary16 (11 bits against bf16's 8, at the same
+// matrix rate), shifted up by kShift so that they stay normal numbers down to
+// 2^-20 of the largest.  A block scale that holds the e4m3 NaN code (no write
+// makes one) counts as 0, so pages that no row sees cannot reach an output.
+//
+// Mapping.  One wave works on 16 * R query rows (query token x head of the
+// group) and 32 keys a step, all in registers:
+//   S^T = K Q^T     matrix rows are keys, columns are query rows;
+//   O^T = V^T P^T   matrix rows are value dims, columns are query rows.
+// The 16x16 result layout (lane: column l % 16, rows 4 (l / 16) + i) makes
+// the scores of two 16-key tiles exactly the k-operand of the second product
+// when its 8 k-slots of lane group g are taken as keys 4g..4g+3 and
+// 16+4g..16+4g+3, so weights never leave their lane, and the row statistics
+// are per column, i.e. lane local.  Contraction order over the head dim is
+// free, so lane group g takes the contiguous quarter g of a key's row (one
+// 16-byte load for 128 dims).  For V, lane column c takes the contiguous
+// dims c * DT .. c * DT + DT - 1 of its 8 keys and pairs the codes of two keys
+// in one byte with masks and shifts before the converter, which then returns
+// exactly the operand's register order.
+// The four waves of a workgroup share the query rows, take every fourth
+// 32-key tile of the workgroup's key range and join through LDS.
+#include "gcache_operators.h"
+
+namespace gcache {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
+typedef u32x2 u32x2_a8 __attribute__((aligned(8)));
+typedef uint64_t u64_a1 __attribute__((aligned(1)));
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
+
+constexpr int kTileKeys = 32;
+constexpr int kAttnWaves = 4;
+// log2 units: weights are 2^kShift * exp2(s - m), m trails the true maximum
+// by at most kLag before the accumulators are rescaled, so weights stay
+// below 2^(kShift + kLag) = 2^14.
+constexpr float kShift = 6.0f, kLag = 8.0f;
+constexpr float kNegInf = -__builtin_inff();
+
+// Zero every byte of x that holds the e4m3 NaN code (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t drop_nan_e4m3x4(uint32_t x) {
+    const uint32_t m = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    return x & ~(m | (m - (m >> 7)));
+}
+template <bool HI>
+__device__ __forceinline__ f16x2 e4m3x2_f16(uint32_t w) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI);
+}
+template <int SEL>
+__device__ __forceinline__ f16x2 e2m1x2_f16(uint32_t w) {
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL);
+}
+__device__ __forceinline__ float group_max(float v) {    // over the four lanes of a column
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float group_sum(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// What a workgroup works on, from the device metadata.
+struct RowTile {
+    int b;                       // request
+    int row0, rows;              // first row of the tile in the request, rows in it (<= 16 R)
+    int q0;                      // first packed query token of the request
+    int qlen, ctx, kv_len;       // ctx = position of the request's first query
+    int sink_tiles, win_tile0, total;   // 32-key tiles: [0, sink_tiles) then from win_tile0
+};
+
+__device__ __forceinline__ int query_start(const AttnParams& p, int b) {
+    const int v = p.qs[b];
+    return min(max(v, 0), p.total_q);
+}
+
+// Visible 32-key tiles of rows [row0, row0 + rows) of request b.
+__device__ __forceinline__ void tile_range(const AttnParams& p, RowTile& t) {
+    // key numbers stay clear of int32's end, so key0 + 32 cannot wrap
+    const int64_t table_keys =
+        p.num_blocks > 0 ? min(p.bt_stride * p.div.size, (int64_t)INT32_MAX - 2 * kTileKeys) : 0;
+    const int seq = max(p.seq_lens[t.b], 0);
+    t.ctx = seq - t.qlen;        // may be negative: those rows see nothing
+    t.kv_len = (int)min((int64_t)seq, table_keys);
+    const int p0 = t.ctx + t.row0 / p.group;
+    const int p1 = t.ctx + (t.row0 + t.rows - 1) / p.group;
+    const int hi = p.mask ? t.kv_len : min(p1 + 1, t.kv_len);
+    int lo = 0, sk = 0;
+    if (p.window > 0) {
+        lo = (int)max((int64_t)0, (int64_t)p0 - p.window + 1);
+        sk = min(p.sinks, hi);
+    }
+    t.win_tile0 = lo / kTileKeys;
+    const int end = hi > 0 ? (hi - 1) / kTileKeys + 1 : 0;
+    t.sink_tiles = sk > 0 ? min((sk - 1) / kTileKeys + 1, min(t.win_tile0, end)) : 0;
+    t.total = p1 < 0 ? 0 : t.sink_tiles + max(0, end - t.win_tile0);
+}
+
+// Row tile `tile` of the call: request b owns the tile numbers from
+// qs[b] * group / RT + b on, which leaves it at least ceil(rows / RT).
+__device__ __forceinline__ bool find_tile(const AttnParams& p, int tile, int RT, RowTile& t) {
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)query_start(p, mid) * p.group / RT + mid <= tile) lo = mid;
+        else hi = mid;
+    }
+    t.b = lo;
+    t.q0 = query_start(p, lo);
+    t.qlen = query_start(p, lo + 1) - t.q0;
+    const int64_t row0 = (tile - ((int64_t)t.q0 * p.group / RT + lo)) * RT;
+    const int64_t rows = (int64_t)t.qlen * p.group;
+    if (t.qlen <= 0 || row0 < 0 || row0 >= rows) return false;
+    t.row0 = (int)row0;
+    t.rows = (int)min((int64_t)RT, rows - row0);
+    tile_range(p, t);
+    return true;
+}
+
+// The pages of 32 consecutive keys.  UNI: block_size is a multiple of 16, so
+// each half lies in one page and everything is wave-uniform; otherwise lane
+// i % 32 holds key i's page.  An invalid page reads page 0, masked.
+struct Pages {
+    int64_t base[2];             // UNI: byte offset of the page
+    int off[2];                  // UNI: token of the half's first key in it
+    bool ok[2];
+    int blk, toff;               // !UNI: this lane's key
+    bool kok;
+};
+
+template <bool UNI>
+__device__ __forceinline__ Pages find_pages(const AttnParams& p, const int32_t* __restrict__ bt_row, int key0) {
+    Pages g;
+    if (UNI) {
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            int64_t bi, off;
+            split_block(key0 + 16 * h, p.div, bi, off);
+            const int32_t blk = bt_row[bi < p.bt_stride ? bi : 0];
+            g.ok[h] = bi < p.bt_stride && blk >= 0 && blk < p.num_blocks;
+            g.base[h] = (int64_t)(g.ok[h] ? blk : 0) * p.L.block_stride;
+            g.off[h] = (int)off;
+        }
+    } else {
+        int64_t bi, off;
+        split_block(key0 + (lane_id() & 31), p.div, bi, off);
+        const int32_t blk = bt_row[bi < p.bt_stride ? bi : 0];
+        g.kok = bi < p.bt_stride && blk >= 0 && blk < p.num_blocks;
+        g.blk = g.kok ? blk : 0;
+        g.toff = (int)off;
+    }
+    return g;
+}
+// Key i (0..31) of the tile: page byte offset and token in the page.
+template <bool UNI>
+__device__ __forceinline__ void key_page(const AttnParams& p, const Pages& g, int half, int i16, int64_t& base,
+                                         int& tok, bool& ok) {
+    if (UNI) {
+        base = g.base[half];
+        tok = g.off[half] + i16;
+        ok = g.ok[half];
+    } else {
+        const int i = 16 * half + i16;
+        base = (int64_t)__shfl(g.blk, i) * p.L.block_stride;
+        tok = __shfl(g.toff, i);
+        ok = __shfl((int)g.kok, i) != 0;
+    }
+}
+
+// Raw cache bytes of one 32-key tile as a lane needs them.
+template <int DP, bool MLA>
+struct Raw {
+    static constexpr int KW = DP / 32;                   // data words of the lane's quarter row
+    static constexpr int KSW = DP / 256 > 0 ? DP / 256 : 1;  // words holding its DP / 64 scales
+    static constexpr int VW = DP / 128 > 0 ? DP / 128 : 1;   // data words of its DP / 16 dims
+    uint32_t k[2][KW];
+    uint32_t ks[2][KSW];
+    uint32_t rope[MLA ? 2 : 1][4];
+    uint32_t v[8][VW];
+    uint32_t vs[8];
+    uint32_t live;               // keys in a valid page: bit j, the lane's 8 keys (0..3, 16..19 + 4g)
+};
+
+template <int DP, bool MLA, bool UNI>
+__device__ __forceinline__ void load_tile(const AttnParams& p, const Pages& pg, int kvh, int lane, Raw<DP, MLA>& r) {
+    constexpr int KB = DP / 8;                           // K data bytes per lane and key
+    const int c = lane & 15, g = lane >> 4;
+    const bool full = MLA || p.hs == DP;
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        int64_t base;
+        int tok;
+        bool ok;
+        key_page<UNI>(p, pg, t, c, base, tok, ok);
+        if (MLA) {
+            const uint8_t* e = p.cache + base + (int64_t)tok * p.L.data_token_stride;
+#pragma unroll
+            for (int u = 0; u < KB / 16; u++) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(e + KB * g + 16 * u);
+#pragma unroll
+                for (int i = 0; i < 4; i++) r.k[t][4 * u + i] = w[i];
+            }
+            const u32x4 w = *reinterpret_cast<const u32x4*>(e + kNvRopeOff + 16 * g);
+#pragma unroll
+            for (int i = 0; i < 4; i++) r.rope[t][i] = w[i];
+            const u32x2 s = *reinterpret_cast<const u32x2*>(e + kNvScaleOff + 8 * g);
+            r.ks[t][0] = s.x;
+            r.ks[t][1 % Raw<DP, MLA>::KSW] = s.y;
+        } else {
+            const uint8_t* kd = p.cache + base + p.L.data_offset + (int64_t)tok * p.L.data_token_stride +
+                                (int64_t)kvh * p.L.data_head_stride + KB * g;
+            const uint8_t* sd = p.cache + base + p.L.scale_offset + (int64_t)tok * p.L.scale_token_stride +
+                                (int64_t)kvh * p.L.scale_head_stride + (DP / 64) * g;
+            if (full) {
+                if (KB == 8) {
+                    const u32x2 w = *reinterpret_cast<const u32x2_a8*>(kd);
+                    r.k[t][0] = w.x;
+                    r.k[t][1] = w.y;
+                } else {
+#pragma unroll
+                    for (int u = 0; u < KB / 16; u++) {
+                        const u32x4 w = *reinterpret_cast<const u32x4_a8*>(kd + 16 * u);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) r.k[t][(4 * u + i) % Raw<DP, MLA>::KW] = w[i];
+                    }
+                }
+                if (DP == 64) r.ks[t][0] = *sd;
+                if (DP == 128) r.ks[t][0] = *reinterpret_cast<const u16_a1*>(sd);
+                if (DP == 256) r.ks[t][0] = *reinterpret_cast<const u32_a1*>(sd);
+            } else {                                     // head_size below DP: units of 16 dims
+                r.ks[t][0] = 0;
+#pragma unroll
+                for (int u = 0; u < KB / 8; u++) {
+                    const bool in = (DP / 4) * g + 16 * u < p.hs;
+                    u32x2 w = {0, 0};
+                    if (in) {
+                        w = *reinterpret_cast<const u32x2_a8*>(kd + 8 * u);
+                        r.ks[t][0] |= (uint32_t)sd[u] << (8 * u);
+                    }
+                    r.k[t][2 * u] = w.x;
+                    r.k[t][2 * u + 1] = w.y;
+                }
+            }
+        }
+    }
+    uint32_t live = 0;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        int64_t base;
+        int tok;
+        bool ok;
+        key_page<UNI>(p, pg, j >> 2, 4 * g + (j & 3), base, tok, ok);
+        live |= (uint32_t)ok << j;
+        if (MLA) {
+            const uint8_t* e = p.cache + base + (int64_t)tok * p.L.data_token_stride;
+            const u32x4 w = *reinterpret_cast<const u32x4*>(e + 16 * c);
+#pragma unroll
+            for (int i = 0; i < 4; i++) r.v[j][i % Raw<DP, MLA>::VW] = w[i];
+            r.vs[j] = *reinterpret_cast<const uint16_t*>(e + kNvScaleOff + 2 * c);
+        } else {
+            const uint8_t* vd = p.cache + base + p.L.side_stride + p.L.data_offset + (int64_t)tok * p.L.data_token_stride +
+                                (int64_t)kvh * p.L.data_head_stride + (DP / 32) * c;
+            const uint8_t* sd = p.cache + base + p.L.side_stride + p.L.scale_offset +
+                                (int64_t)tok * p.L.scale_token_stride + (int64_t)kvh * p.L.scale_head_stride +
+                                (DP * c) / 256;
+            if (full || (DP / 16) * c < p.hs) {
+                if (DP == 64) r.v[j][0] = *reinterpret_cast<const uint16_t*>(vd);
+                if (DP == 128) r.v[j][0] = *reinterpret_cast<const uint32_t*>(vd);
+                if (DP == 256) {
+                    const u32x2 w = *reinterpret_cast<const u32x2_a8*>(vd);
+                    r.v[j][0] = w.x;
+                    r.v[j][1 % Raw<DP, MLA>::VW] = w.y;
+                }
+                r.vs[j] = *sd;
+            } else {
+#pragma unroll
+                for (int i = 0; i < Raw<DP, MLA>::VW; i++) r.v[j][i] = 0;
+                r.vs[j] = 0;
+            }
+        }
+    }
+    r.live = live;
+}
+
+template <int DP, bool MLA, int R, bool UNI>
+__global__ __launch_bounds__(kAttnWaves * kWave, R * DP <= 128 ? 4 : R * DP <= 256 ? 2 : 1)
+void k_attention(AttnParams p, int64_t wg0) {
+    constexpr int KS = DP / 32;                          // head-dim steps of the first product
+    constexpr int RS = MLA ? 2 : 0;                      // RoPE steps
+    constexpr int DT = DP / 16;                          // 16-dim tiles of the output
+    constexpr int RT = 16 * R;
+    constexpr int TC = DT < 8 ? DT : 8;                  // dim tiles joined at a time
+    constexpr int kRowFloats = 16 * TC + 4;
+    __shared__ float s_o[kAttnWaves][16][kRowFloats];
+    __shared__ float s_m[kAttnWaves][16], s_l[kAttnWaves][16];
+
+    // The heads of a (row tile, split) unit read neighbouring bytes of the
+    // same tokens: they get workgroup numbers 8 apart, i.e. the same XCD's L2.
+    const int64_t wg = wg0 + blockIdx.x;
+    const int64_t per = 8 * (int64_t)p.hk;
+    const int rem = (int)(wg % per);
+    const int64_t unit = wg / per * 8 + rem % 8;
+    const int kvh = rem / 8;
+    if (unit >= (int64_t)p.tiles * p.splits) return;
+    const int tile = (int)(unit / p.splits), split = (int)(unit % p.splits);
+    RowTile t;
+    if (!find_tile(p, tile, RT, t)) return;
+    const int v0 = split * p.chunk;                      // chunk * splits fits int32 (host)
+    if (split > 0 && v0 >= t.total) return;
+    // a sequence longer than the planned bound: the last split takes the rest
+    const int v1 = split == p.splits - 1 ? t.total : min(t.total, v0 + p.chunk);
+
+    const int lane = lane_id(), w = wave_id();
+    const int c = lane & 15, g = lane >> 4;
+    const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
+
+    // ---- query rows: binary16 operands and per-row logit factors
+    f16x8 q[R][KS + RS];
+    float fac[R];
+    int pos[R], tok[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const int row = t.row0 + 16 * r + c;
+        const bool in = 16 * r + c < t.rows;
+        const int tl = in ? row / p.group : 0;
+        const int head = kvh * p.group + (in ? row - tl * p.group : 0);
+        tok[r] = t.q0 + tl;
+        pos[r] = in ? t.ctx + tl : -1;
+        const uint16_t* src = p.q + (int64_t)tok[r] * p.q_ts + (int64_t)head * p.q_hs;
+        u32x4 raw[KS + RS];
+        float amax = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS + RS; s++) {
+            const int dim = s < KS ? (DP / 4) * g + 8 * s : kNope + 16 * g + 8 * (s - KS);
+            raw[s] = u32x4{0, 0, 0, 0};
+            if (in && (MLA || dim < p.hs)) raw[s] = *reinterpret_cast<const u32x4*>(src + dim);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[s][i])), fabsf(bf16_hi(raw[s][i]))));
+        }
+        amax = group_max(amax);
+        const int e = (int)(__float_as_uint(amax) >> 23);
+        const int up = min(max(264 - e, 1), 253);        // biased exponent of the row's factor
+        const float mul = __uint_as_float((uint32_t)up << 23);
+        fac[r] = p.scale_log2 * (MLA ? 1.0f : *p.gscale[0]) * __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+        for (int s = 0; s < KS + RS; s++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                q[r][s][2 * i] = (_Float16)(bf16_lo(raw[s][i]) * mul);
+                q[r][s][2 * i + 1] = (_Float16)(bf16_hi(raw[s][i]) * mul);
+            }
+    }
+    const int pos_lo = t.ctx + t.row0 / p.group;         // of the tile's rows
+    const int pos_hi = t.ctx + (t.row0 + t.rows - 1) / p.group;
+
+    f32x4 o[R][DT];
+    float m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        m[r] = kNegInf;
+        l[r] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; d++) o[r][d] = f32x4{0, 0, 0, 0};
+    }
+
+    for (int v = v0 + w; v < v1; v += kAttnWaves) {
+        const int kt = v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0;
+        const int key0 = kt * kTileKeys;
+        Raw<DP, MLA> raw;
+        const Pages pg = find_pages<UNI>(p, bt_row, key0);
+        load_tile<DP, MLA, UNI>(p, pg, kvh, lane, raw);
+
+        // ---- S^T = K Q^T
+        f32x4 s[R][2];
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+#pragma unroll
+            for (int r = 0; r < R; r++) s[r][kk] = f32x4{0, 0, 0, 0};
+            f16x2 sc[DP / 64 > 1 ? DP / 64 : 2];
+#pragma unroll
+            for (int i = 0; i < Raw<DP, MLA>::KSW; i++) {
+                const uint32_t x = drop_nan_e4m3x4(raw.ks[kk][i]);
+                const f16x2 a = e4m3x2_f16<false>(x), b = e4m3x2_f16<true>(x);
+                sc[4 * i] = f16x2{a.x, a.x};
+                if (DP >= 128) sc[4 * i + 1] = f16x2{a.y, a.y};
+                if (DP >= 256) {
+                    sc[4 * i + 2] = f16x2{b.x, b.x};
+                    sc[4 * i + 3] = f16x2{b.y, b.y};
+                }
+            }
+#pragma unroll
+            for (int st = 0; st < KS; st++) {
+                const uint32_t wd = raw.k[kk][st];
+                const f16x2 a0 = e2m1x2_f16<0>(wd) * sc[st / 2], a1 = e2m1x2_f16<1>(wd) * sc[st / 2];
+                const f16x2 a2 = e2m1x2_f16<2>(wd) * sc[st / 2], a3 = e2m1x2_f16<3>(wd) * sc[st / 2];
+                const f16x8 a = {a0.x, a0.y, a1.x, a1.y, a2.x, a2.y, a3.x, a3.y};
+#pragma unroll
+                for (int r = 0; r < R; r++) s[r][kk] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][st], s[r][kk], 0, 0, 0);
+            }
+            if (MLA) {
+#pragma unroll
+                for (int st = 0; st < 2; st++) {
+                    const uint32_t x = raw.rope[kk % (MLA ? 2 : 1)][2 * st], y = raw.rope[kk % (MLA ? 2 : 1)][2 * st + 1];
+                    const f16x2 a0 = e4m3x2_f16<false>(x), a1 = e4m3x2_f16<true>(x);
+                    const f16x2 a2 = e4m3x2_f16<false>(y), a3 = e4m3x2_f16<true>(y);
+                    const f16x8 a = {a0.x, a0.y, a1.x, a1.y, a2.x, a2.y, a3.x, a3.y};
+#pragma unroll
+                    for (int r = 0; r < R; r++)
+                        s[r][kk] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][KS + st % (RS ? RS : 1)], s[r][kk], 0, 0, 0);
+                }
+            }
+        }
+
+        // ---- logits, mask
+        bool all = key0 + kTileKeys <= t.kv_len && __all(raw.live == 0xFFu);
+        if (p.mask) all = all && key0 + kTileKeys <= t.ctx;
+        else all = all && key0 + kTileKeys - 1 <= pos_lo &&
+                   (p.window <= 0 || key0 + kTileKeys <= p.sinks || (int64_t)pos_hi - key0 < p.window);
+        f16x8 pw[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) x[j] = s[r][j >> 2][j & 3] * fac[r];
+            if (!all) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
+                    bool see = pos[r] >= 0 && key < t.kv_len && (raw.live >> j & 1);
+                    if (p.mask) {
+                        const int d = key - t.ctx;
+                        if (see && d >= 0)
+                            see = d < p.mask_cols && p.mask[(int64_t)tok[r] * p.mask_ts + d] != 0;
+                    } else {
+                        see = see && key <= pos[r] &&
+                              (p.window <= 0 || key < p.sinks || (int64_t)pos[r] - key < p.window);
+                    }
+                    if (!see) x[j] = kNegInf;
+                }
+            }
+            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            top = group_max(top);
+            if (__any(top > m[r] + kLag)) {              // wave-uniform
+                const float mn = fmaxf(m[r], top);
+                const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
+                m[r] = mn;
+                l[r] *= al;
+#pragma unroll
+                for (int d = 0; d < DT; d++) o[r][d] *= al;
+            }
+            const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float e = __builtin_amdgcn_exp2f(x[j] + sub);
+                sum += e;
+                pw[r][j] = (_Float16)e;
+            }
+            l[r] += sum;
+        }
+
+        // ---- O^T += V^T P^T
+        // scales of key pairs (2i, 2i+1), per 16-dim block of the lane's dims
+        f16x2 vsc[DP == 512 ? 2 : 1][4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (DP == 512) {
+                const uint32_t x = drop_nan_e4m3x4(__builtin_amdgcn_perm(raw.vs[2 * i + 1], raw.vs[2 * i], 0x05010400u));
+                vsc[0][i] = e4m3x2_f16<false>(x);        // bytes: block 0 of both keys, then block 1
+                vsc[DP == 512 ? 1 : 0][i] = e4m3x2_f16<true>(x);
+                if (DP == 512) vsc[0][i] = e4m3x2_f16<false>(x);
+            } else {
+                vsc[0][i] = e4m3x2_f16<false>(drop_nan_e4m3x4(raw.vs[2 * i] | raw.vs[2 * i + 1] << 8));
+            }
+        }
+        constexpr int VW = Raw<DP, MLA>::VW;
+        constexpr int DW = DT < 8 ? DT : 8;              // dims per data word
+#pragma unroll
+        for (int vw = 0; vw < VW; vw++) {
+            uint32_t ev[4], od[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t a = raw.v[2 * i][vw], b = raw.v[2 * i + 1][vw];
+                ev[i] = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+                od[i] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+            }
+            const int blk = DP == 512 ? vw / 2 : 0;
+#pragma unroll
+            for (int d = 0; d < DW; d++) {
+                f16x8 a;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t x = d & 1 ? od[i] : ev[i];
+                    const f16x2 h = (d / 2 == 0 ? e2m1x2_f16<0>(x) : d / 2 == 1 ? e2m1x2_f16<1>(x)
+                                     : d / 2 == 2 ? e2m1x2_f16<2>(x) : e2m1x2_f16<3>(x)) * vsc[blk][i];
+                    a[2 * i] = h.x;
+                    a[2 * i + 1] = h.y;
+                }
+#pragma unroll
+                for (int r = 0; r < R; r++)
+                    o[r][8 * vw + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw[r], o[r][8 * vw + d], 0, 0, 0);
+            }
+        }
+    }
+
+    // ---- join the four waves, 16 rows and 16 * TC dims at a time
+    const bool partial = p.splits > 1 && t.total > p.chunk;
+    const float gv = MLA ? 1.0f : *p.gscale[1];
+    const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;   // the row and dim column this thread writes
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const float lw = group_sum(l[r]);
+        __syncthreads();
+        if (g == 0) {
+            s_m[w][c] = m[r];
+            s_l[w][c] = lw;
+        }
+        const bool in = 16 * r + jr < t.rows;
+        const int row = t.row0 + 16 * r + jr;
+        const int tl = in ? row / p.group : 0;
+        const int head = kvh * p.group + (in ? row - tl * p.group : 0);
+        const int64_t token = t.q0 + tl;
+        float scale = 0.0f, wt[kAttnWaves];
+#pragma unroll
+        for (int ch = 0; ch < DT / TC; ch++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int d = 0; d < TC; d += 4)
+                    *reinterpret_cast<f32x4*>(&s_o[w][c][(4 * g + i) * TC + d]) =
+                        f32x4{o[r][ch * TC + d][i], o[r][ch * TC + d + 1][i], o[r][ch * TC + d + 2][i],
+                              o[r][ch * TC + d + 3][i]};
+            __syncthreads();
+            if (ch == 0) {
+                float mm = kNegInf;
+#pragma unroll
+                for (int k = 0; k < kAttnWaves; k++) mm = fmaxf(mm, s_m[k][jr]);
+                float ll = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kAttnWaves; k++) {
+                    wt[k] = s_m[k][jr] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(s_m[k][jr] - mm);
+                    ll = __builtin_fmaf(wt[k], s_l[k][jr], ll);
+                }
+                if (partial) {
+                    scale = 1.0f;
+                    if (in && jc == 0) {
+                        float* ml = p.ws_ml + 2 * ((int64_t)split * p.total_q * p.hq + token * p.hq + head);
+                        ml[0] = mm;
+                        ml[1] = ll;
+                    }
+                } else {
+                    scale = ll == 0.0f ? 0.0f : gv / ll;
+                    if (in && jc == 0 && p.lse)
+                        p.lse[token * p.lse_ts + head] =
+                            ll == 0.0f ? kNegInf : (mm - kShift + __builtin_log2f(ll)) * 0.6931471805599453f;
+                }
+            }
+            float acc[TC];
+#pragma unroll
+            for (int d = 0; d < TC; d++) acc[d] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kAttnWaves; k++)
+#pragma unroll
+                for (int d = 0; d < TC; d++) acc[d] = __builtin_fmaf(wt[k], s_o[k][jr][jc * TC + d], acc[d]);
+            const int dim = jc * DT + ch * TC;
+            if (in && (MLA || dim < p.hs)) {
+                if (partial) {
+                    float* dst = p.ws_o + ((int64_t)split * p.total_q * p.hq + token * p.hq + head) * p.hs + dim;
+#pragma unroll
+                    for (int d = 0; d < TC; d += 4)
+                        *reinterpret_cast<f32x4*>(dst + d) = f32x4{acc[d], acc[d + 1], acc[d + 2], acc[d + 3]};
+                } else {
+                    uint16_t* dst = p.out + token * p.o_ts + (int64_t)head * p.o_hs + dim;
+                    uint32_t pk[TC / 2];
+#pragma unroll
+                    for (int d = 0; d < TC / 2; d++) pk[d] = pack_bf16x2(acc[2 * d] * scale, acc[2 * d + 1] * scale);
+                    if (TC == 8) *reinterpret_cast<u32x4*>(dst) = u32x4{pk[0], pk[1], pk[2 % (TC / 2)], pk[3 % (TC / 2)]};
+                    else *reinterpret_cast<u32x2*>(dst) = u32x2{pk[0], pk[1]};
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// Join the key splits of a row: one wave per (token, head).
+__global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, int64_t wg0) {
+    const int lane = lane_id();
+    const int RT = p.row_tile;
+    const int64_t id = (wg0 + blockIdx.x) * kWavesPerBlock + wave_id();
+    const int64_t rows = (int64_t)p.total_q * p.hq;
+    if (id >= rows) return;
+    const int token = (int)(id / p.hq), head = (int)(id % p.hq);
+    int lo = 0, hi = p.batch;                            // the last request that starts at or before token
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (query_start(p, mid) <= token) lo = mid;
+        else hi = mid;
+    }
+    RowTile t;
+    t.b = lo;
+    t.q0 = query_start(p, lo);
+    t.qlen = query_start(p, lo + 1) - t.q0;
+    const int tl = token - t.q0;
+    if (tl < 0 || tl >= t.qlen) return;                  // a row of no request
+    const int row = tl * p.group + head % p.group;
+    t.row0 = row / RT * RT;
+    t.rows = (int)min((int64_t)RT, (int64_t)t.qlen * p.group - t.row0);
+    tile_range(p, t);
+    if (t.total <= p.chunk) return;                      // written by its only workgroup
+    const int n = min((t.total - 1) / p.chunk + 1, p.splits);
+    float mm = kNegInf;
+    for (int k = 0; k < n; k++) mm = fmaxf(mm, p.ws_ml[2 * (k * rows + id)]);
+    float ll = 0.0f;
+    for (int k = 0; k < n; k++) {
+        const float mk = p.ws_ml[2 * (k * rows + id)];
+        const float wt = mk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk - mm);
+        ll = __builtin_fmaf(wt, p.ws_ml[2 * (k * rows + id) + 1], ll);
+    }
+    const float scale = ll == 0.0f ? 0.0f : (p.gscale[1] ? *p.gscale[1] : 1.0f) / ll;
+    for (int d = 4 * lane; d < p.hs; d += 4 * kWave) {
+        f32x4 acc = {0, 0, 0, 0};
+        for (int k = 0; k < n; k++) {
+            const float mk = p.ws_ml[2 * (k * rows + id)];
+            const float wt = mk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk - mm);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(p.ws_o + (k * rows + id) * p.hs + d);
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(wt, x[i], acc[i]);
+        }
+        *reinterpret_cast<u32x2*>(p.out + (int64_t)token * p.o_ts + (int64_t)head * p.o_hs + d) =
+            u32x2{pack_bf16x2(acc[0] * scale, acc[1] * scale), pack_bf16x2(acc[2] * scale, acc[3] * scale)};
+    }
+    if (lane == 0 && p.lse)
+        p.lse[(int64_t)token * p.lse_ts + head] =
+            ll == 0.0f ? kNegInf : (mm - kShift + __builtin_log2f(ll)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t dp, int32_t dv,
+                        int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail) {
+    AttnPlan a;
+    const int64_t group = hq / hk, rows = total_q * group;
+    const int64_t mean = (rows + batch - 1) / batch;     // rows of a request and kv head
+    a.row_tiles = mean <= 16 || dp > 256 ? 1 : (mean <= 32 || dp > 128) ? 2 : 4;
+    const int64_t rt = 16 * a.row_tiles;
+    a.tiles = (int32_t)(rows / rt + batch);
+    // 32-key tiles that a row tile can see (a bound; only the split depends on it)
+    int64_t keys = max_seq_len;
+    if (window > 0) {
+        const int64_t seen = (int64_t)window + rt / group + 1 + sinks + 2 * kTileKeys;
+        if (seen < keys) keys = seen;
+    }
+    const int64_t kt = (keys + kTileKeys - 1) / kTileKeys + 1;
+    const int64_t groups = (int64_t)a.tiles * hk;
+    const int64_t want = 1024;
+    int64_t splits = want / groups;
+    if (splits > kt / 8) splits = kt / 8;                // at least two tiles for a wave
+    if (splits > 256) splits = 256;
+    const int64_t per = total_q * hq * (dv + 2);
+    if (per > 0 && splits > ws_floats_avail / per) splits = ws_floats_avail / per;
+    if (splits < 1) splits = 1;
+    int64_t chunk = (kt + splits - 1) / splits;
+    chunk = (chunk + kAttnWaves - 1) / kAttnWaves * kAttnWaves;
+    splits = (kt + chunk - 1) / chunk;
+    a.splits = (int32_t)splits;
+    a.chunk = splits == 1 ? INT32_MAX : (int32_t)chunk;
+    a.ws_floats = splits > 1 ? splits * per : 0;
+    return a;
+}
+
+template <int DP, bool MLA, int R>
+static hipError_t launch_r(const AttnParams& p, hipStream_t s) {
+    const int64_t units = (int64_t)p.tiles * p.splits;
+    const int64_t wgs = (units + 7) / 8 * 8 * p.hk;
+    const bool join = p.splits > 1;
+    const hipError_t e = launch_span(p.div.size % 16 == 0 ? k_attention<DP, MLA, R, true> : k_attention<DP, MLA, R, false>,
+                                     wgs, kAttnWaves * kWave, s, true, !join, p);
+    if (e != hipSuccess || !join) return e;
+    AttnParams q = p;
+    q.row_tile = 16 * R;
+    const int64_t waves = (int64_t)p.total_q * p.hq;
+    return launch_span(k_attention_join, (waves + kWavesPerBlock - 1) / kWavesPerBlock, kBlockThreads, s, false, true, q);
+}
+
+hipError_t launch_attention_kv(const AttnParams& p, int r, hipStream_t s) {
+    if (p.hs <= 64) return r == 1 ? launch_r<64, false, 1>(p, s) : r == 2 ? launch_r<64, false, 2>(p, s) : launch_r<64, false, 4>(p, s);
+    if (p.hs <= 128)
+        return r == 1 ? launch_r<128, false, 1>(p, s) : r == 2 ? launch_r<128, false, 2>(p, s) : launch_r<128, false, 4>(p, s);
+    return r == 1 ? launch_r<256, false, 1>(p, s) : launch_r<256, false, 2>(p, s);
+}
+hipError_t launch_attention_ds_mla(const AttnParams& p, int, hipStream_t s) {
+    return launch_r<512, true, 1>(p, s);
+}
+
+}  // namespace gcache
