@@ -70,13 +70,31 @@ template <int SEL>
 __device__ __forceinline__ f16x2 e2m1x2_f16(uint32_t w) {
     return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, SEL);
 }
-__device__ __forceinline__ float group_max(float v) {    // over the four lanes of a column
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+// Over the four lanes l % 16 + 16 k of a column: the two swap instructions
+// exchange rows of 16 (then halves of 32) between two copies of v, so each
+// lane holds its own value and its partner's without an LDS round trip.
+__device__ __forceinline__ float group_max(float v) {
+    const u32x2 a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a.x), __uint_as_float(a.y));
+    const u32x2 b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b.x), __uint_as_float(b.y));
+}
+// Largest of 8 (16) logits: three at a time.  The operands come out of
+// multiplies, so the plain instruction needs none of the quieting that fmaxf
+// adds to each operand; the last step is fmaxf again.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float max8(const f32x4& a, const f32x4& b) {
+    return fmaxf(max3(max3(a[0], a[1], a[2]), a[3], b[0]), max3(b[1], b[2], b[3]));
 }
 __device__ __forceinline__ float group_sum(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    const u32x2 a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a.x) + __uint_as_float(a.y);
+    const u32x2 b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b.x) + __uint_as_float(b.y);
 }
 
 // What a workgroup works on, from the device metadata.
@@ -136,53 +154,118 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int tile, int RT,
     return true;
 }
 
-// The pages of 32 consecutive keys.  UNI: block_size is a multiple of 16, so
-// each half lies in one page and everything is wave-uniform; otherwise lane
-// i % 32 holds key i's page.  An invalid page reads page 0, masked.
-struct Pages {
-    int64_t base[2];             // UNI: byte offset of the page
-    int off[2];                  // UNI: token of the half's first key in it
-    bool ok[2];
-    int blk, toff;               // !UNI: this lane's key
-    bool kok;
-};
-
-template <bool UNI>
-__device__ __forceinline__ Pages find_pages(const AttnParams& p, const int32_t* __restrict__ bt_row, int key0) {
-    Pages g;
-    if (UNI) {
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            int64_t bi, off;
-            split_block(key0 + 16 * h, p.div, bi, off);
-            const int32_t blk = bt_row[bi < p.bt_stride ? bi : 0];
-            g.ok[h] = bi < p.bt_stride && blk >= 0 && blk < p.num_blocks;
-            g.base[h] = (int64_t)(g.ok[h] ? blk : 0) * p.L.block_stride;
-            g.off[h] = (int)off;
-        }
+// Block and offset of a position; positions are below 2^31.
+__device__ __forceinline__ void split_position(const AttnParams& p, int pos, int& blk, int& off) {
+    const int size = (int)p.div.size;
+    if (p.div.shift >= 0) {
+        blk = pos >> p.div.shift;
+        off = pos & (size - 1);
     } else {
-        int64_t bi, off;
-        split_block(key0 + (lane_id() & 31), p.div, bi, off);
-        const int32_t blk = bt_row[bi < p.bt_stride ? bi : 0];
-        g.kok = bi < p.bt_stride && blk >= 0 && blk < p.num_blocks;
-        g.blk = g.kok ? blk : 0;
-        g.toff = (int)off;
+        blk = (int)((uint32_t)pos / (uint32_t)size);
+        off = pos - blk * size;
     }
+}
+
+// The block-table entries of KEYS consecutive keys, spread over the lanes.
+// UNI: block_size is a multiple of 16, so every 16 keys lie in one page: lane
+// i holds the page of keys 16 i .. 16 i + 15, and their bytes are at wave-uniform
+// addresses to which a lane adds loop-invariant 32-bit offsets.  Otherwise lane
+// i holds key i's page.  The entry is only looked at when it is used (a step
+// later), so its load stays in flight.
+struct KeyPages {
+    int blk;                     // as in the table
+    int off;                     // token in the page, -1: behind the table's row
+};
+template <bool UNI, int KEYS>
+__device__ __forceinline__ KeyPages find_pages(const AttnParams& p, const int32_t* __restrict__ bt_row, int key0, int lane) {
+    int bi;
+    KeyPages g;
+    split_position(p, key0 + (UNI ? 16 * (lane & (KEYS / 16 - 1)) : lane & (KEYS - 1)), bi, g.off);
+    const bool in = bi < p.bt_stride;
+    g.blk = bt_row[in ? bi : 0];
+    if (!in) g.off = -1;
     return g;
 }
-// Key i (0..31) of the tile: page byte offset and token in the page.
+// The page of 16-key group h (UNI) or of key i: block (0 when there is none,
+// which is then masked) and token.
 template <bool UNI>
-__device__ __forceinline__ void key_page(const AttnParams& p, const Pages& g, int half, int i16, int64_t& base,
-                                         int& tok, bool& ok) {
+__device__ __forceinline__ bool take_page(const AttnParams& p, const KeyPages& g, int h, int i, int& blk, int& off) {
+    blk = UNI ? __builtin_amdgcn_readlane(g.blk, h) : __shfl(g.blk, i);
+    off = UNI ? __builtin_amdgcn_readlane(g.off, h) : __shfl(g.off, i);
+    const bool ok = off >= 0 && (uint32_t)blk < (uint64_t)p.num_blocks;
+    blk = ok ? blk : 0;
+    off = ok ? off : 0;
+    return ok;
+}
+// Bit 4 h + i: the page of the lane's key 16 h + 4 (lane / 16) + i exists.
+template <bool UNI, int KEYS>
+__device__ __forceinline__ uint32_t live_keys(const AttnParams& p, const KeyPages& g, int lane) {
+    const bool ok = g.off >= 0 && (uint32_t)g.blk < (uint64_t)p.num_blocks;
+    const uint64_t bits = __ballot(ok);
+    uint32_t live = 0;
+#pragma unroll
+    for (int h = 0; h < KEYS / 16; h++)
+        live |= UNI ? (bits >> h & 1 ? 0xFu << (4 * h) : 0u) : (uint32_t)(bits >> (16 * h + 4 * (lane >> 4)) & 0xF) << (4 * h);
+    return live;
+}
+
+// A lane's offsets from the first key of a half: its K key (lane % 16) and
+// its four V keys (4 (lane / 16) + j), each to the lane's part of the row.
+// UNI takes calls whose 16-key span fits 32 bits (the launcher checks).
+struct LaneOffsets {
+    uint32_t kd, ks, vd[4], vs[4];
+};
+template <int DP, bool MLA>
+__device__ __forceinline__ LaneOffsets lane_offsets(const AttnParams& p, int kvh, int lane) {
+    const int c = lane & 15, g = lane >> 4;
+    LaneOffsets o;
+    const uint32_t tok_d = (uint32_t)p.L.data_token_stride, tok_s = (uint32_t)p.L.scale_token_stride;
+    const uint32_t hd = MLA ? 0 : (uint32_t)(kvh * p.L.data_head_stride), hsc = MLA ? 0 : (uint32_t)(kvh * p.L.scale_head_stride);
+    const uint32_t side = MLA ? 0 : (uint32_t)p.L.side_stride;
+    o.kd = c * tok_d + hd + (DP / 8) * g;
+    o.ks = c * tok_s + hsc + (DP / 64) * g;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        o.vd[j] = (4 * g + j) * tok_d + hd + (DP / 32) * c + side;
+        o.vs[j] = (4 * g + j) * tok_s + hsc + (DP * c) / 256 + side;
+    }
+    return o;
+}
+
+// First bytes of 16-key group h at wave-uniform addresses (UNI).
+struct GroupBytes {
+    const uint8_t *d, *s;
+};
+template <bool UNI, bool MLA>
+__device__ __forceinline__ GroupBytes group_bytes(const AttnParams& p, const KeyPages& g, int h) {
+    GroupBytes b = {nullptr, nullptr};
     if (UNI) {
-        base = g.base[half];
-        tok = g.off[half] + i16;
-        ok = g.ok[half];
+        int blk, off;
+        take_page<true>(p, g, h, 0, blk, off);
+        const uint8_t* page = p.cache + (int64_t)blk * p.L.block_stride;
+        b.d = page + (int64_t)off * p.L.data_token_stride + (MLA ? 0 : p.L.data_offset);
+        if (!MLA) b.s = page + (int64_t)off * p.L.scale_token_stride + p.L.scale_offset;
+    }
+    return b;
+}
+// Where the lane's K key of group h (value == false) or its V key j of it
+// reads: the lane's data bytes and scale bytes.
+template <int DP, bool MLA, bool UNI>
+__device__ __forceinline__ void key_bytes(const AttnParams& p, const KeyPages& g, const GroupBytes& b, const LaneOffsets& o,
+                                          int h, bool value, int j, int kvh, int lane, const uint8_t*& d,
+                                          const uint8_t*& s) {
+    const int c = lane & 15, gr = lane >> 4;
+    if (UNI) {
+        d = b.d + (value ? o.vd[j] : o.kd);
+        s = b.s + (value ? o.vs[j] : o.ks);
     } else {
-        const int i = 16 * half + i16;
-        base = (int64_t)__shfl(g.blk, i) * p.L.block_stride;
-        tok = __shfl(g.toff, i);
-        ok = __shfl((int)g.kok, i) != 0;
+        int blk, off;
+        take_page<false>(p, g, h, 16 * h + (value ? 4 * gr + j : c), blk, off);
+        const uint8_t* page = p.cache + (int64_t)blk * p.L.block_stride + (value ? p.L.side_stride : 0);
+        d = page + p.L.data_offset + (int64_t)off * p.L.data_token_stride + (int64_t)kvh * p.L.data_head_stride +
+            (value ? (DP / 32) * c : (DP / 8) * gr);
+        s = page + p.L.scale_offset + (int64_t)off * p.L.scale_token_stride + (int64_t)kvh * p.L.scale_head_stride +
+            (value ? (DP * c) / 256 : (DP / 64) * gr);
     }
 }
 
@@ -197,25 +280,25 @@ struct Raw {
     uint32_t rope[MLA ? 2 : 1][4];
     uint32_t v[8][VW];
     uint32_t vs[8];
-    uint32_t live;               // keys in a valid page: bit j, the lane's 8 keys (0..3, 16..19 + 4g)
+    uint32_t live;               // live_keys()
 };
 
 template <int DP, bool MLA, bool UNI>
-__device__ __forceinline__ void load_tile(const AttnParams& p, const Pages& pg, int kvh, int lane, Raw<DP, MLA>& r) {
+__device__ __forceinline__ void load_tile(const AttnParams& p, const KeyPages& pg, const LaneOffsets& lo, int kvh, int lane,
+                                          Raw<DP, MLA>& r) {
     constexpr int KB = DP / 8;                           // K data bytes per lane and key
     const int c = lane & 15, g = lane >> 4;
     const bool full = MLA || p.hs == DP;
+    const GroupBytes gb[2] = {group_bytes<UNI, MLA>(p, pg, 0), group_bytes<UNI, MLA>(p, pg, 1)};
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-        int64_t base;
-        int tok;
-        bool ok;
-        key_page<UNI>(p, pg, t, c, base, tok, ok);
+        const uint8_t *kd, *sd;
+        key_bytes<DP, MLA, UNI>(p, pg, gb[t], lo, t, false, 0, kvh, lane, kd, sd);
         if (MLA) {
-            const uint8_t* e = p.cache + base + (int64_t)tok * p.L.data_token_stride;
+            const uint8_t* e = kd - KB * g;
 #pragma unroll
             for (int u = 0; u < KB / 16; u++) {
-                const u32x4 w = *reinterpret_cast<const u32x4*>(e + KB * g + 16 * u);
+                const u32x4 w = *reinterpret_cast<const u32x4*>(kd + 16 * u);
 #pragma unroll
                 for (int i = 0; i < 4; i++) r.k[t][4 * u + i] = w[i];
             }
@@ -226,10 +309,6 @@ __device__ __forceinline__ void load_tile(const AttnParams& p, const Pages& pg, 
             r.ks[t][0] = s.x;
             r.ks[t][1 % Raw<DP, MLA>::KSW] = s.y;
         } else {
-            const uint8_t* kd = p.cache + base + p.L.data_offset + (int64_t)tok * p.L.data_token_stride +
-                                (int64_t)kvh * p.L.data_head_stride + KB * g;
-            const uint8_t* sd = p.cache + base + p.L.scale_offset + (int64_t)tok * p.L.scale_token_stride +
-                                (int64_t)kvh * p.L.scale_head_stride + (DP / 64) * g;
             if (full) {
                 if (KB == 8) {
                     const u32x2 w = *reinterpret_cast<const u32x2_a8*>(kd);
@@ -262,26 +341,17 @@ __device__ __forceinline__ void load_tile(const AttnParams& p, const Pages& pg, 
             }
         }
     }
-    uint32_t live = 0;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-        int64_t base;
-        int tok;
-        bool ok;
-        key_page<UNI>(p, pg, j >> 2, 4 * g + (j & 3), base, tok, ok);
-        live |= (uint32_t)ok << j;
+        const uint8_t *vd, *sd;
+        key_bytes<DP, MLA, UNI>(p, pg, gb[j >> 2], lo, j >> 2, true, j & 3, kvh, lane, vd, sd);
         if (MLA) {
-            const uint8_t* e = p.cache + base + (int64_t)tok * p.L.data_token_stride;
-            const u32x4 w = *reinterpret_cast<const u32x4*>(e + 16 * c);
+            const uint8_t* e = vd - 16 * c;
+            const u32x4 w = *reinterpret_cast<const u32x4*>(vd);
 #pragma unroll
             for (int i = 0; i < 4; i++) r.v[j][i % Raw<DP, MLA>::VW] = w[i];
             r.vs[j] = *reinterpret_cast<const uint16_t*>(e + kNvScaleOff + 2 * c);
         } else {
-            const uint8_t* vd = p.cache + base + p.L.side_stride + p.L.data_offset + (int64_t)tok * p.L.data_token_stride +
-                                (int64_t)kvh * p.L.data_head_stride + (DP / 32) * c;
-            const uint8_t* sd = p.cache + base + p.L.side_stride + p.L.scale_offset +
-                                (int64_t)tok * p.L.scale_token_stride + (int64_t)kvh * p.L.scale_head_stride +
-                                (DP * c) / 256;
             if (full || (DP / 16) * c < p.hs) {
                 if (DP == 64) r.v[j][0] = *reinterpret_cast<const uint16_t*>(vd);
                 if (DP == 128) r.v[j][0] = *reinterpret_cast<const uint32_t*>(vd);
@@ -298,11 +368,107 @@ __device__ __forceinline__ void load_tile(const AttnParams& p, const Pages& pg, 
             }
         }
     }
-    r.live = live;
+    r.live = live_keys<UNI, kTileKeys>(p, pg, lane);
 }
 
-template <int DP, bool MLA, int R, bool UNI>
-__global__ __launch_bounds__(kAttnWaves * kWave, R * DP <= 128 ? 4 : R * DP <= 256 ? 2 : 1)
+// One row of queries a column: lane l takes row t.row0 + row_off + l % 16, its
+// values as the second operand of S^T = K Q^T, and the factor from scores to
+// logits in log2 units.  Rows behind the tile are zeros at position -1.
+template <int DP, bool MLA>
+__device__ __forceinline__ void load_query(const AttnParams& p, const RowTile& t, int kvh, int row_off, int lane,
+                                           f16x8* q, float& fac, int& pos, int& tok) {
+    constexpr int KS = DP / 32, RS = MLA ? 2 : 0;
+    const int c = lane & 15, g = lane >> 4;
+    const bool in = row_off + c < t.rows;
+    const int row = in ? t.row0 + row_off + c : t.row0;
+    const int tl = row / p.group;
+    const int head = kvh * p.group + row - tl * p.group;
+    tok = t.q0 + tl;
+    pos = in ? t.ctx + tl : -1;
+    const uint16_t* src = p.q + (int64_t)tok * p.q_ts + (int64_t)head * p.q_hs;
+    u32x4 raw[KS + RS];
+    float amax = 0.0f;
+#pragma unroll
+    for (int s = 0; s < KS + RS; s++) {
+        const int dim = s < KS ? (DP / 4) * g + 8 * s : kNope + 16 * g + 8 * (s - KS);
+        raw[s] = u32x4{0, 0, 0, 0};
+        if (in && (MLA || dim < p.hs)) raw[s] = *reinterpret_cast<const u32x4*>(src + dim);
+    }
+#pragma unroll
+    for (int s = 0; s < KS + RS; s++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[s][i])), fabsf(bf16_hi(raw[s][i]))));
+    amax = group_max(amax);
+    const int e = (int)(__float_as_uint(amax) >> 23);
+    const int up = min(max(264 - e, 1), 253);            // biased exponent of the row's scaling
+    const float mul = __uint_as_float((uint32_t)up << 23);
+    fac = p.scale_log2 * (MLA ? 1.0f : *p.gscale[0]) * __uint_as_float((uint32_t)(254 - up) << 23);
+#pragma unroll
+    for (int s = 0; s < KS + RS; s++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            q[s][2 * i] = (_Float16)(bf16_lo(raw[s][i]) * mul);
+            q[s][2 * i + 1] = (_Float16)(bf16_hi(raw[s][i]) * mul);
+        }
+}
+
+// A row at position pos sees the keys <= hi that are > lo or sinks, and of a
+// tree's drafted tokens those that its mask names.
+template <bool TREE>
+__device__ __forceinline__ int sight_hi(const AttnParams& p, const RowTile& t, int pos) {
+    return pos < 0 ? -1 : TREE ? t.kv_len - 1 : min(pos, t.kv_len - 1);
+}
+__device__ __forceinline__ int sight_lo(const AttnParams& p, int pos) {
+    return p.window > 0 && pos >= p.window ? pos - p.window : -1;
+}
+// Bit 4 h + i: the lane's key key0 + 16 h + i (h < H, i < 4) is <= last.
+template <int H>
+__device__ __forceinline__ uint32_t keys_upto(int last, int key0) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int h = 0; h < H; h++) bits |= ((1u << min(max(last - key0 + 1 - 16 * h, 0), 4)) - 1) << (4 * h);
+    return bits;
+}
+// Hidden keys' logits of one row become -infinity; key0 counts the lane group,
+// live as from live_keys.
+template <bool TREE, int H>
+__device__ __forceinline__ void hide(const AttnParams& p, const RowTile& t, int pos, int tok, int key0, uint32_t live,
+                                     f32x4* x) {
+    uint32_t see = live & keys_upto<H>(sight_hi<TREE>(p, t, pos), key0);
+    if (TREE) {
+        // drafted keys: their byte in the row's mask, four loads at a time
+        const uint8_t* row = p.mask + (int64_t)tok * p.mask_ts;
+        uint32_t named = 0;
+#pragma unroll 1
+        for (int h = 0; h < H; h++) {
+            const int d0 = key0 + 16 * h - t.ctx;
+            uint32_t byte[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                byte[i] = (see >> (4 * h + i) & 1) && d0 + i >= 0 && d0 + i < p.mask_cols ? row[d0 + i] : 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++) named |= (uint32_t)(byte[i] != 0) << (4 * h + i);
+        }
+        see &= keys_upto<H>(t.ctx - 1, key0) | named;
+    } else if (p.window > 0) {
+        see &= ~keys_upto<H>(sight_lo(p, pos), key0) | keys_upto<H>(p.sinks - 1, key0);
+    }
+#pragma unroll
+    for (int h = 0; h < H; h++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[h][i] = see >> (4 * h + i) & 1 ? x[h][i] : kNegInf;
+}
+// No row of the tile needs a mask for keys [key0, key0 + n) of existing pages.
+template <bool TREE>
+__device__ __forceinline__ bool all_seen(const AttnParams& p, const RowTile& t, int pos_lo, int pos_hi, int key0, int n) {
+    if (key0 + n > t.kv_len) return false;
+    if (TREE) return key0 + n <= t.ctx;
+    return key0 + n - 1 <= pos_lo && (p.window <= 0 || key0 + n <= p.sinks || key0 > pos_hi - p.window);
+}
+
+template <int DP, bool MLA, int R, bool UNI, bool TREE>
+__global__ __launch_bounds__(kAttnWaves * kWave, R * DP <= 128 ? 3 : R * DP <= 256 ? 2 : 1)
 void k_attention(AttnParams p, int64_t wg0) {
     constexpr int KS = DP / 32;                          // head-dim steps of the first product
     constexpr int RS = MLA ? 2 : 0;                      // RoPE steps
@@ -333,43 +499,11 @@ void k_attention(AttnParams p, int64_t wg0) {
     const int c = lane & 15, g = lane >> 4;
     const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
 
-    // ---- query rows: binary16 operands and per-row logit factors
     f16x8 q[R][KS + RS];
     float fac[R];
     int pos[R], tok[R];
 #pragma unroll
-    for (int r = 0; r < R; r++) {
-        const int row = t.row0 + 16 * r + c;
-        const bool in = 16 * r + c < t.rows;
-        const int tl = in ? row / p.group : 0;
-        const int head = kvh * p.group + (in ? row - tl * p.group : 0);
-        tok[r] = t.q0 + tl;
-        pos[r] = in ? t.ctx + tl : -1;
-        const uint16_t* src = p.q + (int64_t)tok[r] * p.q_ts + (int64_t)head * p.q_hs;
-        u32x4 raw[KS + RS];
-        float amax = 0.0f;
-#pragma unroll
-        for (int s = 0; s < KS + RS; s++) {
-            const int dim = s < KS ? (DP / 4) * g + 8 * s : kNope + 16 * g + 8 * (s - KS);
-            raw[s] = u32x4{0, 0, 0, 0};
-            if (in && (MLA || dim < p.hs)) raw[s] = *reinterpret_cast<const u32x4*>(src + dim);
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[s][i])), fabsf(bf16_hi(raw[s][i]))));
-        }
-        amax = group_max(amax);
-        const int e = (int)(__float_as_uint(amax) >> 23);
-        const int up = min(max(264 - e, 1), 253);        // biased exponent of the row's factor
-        const float mul = __uint_as_float((uint32_t)up << 23);
-        fac[r] = p.scale_log2 * (MLA ? 1.0f : *p.gscale[0]) * __uint_as_float((uint32_t)(254 - up) << 23);
-#pragma unroll
-        for (int s = 0; s < KS + RS; s++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                q[r][s][2 * i] = (_Float16)(bf16_lo(raw[s][i]) * mul);
-                q[r][s][2 * i + 1] = (_Float16)(bf16_hi(raw[s][i]) * mul);
-            }
-    }
+    for (int r = 0; r < R; r++) load_query<DP, MLA>(p, t, kvh, 16 * r, lane, q[r], fac[r], pos[r], tok[r]);
     const int pos_lo = t.ctx + t.row0 / p.group;         // of the tile's rows
     const int pos_hi = t.ctx + (t.row0 + t.rows - 1) / p.group;
 
@@ -383,12 +517,28 @@ void k_attention(AttnParams p, int64_t wg0) {
         for (int d = 0; d < DT; d++) o[r][d] = f32x4{0, 0, 0, 0};
     }
 
+    // The next tile's bytes and the page ids of the one behind it are in
+    // flight while a tile is worked on.
+    const auto tile_key = [&](int v) { return (v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0) * kTileKeys; };
+    const LaneOffsets lo = lane_offsets<DP, MLA>(p, kvh, lane);
+    // (The page ids are asked for before the bytes: loads return in order, so
+    // waiting for the ids leaves the bytes in flight.)
+    Raw<DP, MLA> next;
+    KeyPages pg, pg_next;
+    if (v0 + w < v1) {
+        pg = find_pages<UNI, kTileKeys>(p, bt_row, tile_key(v0 + w), lane);
+        pg_next = pg;
+        if (v0 + w + kAttnWaves < v1) pg_next = find_pages<UNI, kTileKeys>(p, bt_row, tile_key(v0 + w + kAttnWaves), lane);
+        load_tile<DP, MLA, UNI>(p, pg, lo, kvh, lane, next);
+    }
     for (int v = v0 + w; v < v1; v += kAttnWaves) {
-        const int kt = v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0;
-        const int key0 = kt * kTileKeys;
-        Raw<DP, MLA> raw;
-        const Pages pg = find_pages<UNI>(p, bt_row, key0);
-        load_tile<DP, MLA, UNI>(p, pg, kvh, lane, raw);
+        const int key0 = tile_key(v);
+        const Raw<DP, MLA> raw = next;
+        if (v + kAttnWaves < v1) {
+            pg = pg_next;
+            if (v + 2 * kAttnWaves < v1) pg_next = find_pages<UNI, kTileKeys>(p, bt_row, tile_key(v + 2 * kAttnWaves), lane);
+            load_tile<DP, MLA, UNI>(p, pg, lo, kvh, lane, next);
+        }
 
         // ---- S^T = K Q^T
         f32x4 s[R][2];
@@ -432,47 +582,43 @@ void k_attention(AttnParams p, int64_t wg0) {
         }
 
         // ---- logits, mask
-        bool all = key0 + kTileKeys <= t.kv_len && __all(raw.live == 0xFFu);
-        if (p.mask) all = all && key0 + kTileKeys <= t.ctx;
-        else all = all && key0 + kTileKeys - 1 <= pos_lo &&
-                   (p.window <= 0 || key0 + kTileKeys <= p.sinks || (int64_t)pos_hi - key0 < p.window);
-        f16x8 pw[R];
+        const bool all = all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kTileKeys) && __all(raw.live == 0xFFu);
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            float x[8];
+            s[r][0] *= fac[r];
+            s[r][1] *= fac[r];
+        }
+        if (!all) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) x[j] = s[r][j >> 2][j & 3] * fac[r];
-            if (!all) {
+            for (int r = 0; r < R; r++) hide<TREE, 2>(p, t, pos[r], tok[r], key0 + 4 * g, raw.live, s[r]);
+        }
+        // ---- running maximum; the accumulators follow it with a lag
+        float top[R];
+        bool late = false;
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const int key = key0 + 16 * (j >> 2) + 4 * g + (j & 3);
-                    bool see = pos[r] >= 0 && key < t.kv_len && (raw.live >> j & 1);
-                    if (p.mask) {
-                        const int d = key - t.ctx;
-                        if (see && d >= 0)
-                            see = d < p.mask_cols && p.mask[(int64_t)tok[r] * p.mask_ts + d] != 0;
-                    } else {
-                        see = see && key <= pos[r] &&
-                              (p.window <= 0 || key < p.sinks || (int64_t)pos[r] - key < p.window);
-                    }
-                    if (!see) x[j] = kNegInf;
-                }
-            }
-            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-            top = group_max(top);
-            if (__any(top > m[r] + kLag)) {              // wave-uniform
-                const float mn = fmaxf(m[r], top);
+        for (int r = 0; r < R; r++) {
+            top[r] = group_max(max8(s[r][0], s[r][1]));
+            late = late || top[r] > m[r] + kLag;
+        }
+        if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first tiles
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const float mn = fmaxf(m[r], top[r]);
                 const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
                 m[r] = mn;
                 l[r] *= al;
 #pragma unroll
                 for (int d = 0; d < DT; d++) o[r][d] *= al;
             }
+        }
+        f16x8 pw[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
             const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
             float sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const float e = __builtin_amdgcn_exp2f(x[j] + sub);
+                const float e = __builtin_amdgcn_exp2f(s[r][j >> 2][j & 3] + sub);
                 sum += e;
                 pw[r][j] = (_Float16)e;
             }
@@ -603,6 +749,316 @@ void k_attention(AttnParams p, int64_t wg0) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many query rows: four waves with 32 rows each and one stream of keys.  A
+// 64-key step's operands are dequantized once, a quarter by each wave, into
+// LDS in the exact register order of the matrix instruction (1 KiB a
+// fragment, lane l at 16 l: conflict-free 16-byte reads and writes), double
+// buffered: step i is multiplied while step i + 1 is converted and step
+// i + 2's bytes are in flight.  Against dequantizing in every wave this takes
+// the converters' share of the vector instructions from 58 to 25 per cent.
+// ---------------------------------------------------------------------------
+constexpr int kStepKeys = 64;
+
+template <int DP>
+struct Share {
+    static constexpr int KS = DP / 32, DT = DP / 16;
+    static constexpr int KF = 4 * KS;                    // K fragments of a step
+    static constexpr int VF = 2 * DT;                    // V fragments of a step
+    static constexpr int HT = DT / 2;                    // V dim tiles a wave converts
+    uint32_t k[DP / 32];                                 // raw: one key of 16
+    uint32_t ks;
+    uint32_t v[8];                                       // raw: HT codes of eight keys
+    uint32_t vs[8];
+};
+
+template <int DP, bool UNI>
+__device__ __forceinline__ void load_share(const AttnParams& p, const KeyPages& pg, const LaneOffsets& lo, int kvh,
+                                           int lane, int w, Share<DP>& r, uint32_t& live) {
+    constexpr int KB = DP / 8;
+    const int c = lane & 15, g = lane >> 4;
+    const bool full = p.hs == DP;
+    // wave w: the K rows of keys 16 w .. 16 w + 15; V of keys 32 (w / 2) .. + 31, half w % 2 of the lane's dims
+    live = live_keys<UNI, kStepKeys>(p, pg, lane);
+    const uint8_t *kd, *sd;
+    const int vh = w & 2;                                // V's first group
+    const GroupBytes gb[2] = {group_bytes<UNI, false>(p, pg, vh), group_bytes<UNI, false>(p, pg, vh + 1)};
+    const GroupBytes kb = {w & 1 ? gb[1].d : gb[0].d, w & 1 ? gb[1].s : gb[0].s};
+    key_bytes<DP, false, UNI>(p, pg, kb, lo, w, false, 0, kvh, lane, kd, sd);
+    if (full) {
+        if (KB == 8) {
+            const u32x2 x = *reinterpret_cast<const u32x2_a8*>(kd);
+            r.k[0] = x.x;
+            r.k[1] = x.y;
+        } else {
+#pragma unroll
+            for (int u = 0; u < KB / 16; u++) {
+                const u32x4 x = *reinterpret_cast<const u32x4_a8*>(kd + 16 * u);
+#pragma unroll
+                for (int i = 0; i < 4; i++) r.k[(4 * u + i) % (DP / 32)] = x[i];
+            }
+        }
+        if (DP == 64) r.ks = *sd;
+        if (DP == 128) r.ks = *reinterpret_cast<const u16_a1*>(sd);
+        if (DP == 256) r.ks = *reinterpret_cast<const u32_a1*>(sd);
+    } else {
+        r.ks = 0;
+#pragma unroll
+        for (int u = 0; u < KB / 8; u++) {
+            u32x2 x = {0, 0};
+            if ((DP / 4) * g + 16 * u < p.hs) {
+                x = *reinterpret_cast<const u32x2_a8*>(kd + 8 * u);
+                r.ks |= (uint32_t)sd[u] << (8 * u);
+            }
+            r.k[2 * u] = x.x;
+            r.k[2 * u + 1] = x.y;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const uint8_t *vd, *sv;
+        key_bytes<DP, false, UNI>(p, pg, gb[j >> 2], lo, vh + (j >> 2), true, j & 3, kvh, lane, vd, sv);
+        r.v[j] = 0;
+        r.vs[j] = 0;
+        if (full || (DP / 16) * c < p.hs) {
+            if (DP == 64) r.v[j] = vd[w & 1];
+            if (DP == 128) r.v[j] = reinterpret_cast<const uint16_t*>(vd)[w & 1];
+            if (DP == 256) r.v[j] = reinterpret_cast<const uint32_t*>(vd)[w & 1];
+            r.vs[j] = *sv;
+        }
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ void convert_share(const Share<DP>& r, int lane, int w, f16x8* lds) {
+    typedef Share<DP> S;
+    const uint32_t x = drop_nan_e4m3x4(r.ks);
+    const f16x2 a = e4m3x2_f16<false>(x), b = e4m3x2_f16<true>(x);
+    const f16x2 sc[4] = {{a.x, a.x}, {a.y, a.y}, {b.x, b.x}, {b.y, b.y}};
+#pragma unroll
+    for (int st = 0; st < S::KS; st++) {
+        const uint32_t wd = r.k[st];
+        const f16x2 a0 = e2m1x2_f16<0>(wd) * sc[st / 2], a1 = e2m1x2_f16<1>(wd) * sc[st / 2];
+        const f16x2 a2 = e2m1x2_f16<2>(wd) * sc[st / 2], a3 = e2m1x2_f16<3>(wd) * sc[st / 2];
+        lds[(w * S::KS + st) * kWave + lane] = f16x8{a0.x, a0.y, a1.x, a1.y, a2.x, a2.y, a3.x, a3.y};
+    }
+    f16x2 vsc[4];
+    uint32_t ev[4], od[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        vsc[i] = e4m3x2_f16<false>(drop_nan_e4m3x4(r.vs[2 * i] | r.vs[2 * i + 1] << 8));
+        const uint32_t lo = r.v[2 * i], hi = r.v[2 * i + 1];
+        ev[i] = (lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u);
+        od[i] = ((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u);
+    }
+    f16x8* dst = lds + (S::KF + (w >> 1) * S::DT + (w & 1) * S::HT) * kWave + lane;
+#pragma unroll
+    for (int d = 0; d < S::HT; d++) {
+        f16x8 f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t y = d & 1 ? od[i] : ev[i];
+            const f16x2 h = (d / 2 == 0 ? e2m1x2_f16<0>(y) : d / 2 == 1 ? e2m1x2_f16<1>(y)
+                             : d / 2 == 2 ? e2m1x2_f16<2>(y) : e2m1x2_f16<3>(y)) * vsc[i];
+            f[2 * i] = h.x;
+            f[2 * i + 1] = h.y;
+        }
+        dst[d * kWave] = f;
+    }
+}
+
+template <int DP, int R, bool UNI, bool TREE>
+__global__ __launch_bounds__(kAttnWaves * kWave, DP <= 128 ? 2 : 1) void k_attention_rows(AttnParams p, int64_t wg0) {
+    typedef Share<DP> S;
+    constexpr int KS = S::KS, DT = S::DT;
+    constexpr int RT = kAttnWaves * 16 * R;
+    __shared__ f16x8 s_frag[2][(S::KF + S::VF) * kWave];
+
+    const int64_t wg = wg0 + blockIdx.x;
+    const int64_t per = 8 * (int64_t)p.hk;
+    const int rem = (int)(wg % per);
+    const int64_t unit = wg / per * 8 + rem % 8;
+    const int kvh = rem / 8;
+    if (unit >= (int64_t)p.tiles * p.splits) return;
+    const int tile = (int)(unit / p.splits), split = (int)(unit % p.splits);
+    RowTile t;
+    if (!find_tile(p, tile, RT, t)) return;
+    const int v0 = split * p.chunk;                      // 32-key tiles, as in k_attention; chunk is even
+    if (split > 0 && v0 >= t.total) return;
+    const int v1 = split == p.splits - 1 ? t.total : min(t.total, v0 + p.chunk);
+
+    const int lane = lane_id(), w = wave_id();
+    const int c = lane & 15, g = lane >> 4;
+    const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
+    f16x8 q[R][KS];
+    float fac[R];
+    int pos[R], tok[R];
+#pragma unroll
+    for (int r = 0; r < R; r++)
+        load_query<DP, false>(p, t, kvh, 16 * (R * w + r), lane, q[r], fac[r], pos[r], tok[r]);
+    const int row_a = min(t.row0 + 16 * R * w, t.row0 + t.rows - 1);
+    const int row_b = min(t.row0 + 16 * R * w + 16 * R - 1, t.row0 + t.rows - 1);
+    const int pos_lo = t.ctx + row_a / p.group, pos_hi = t.ctx + row_b / p.group;   // of the wave's rows
+
+    f32x4 o[R][DT];
+    float m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        m[r] = kNegInf;
+        l[r] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; d++) o[r][d] = f32x4{0, 0, 0, 0};
+    }
+    const LaneOffsets lo = lane_offsets<DP, false>(p, kvh, lane);
+    // Steps of 64 keys: the tiles [v0, v1) are runs of sink tiles and window
+    // tiles; a step covers two consecutive tile numbers of one run.  Keys of a
+    // step behind its run (or behind v1) are hidden by `end`.
+    const auto step_key = [&](int v) { return (v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0) * kTileKeys; };
+    const auto run_end = [&](int v) { return v < t.sink_tiles ? min(t.sink_tiles, v1) : v1; };
+    Share<DP> raw;
+    KeyPages pg, pg_next;
+    uint32_t live, live_n = 0, live_nn = 0;
+    const auto after = [&](int x) { return min(x + 2, run_end(x)); };
+    const auto look_up = [&](int x) { return find_pages<UNI, kStepKeys>(p, bt_row, step_key(x < v1 ? x : v0), lane); };
+    int v = v0, vn = v1, vnn = v1, vp = v1;              // this step, the converted, the loading, the looked-up one
+    if (v < v1) {
+        pg = look_up(v);
+        vn = after(v);
+        pg_next = look_up(vn);
+        load_share<DP, UNI>(p, pg, lo, kvh, lane, w, raw, live);
+        convert_share<DP>(raw, lane, w, s_frag[0]);
+        if (vn < v1) {
+            vnn = after(vn);
+            pg = pg_next;
+            pg_next = look_up(vnn);
+            load_share<DP, UNI>(p, pg, lo, kvh, lane, w, raw, live_n);
+        }
+    }
+    __syncthreads();
+    for (int buf = 0; v < v1; buf ^= 1) {                // workgroup-uniform
+        if (vn < v1) {
+            convert_share<DP>(raw, lane, w, s_frag[buf ^ 1]);
+            if (vnn < v1) {
+                vp = after(vnn);
+                pg = pg_next;
+                pg_next = look_up(vp);
+                load_share<DP, UNI>(p, pg, lo, kvh, lane, w, raw, live_nn);
+            }
+        }
+        const int key0 = step_key(v), tiles = after(v) - v;   // one or two tiles
+        const f16x8* fr = s_frag[buf] + lane;
+        const uint32_t lv = tiles == 2 ? live : live & 0xFFu;
+        const bool all = lv == 0xFFFFu && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kStepKeys);
+
+        f32x4 s[R][4];
+#pragma unroll
+        for (int kt = 0; kt < 4; kt++) {
+#pragma unroll
+            for (int r = 0; r < R; r++) s[r][kt] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int st = 0; st < KS; st++) {
+                const f16x8 a = fr[(kt * KS + st) * kWave];
+#pragma unroll
+                for (int r = 0; r < R; r++) s[r][kt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][st], s[r][kt], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++)
+#pragma unroll
+            for (int kt = 0; kt < 4; kt++) s[r][kt] *= fac[r];
+        if (!__all(all)) {
+#pragma unroll
+            for (int r = 0; r < R; r++) hide<TREE, 4>(p, t, pos[r], tok[r], key0 + 4 * g, lv, s[r]);
+        }
+        float top[R];
+        bool late = false;
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            top[r] = group_max(fmaxf(max8(s[r][0], s[r][1]), max8(s[r][2], s[r][3])));
+            late = late || top[r] > m[r] + kLag;
+        }
+        if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first tiles
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const float mn = fmaxf(m[r], top[r]);
+                const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
+                m[r] = mn;
+                l[r] *= al;
+#pragma unroll
+                for (int d = 0; d < DT; d++) o[r][d] *= al;
+            }
+        }
+        f16x8 pw[R][2];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                const float e = __builtin_amdgcn_exp2f(s[r][j >> 2][j & 3] + sub);
+                sum += e;
+                pw[r][j >> 3][j & 7] = (_Float16)e;
+            }
+            l[r] += sum;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int d = 0; d < DT; d++) {
+                const f16x8 a = fr[(S::KF + h * DT + d) * kWave];
+#pragma unroll
+                for (int r = 0; r < R; r++) o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw[r][h], o[r][d], 0, 0, 0);
+            }
+        v = vn;
+        vn = vnn;
+        vnn = vp;
+        live = live_n;
+        live_n = live_nn;
+        if (v >= v1) break;
+        __syncthreads();
+    }
+
+    // ---- each lane holds 4 runs of DT dims of its row
+    const bool partial = p.splits > 1 && t.total > p.chunk;
+    const float gv = *p.gscale[1];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const float ll = group_sum(l[r]);
+        const int off = 16 * (R * w + r) + c;
+        if (off >= t.rows) continue;
+        const int row = t.row0 + off, tl = row / p.group, head = kvh * p.group + row - tl * p.group;
+        const int64_t id = (int64_t)(t.q0 + tl) * p.hq + head;
+        const float scale = partial ? 1.0f : ll == 0.0f ? 0.0f : gv / ll;
+        if (g == 0) {
+            if (partial) {
+                float* ml = p.ws_ml + 2 * ((int64_t)split * p.total_q * p.hq + id);
+                ml[0] = m[r];
+                ml[1] = ll;
+            } else if (p.lse) {
+                p.lse[(int64_t)(t.q0 + tl) * p.lse_ts + head] =
+                    ll == 0.0f ? kNegInf : (m[r] - kShift + __builtin_log2f(ll)) * 0.6931471805599453f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int dim = (4 * g + i) * DT;
+            if (dim >= p.hs) continue;
+            if (partial) {
+                float* dst = p.ws_o + ((int64_t)split * p.total_q * p.hq + id) * p.hs + dim;
+#pragma unroll
+                for (int d = 0; d < DT; d += 4)
+                    *reinterpret_cast<f32x4*>(dst + d) = f32x4{o[r][d][i], o[r][d + 1][i], o[r][d + 2][i], o[r][d + 3][i]};
+            } else {
+                uint16_t* dst = p.out + (int64_t)(t.q0 + tl) * p.o_ts + (int64_t)head * p.o_hs + dim;
+#pragma unroll
+                for (int d = 0; d < DT; d += 4)
+                    *reinterpret_cast<u32x2*>(dst + d) = u32x2{pack_bf16x2(o[r][d][i] * scale, o[r][d + 1][i] * scale),
+                                                               pack_bf16x2(o[r][d + 2][i] * scale, o[r][d + 3][i] * scale)};
+            }
+        }
+    }
+}
+
 // Join the key splits of a row: one wave per (token, head).
 __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, int64_t wg0) {
     const int lane = lane_id();
@@ -663,7 +1119,7 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     AttnPlan a;
     const int64_t group = hq / hk, rows = total_q * group;
     const int64_t mean = (rows + batch - 1) / batch;     // rows of a request and kv head
-    a.row_tiles = mean <= 16 || dp > 256 ? 1 : (mean <= 32 || dp > 128) ? 2 : 4;
+    a.row_tiles = mean <= 16 || dp > 256 || (dp == 256 && mean <= 32) ? 1 : mean <= 32 ? 2 : 8;
     const int64_t rt = 16 * a.row_tiles;
     a.tiles = (int32_t)(rows / rt + batch);
     // 32-key tiles that a row tile can see (a bound; only the split depends on it)
@@ -690,25 +1146,37 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     return a;
 }
 
-template <int DP, bool MLA, int R>
+template <int DP, bool MLA, int R, bool ROWS = false>
 static hipError_t launch_r(const AttnParams& p, hipStream_t s) {
     const int64_t units = (int64_t)p.tiles * p.splits;
     const int64_t wgs = (units + 7) / 8 * 8 * p.hk;
     const bool join = p.splits > 1;
-    const hipError_t e = launch_span(p.div.size % 16 == 0 ? k_attention<DP, MLA, R, true> : k_attention<DP, MLA, R, false>,
-                                     wgs, kAttnWaves * kWave, s, true, !join, p);
+    // 16 keys of one page within 32-bit offsets of the first
+    const int64_t span = 16 * (p.L.data_token_stride + p.L.scale_token_stride) +
+                         p.hk * (p.L.data_head_stride + p.L.scale_head_stride) + p.L.side_stride + 1024;
+    const bool uni = p.div.size % 16 == 0 && span < INT32_MAX;
+    void (*k)(AttnParams, int64_t);
+    if constexpr (ROWS)
+        k = p.mask ? (uni ? k_attention_rows<DP, R, true, true> : k_attention_rows<DP, R, false, true>)
+                   : (uni ? k_attention_rows<DP, R, true, false> : k_attention_rows<DP, R, false, false>);
+    else
+        k = p.mask ? (uni ? k_attention<DP, MLA, R, true, true> : k_attention<DP, MLA, R, false, true>)
+                   : (uni ? k_attention<DP, MLA, R, true, false> : k_attention<DP, MLA, R, false, false>);
+    const hipError_t e = launch_span(k, wgs, kAttnWaves * kWave, s, true, !join, p);
     if (e != hipSuccess || !join) return e;
     AttnParams q = p;
-    q.row_tile = 16 * R;
+    q.row_tile = 16 * R * (ROWS ? kAttnWaves : 1);
     const int64_t waves = (int64_t)p.total_q * p.hq;
     return launch_span(k_attention_join, (waves + kWavesPerBlock - 1) / kWavesPerBlock, kBlockThreads, s, false, true, q);
 }
 
 hipError_t launch_attention_kv(const AttnParams& p, int r, hipStream_t s) {
-    if (p.hs <= 64) return r == 1 ? launch_r<64, false, 1>(p, s) : r == 2 ? launch_r<64, false, 2>(p, s) : launch_r<64, false, 4>(p, s);
+    if (p.hs <= 64)
+        return r == 1 ? launch_r<64, false, 1>(p, s) : r == 2 ? launch_r<64, false, 2>(p, s) : launch_r<64, false, 2, true>(p, s);
     if (p.hs <= 128)
-        return r == 1 ? launch_r<128, false, 1>(p, s) : r == 2 ? launch_r<128, false, 2>(p, s) : launch_r<128, false, 4>(p, s);
-    return r == 1 ? launch_r<256, false, 1>(p, s) : launch_r<256, false, 2>(p, s);
+        return r == 1 ? launch_r<128, false, 1>(p, s)
+               : r == 2 ? launch_r<128, false, 2>(p, s) : launch_r<128, false, 2, true>(p, s);
+    return r == 1 ? launch_r<256, false, 1>(p, s) : launch_r<256, false, 2, true>(p, s);
 }
 hipError_t launch_attention_ds_mla(const AttnParams& p, int, hipStream_t s) {
     return launch_r<512, true, 1>(p, s);
