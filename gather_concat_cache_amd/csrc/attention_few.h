@@ -1,0 +1,410 @@
+// attention_few.h -- attention of few query rows (one token to a few drafted
+// ones): the four waves of a workgroup share 16 * R query rows, take every
+// fourth 32-key tile of the workgroup's key range straight into registers and
+// join through LDS.  Bound by HBM for long contexts (each wave has a tile's
+// bytes in flight while it works on another) and by the chain of dependent
+// loads for short ones.
+#pragma once
+
+#include "attention_device.h"
+
+namespace gcache {
+
+constexpr int kFewWaves = 4;
+
+// Cache bytes of one 32-key tile as a lane needs them: its quarter of K rows
+// lane % 16 and 16 + lane % 16; its DP / 16 dims of eight V rows.
+template <int DP, bool MLA>
+struct RawK {
+    static constexpr int W = DP / 32;                    // data words of a quarter row
+    static constexpr int SW = DP > 256 ? 2 : 1;          // words holding its DP / 64 scales
+    uint32_t k[2][W], s[2][SW], rope[2][MLA ? 4 : 1];
+};
+template <int DP>
+struct RawV {
+    static constexpr int W = DP > 128 ? DP / 128 : 1;
+    uint32_t v[8][W], s[8];
+};
+
+template <bool UNI>
+struct LaneParts {               // 32-bit offsets of the lane's parts of rows
+    uint32_t kd, ks, rope, vd[4], vs[4];
+};
+template <int DP, bool MLA, bool UNI>
+__device__ __forceinline__ LaneParts<UNI> lane_parts(const AttnParams& p, int kvh, int lane) {
+    const int c = lane & 15, g = lane >> 4;
+    const uint32_t hd = (uint32_t)(kvh * p.L.data_head_stride), hs = (uint32_t)(kvh * p.L.scale_head_stride);
+    const uint32_t side = (uint32_t)p.L.side_stride;
+    LaneParts<UNI> o;
+    o.kd = data_part<UNI>(p, c, hd + (DP / 8) * g);
+    o.ks = scale_part<UNI>(p, c, hs + (DP / 64) * g);
+    o.rope = MLA ? data_part<UNI>(p, c, kNvRopeOff + 16 * g) : 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        o.vd[j] = data_part<UNI>(p, 4 * g + j, side + hd + (DP / 32) * c);
+        o.vs[j] = scale_part<UNI>(p, 4 * g + j, side + hs + (DP * c) / 256);
+    }
+    return o;
+}
+
+template <int DP, bool MLA, bool UNI>
+__device__ __forceinline__ void load_k(const AttnParams& p, const KeyPages& pg, const RowBytes* gb, const LaneParts<UNI>& lo,
+                                       int lane, RawK<DP, MLA>& r) {
+    constexpr int KB = DP / 8;                           // data bytes per lane and key
+    const int c = lane & 15, g = lane >> 4;
+    const bool full = MLA || p.hs == DP;
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+        const RowBytes b = UNI ? gb[t] : row_bytes<UNI>(p, pg, t, c);
+        const uint8_t *kd = b.d + lo.kd, *sd = b.s + lo.ks;
+        if (full) {
+            if (KB == 8) {
+                const u32x2 w = *reinterpret_cast<const u32x2_a8*>(kd);
+                r.k[t][0] = w.x;
+                r.k[t][1] = w.y;
+            } else {
+#pragma unroll
+                for (int u = 0; u < KB / 16; u++) {
+                    const u32x4 w = *reinterpret_cast<const u32x4_a8*>(kd + 16 * u);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) r.k[t][(4 * u + i) % (DP / 32)] = w[i];
+                }
+            }
+            if (DP == 64) r.s[t][0] = *sd;
+            if (DP == 128) r.s[t][0] = *reinterpret_cast<const u16_a1*>(sd);
+            if (DP == 256) r.s[t][0] = *reinterpret_cast<const u32_a1*>(sd);
+            if (DP == 512) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(sd);
+                r.s[t][0] = w.x;
+                r.s[t][RawK<DP, MLA>::SW - 1] = w.y;
+            }
+            if (MLA) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(b.d + lo.rope);
+#pragma unroll
+                for (int i = 0; i < 4; i++) r.rope[t][i % (MLA ? 4 : 1)] = w[i];
+            }
+        } else {                                         // head_size below DP: units of 16 dims
+            r.s[t][0] = 0;
+#pragma unroll
+            for (int u = 0; u < KB / 8; u++) {
+                u32x2 w = {0, 0};
+                if ((DP / 4) * g + 16 * u < p.hs) {
+                    w = *reinterpret_cast<const u32x2_a8*>(kd + 8 * u);
+                    r.s[t][0] |= (uint32_t)sd[u] << (8 * u);
+                }
+                r.k[t][2 * u] = w.x;
+                r.k[t][2 * u + 1] = w.y;
+            }
+        }
+    }
+}
+
+template <int DP, bool MLA, bool UNI>
+__device__ __forceinline__ void load_v(const AttnParams& p, const KeyPages& pg, const RowBytes* gb, const LaneParts<UNI>& lo,
+                                       int lane, RawV<DP>& r) {
+    const int c = lane & 15, g = lane >> 4;
+    const bool in = MLA || p.hs == DP || (DP / 16) * c < p.hs;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const RowBytes b = UNI ? gb[j >> 2] : row_bytes<UNI>(p, pg, j >> 2, 4 * g + (j & 3));
+        const uint8_t *vd = b.d + lo.vd[j & 3], *sd = b.s + lo.vs[j & 3];
+        if (in) {
+            if (DP == 64) r.v[j][0] = *reinterpret_cast<const uint16_t*>(vd);
+            if (DP == 128) r.v[j][0] = *reinterpret_cast<const uint32_t*>(vd);
+            if (DP == 256) {
+                const u32x2 w = *reinterpret_cast<const u32x2_a8*>(vd);
+                r.v[j][0] = w.x;
+                r.v[j][RawV<DP>::W > 1 ? 1 : 0] = w.y;
+            }
+            if (DP == 512) {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(vd);
+#pragma unroll
+                for (int i = 0; i < 4; i++) r.v[j][i % RawV<DP>::W] = w[i];
+            }
+            r.s[j] = DP == 512 ? (uint32_t)*reinterpret_cast<const uint16_t*>(sd) : (uint32_t)*sd;
+        } else {
+#pragma unroll
+            for (int i = 0; i < RawV<DP>::W; i++) r.v[j][i] = 0;
+            r.s[j] = 0;
+        }
+    }
+}
+
+template <int DP, bool MLA, int R, bool UNI, bool TREE>
+__global__ __launch_bounds__(kFewWaves * kWave, R * DP <= 128 ? 3 : R * DP <= 256 ? 2 : 1)
+void k_attention_few(AttnParams p, int64_t wg0) {
+    constexpr int KS = DP / 32;                          // head-dim steps of the first product
+    constexpr int RS = MLA ? 2 : 0;                      // RoPE steps
+    constexpr int DT = DP / 16;                          // 16-dim tiles of the output
+    constexpr int DW = DT < 8 ? DT : 8;                  // dims of a V word
+    constexpr int RT = 16 * R;
+    __shared__ float s_o[kFewWaves][16][16 * DW + 4];
+    __shared__ float s_m[kFewWaves][16], s_l[kFewWaves][16];
+
+    // The heads of a (row tile, split) unit read neighbouring bytes of the
+    // same tokens: they get workgroup numbers 8 apart, i.e. the same XCD's L2.
+    const int64_t wg = wg0 + blockIdx.x;
+    const int64_t per = 8 * (int64_t)p.hk;
+    const int rem = (int)(wg % per);
+    const int64_t unit = wg / per * 8 + rem % 8;
+    const int kvh = rem / 8;
+    if (unit >= (int64_t)p.tiles * p.splits) return;
+    const int tile = (int)(unit / p.splits), split = (int)(unit % p.splits);
+    RowTile t;
+    if (!find_tile(p, tile, RT, t)) return;
+    const int v0 = split * p.chunk;                      // chunk * splits fits int32 (host)
+    if (split > 0 && v0 >= t.total) return;
+    // a sequence longer than the planned bound: the last split takes the rest
+    const int v1 = split == p.splits - 1 ? t.total : min(t.total, v0 + p.chunk);
+
+    const int lane = lane_id(), w = wave_id();
+    const int c = lane & 15, g = lane >> 4;
+    const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
+    const auto tile_key = [&](int v) { return (v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0) * kTileKeys; };
+    const auto look_up = [&](int v) { return find_pages<UNI, kTileKeys>(p, bt_row, tile_key(v < v1 ? v : v0), lane); };
+    const LaneParts<UNI> lo = lane_parts<DP, MLA, UNI>(p, kvh, lane);
+
+    // Loads return in order: page ids are asked for before the bytes of the
+    // tile ahead, so waiting for ids leaves bytes in flight.
+    RawK<DP, MLA> rk;
+    RawV<DP> rv;
+    KeyPages pg, pg_next;
+    int v = v0 + w;
+    if (v < v1) {
+        pg = look_up(v);
+        pg_next = look_up(v + kFewWaves);
+        const RowBytes gb[2] = {group_bytes<UNI>(p, pg, 0), group_bytes<UNI>(p, pg, 1)};
+        load_k<DP, MLA, UNI>(p, pg, gb, lo, lane, rk);
+        load_v<DP, MLA, UNI>(p, pg, gb, lo, lane, rv);
+    }
+
+    f16x8 q[R][KS + RS];
+    float fac[R];
+    int pos[R], tok[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) load_query<DP, MLA>(p, t, kvh, 16 * r, lane, q[r], fac[r], pos[r], tok[r]);
+    const int pos_lo = t.ctx + t.row0 / p.group, pos_hi = t.ctx + (t.row0 + t.rows - 1) / p.group;
+
+    f32x4 o[R][DT];
+    float m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        m[r] = kNegInf;
+        l[r] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; d++) o[r][d] = f32x4{0, 0, 0, 0};
+    }
+
+    for (; v < v1; v += kFewWaves) {
+        const bool more = v + kFewWaves < v1;
+        const int key0 = tile_key(v);
+        const uint32_t live = live_keys<UNI, kTileKeys>(p, pg, lane);
+        // ---- S^T = K Q^T
+        f32x4 s[R][2];
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+#pragma unroll
+            for (int r = 0; r < R; r++) s[r][kk] = f32x4{0, 0, 0, 0};
+            f16x2 sc[RawK<DP, MLA>::SW * 4];
+#pragma unroll
+            for (int i = 0; i < RawK<DP, MLA>::SW; i++) {
+                const uint32_t x = drop_nan_e4m3x4(rk.s[kk][i]);
+                const f16x2 a = e4m3x2_f16<false>(x), b = e4m3x2_f16<true>(x);
+                sc[4 * i] = f16x2{a.x, a.x};
+                sc[4 * i + 1] = f16x2{a.y, a.y};
+                sc[4 * i + 2] = f16x2{b.x, b.x};
+                sc[4 * i + 3] = f16x2{b.y, b.y};
+            }
+#pragma unroll
+            for (int st = 0; st < KS; st++) {
+                const f16x8 a = k_operand(rk.k[kk][st], sc[st / 2]);
+#pragma unroll
+                for (int r = 0; r < R; r++) s[r][kk] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][st], s[r][kk], 0, 0, 0);
+            }
+#pragma unroll
+            for (int st = 0; st < RS; st++) {
+                const f16x8 a = rope_operand(rk.rope[kk][2 * st], rk.rope[kk][2 * st + 1]);
+#pragma unroll
+                for (int r = 0; r < R; r++)
+                    s[r][kk] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][KS + st], s[r][kk], 0, 0, 0);
+            }
+        }
+        // ---- the next tile's K takes the registers just used
+        RowBytes gb[2];
+        if (more) {
+            pg = pg_next;
+            pg_next = look_up(v + 2 * kFewWaves);
+            gb[0] = group_bytes<UNI>(p, pg, 0);
+            gb[1] = group_bytes<UNI>(p, pg, 1);
+            load_k<DP, MLA, UNI>(p, pg, gb, lo, lane, rk);
+        }
+        // ---- logits, mask
+        const bool all = live == 0xFFu && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kTileKeys);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            s[r][0] *= fac[r];
+            s[r][1] *= fac[r];
+        }
+        if (!__all(all)) {
+#pragma unroll
+            for (int r = 0; r < R; r++) hide<TREE, 2>(p, t, pos[r], tok[r], key0 + 4 * g, live, s[r]);
+        }
+        // ---- running maximum; the accumulators follow it with a lag
+        float top[R];
+        bool late = false;
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            top[r] = group_max(max8(s[r][0], s[r][1]));
+            late = late || top[r] > m[r] + kLag;
+        }
+        if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first tiles
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const float mn = fmaxf(m[r], top[r]);
+                const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
+                m[r] = mn;
+                l[r] *= al;
+#pragma unroll
+                for (int d = 0; d < DT; d++) o[r][d] *= al;
+            }
+        }
+        f16x8 pw[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float e = __builtin_amdgcn_exp2f(s[r][j >> 2][j & 3] + sub);
+                sum += e;
+                pw[r][j] = (_Float16)e;
+            }
+            l[r] += sum;
+        }
+        // ---- O^T += V^T P^T
+        f16x2 vsc[DP == 512 ? 2 : 1][4];
+        if (DP == 512) {                                 // the lane's dims span two blocks
+            uint32_t lo8[8], hi8[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                lo8[j] = rv.s[j] & 0xFF;
+                hi8[j] = rv.s[j] >> 8;
+            }
+            v_scales(lo8, vsc[0]);
+            v_scales(hi8, vsc[DP == 512 ? 1 : 0]);
+        } else {
+            v_scales(rv.s, vsc[0]);
+        }
+#pragma unroll
+        for (int vw = 0; vw < RawV<DP>::W; vw++) {
+            uint32_t word[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) word[j] = rv.v[j][vw];
+            const PairedCodes x = pair_codes(word);
+            const f16x2* sc = vsc[DP == 512 ? vw / 2 : 0];
+            const auto mul = [&](int d, const f16x8& a) {
+#pragma unroll
+                for (int r = 0; r < R; r++)
+                    o[r][8 * vw + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw[r], o[r][8 * vw + d], 0, 0, 0);
+            };
+            mul(0, v_operand<0>(x, sc));
+            mul(1, v_operand<1>(x, sc));
+            mul(2, v_operand<2>(x, sc));
+            mul(3, v_operand<3>(x, sc));
+            if (DW > 4) {
+                mul(4 % DT, v_operand<4>(x, sc));
+                mul(5 % DT, v_operand<5>(x, sc));
+                mul(6 % DT, v_operand<6>(x, sc));
+                mul(7 % DT, v_operand<7>(x, sc));
+            }
+        }
+        if (more) load_v<DP, MLA, UNI>(p, pg, gb, lo, lane, rv);
+    }
+
+    // ---- join the four waves, 16 rows and 16 * DW dims at a time
+    const bool partial = p.splits > 1 && t.total > p.chunk;
+    const float gv = MLA ? 1.0f : *p.gscale[1];
+    const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;   // the row and dim column this thread writes
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const float lw = group_sum(l[r]);
+        __syncthreads();
+        if (g == 0) {
+            s_m[w][c] = m[r];
+            s_l[w][c] = lw;
+        }
+        const bool in = 16 * r + jr < t.rows;
+        const int row = in ? t.row0 + 16 * r + jr : t.row0;
+        const int tl = row / p.group;
+        const int head = kvh * p.group + row - tl * p.group;
+        const int64_t token = t.q0 + tl, id = token * p.hq + head;
+        float scale = 0.0f, wt[kFewWaves];
+#pragma unroll
+        for (int ch = 0; ch < DT / DW; ch++) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int d = 0; d < DW; d += 4)
+                    *reinterpret_cast<f32x4*>(&s_o[w][c][(4 * g + i) * DW + d]) =
+                        f32x4{o[r][ch * DW + d][i], o[r][ch * DW + d + 1][i], o[r][ch * DW + d + 2][i],
+                              o[r][ch * DW + d + 3][i]};
+            __syncthreads();
+            if (ch == 0) {
+                float mm = kNegInf;
+#pragma unroll
+                for (int k = 0; k < kFewWaves; k++) mm = fmaxf(mm, s_m[k][jr]);
+                float ll = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kFewWaves; k++) {
+                    wt[k] = s_m[k][jr] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(s_m[k][jr] - mm);
+                    ll = __builtin_fmaf(wt[k], s_l[k][jr], ll);
+                }
+                scale = partial ? 1.0f : ll == 0.0f ? 0.0f : gv / ll;
+                if (in && jc == 0) {
+                    if (partial) {
+                        float* ml = p.ws_ml + 2 * ((int64_t)split * p.total_q * p.hq + id);
+                        ml[0] = mm;
+                        ml[1] = ll;
+                    } else if (p.lse) {
+                        p.lse[token * p.lse_ts + head] = row_lse(mm, ll);
+                    }
+                }
+            }
+            float acc[DW];
+#pragma unroll
+            for (int d = 0; d < DW; d++) acc[d] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kFewWaves; k++)
+#pragma unroll
+                for (int d = 0; d < DW; d++) acc[d] = __builtin_fmaf(wt[k], s_o[k][jr][jc * DW + d], acc[d]);
+            const int dim = jc * DT + ch * DW;
+            if (in && (MLA || dim < p.hs)) {
+                if (partial) {
+                    float* dst = p.ws_o + ((int64_t)split * p.total_q * p.hq + id) * p.hs + dim;
+#pragma unroll
+                    for (int d = 0; d < DW; d += 4)
+                        *reinterpret_cast<f32x4*>(dst + d) = f32x4{acc[d], acc[d + 1], acc[d + 2], acc[d + 3]};
+                } else {
+                    uint16_t* dst = p.out + token * p.o_ts + (int64_t)head * p.o_hs + dim;
+                    uint32_t pk[DW / 2];
+#pragma unroll
+                    for (int d = 0; d < DW / 2; d++) pk[d] = pack_bf16x2(acc[2 * d] * scale, acc[2 * d + 1] * scale);
+                    if (DW == 8) *reinterpret_cast<u32x4*>(dst) = u32x4{pk[0], pk[1], pk[2 % (DW / 2)], pk[3 % (DW / 2)]};
+                    else *reinterpret_cast<u32x2*>(dst) = u32x2{pk[0], pk[1]};
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <int DP, bool MLA, int R>
+hipError_t launch_few(const AttnParams& p, hipStream_t s) {
+    const bool uni = uniform_pages(p);
+    return launch_attention_parts(
+        p.mask ? (uni ? k_attention_few<DP, MLA, R, true, true> : k_attention_few<DP, MLA, R, false, true>)
+               : (uni ? k_attention_few<DP, MLA, R, true, false> : k_attention_few<DP, MLA, R, false, false>),
+        kFewWaves, 16 * R, p, s);
+}
+
+}  // namespace gcache

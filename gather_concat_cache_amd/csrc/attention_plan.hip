@@ -1,0 +1,117 @@
+// attention_plan.hip -- host side of the attention calls: which kernel, how
+// many key splits, the launch sequence; and the kernel that joins the splits.
+#include "attention_device.h"
+
+namespace gcache {
+
+// Join the key splits of a row: one wave per (token, head).
+__global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, int64_t wg0) {
+    const int lane = lane_id();
+    const int RT = p.row_tile;
+    const int64_t id = (wg0 + blockIdx.x) * kWavesPerBlock + wave_id();
+    const int64_t rows = (int64_t)p.total_q * p.hq;
+    if (id >= rows) return;
+    const int token = (int)(id / p.hq), head = (int)(id % p.hq);
+    int lo = 0, hi = p.batch;                            // the last request that starts at or before token
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (query_start(p, mid) <= token) lo = mid;
+        else hi = mid;
+    }
+    RowTile t;
+    t.b = lo;
+    t.q0 = query_start(p, lo);
+    t.qlen = query_start(p, lo + 1) - t.q0;
+    const int tl = token - t.q0;
+    if (tl < 0 || tl >= t.qlen) return;                  // a row of no request
+    const int row = tl * p.group + head % p.group;
+    t.row0 = row / RT * RT;
+    t.rows = (int)min((int64_t)RT, (int64_t)t.qlen * p.group - t.row0);
+    tile_range(p, t);
+    if (t.total <= p.chunk) return;                      // written by its only workgroup
+    const int n = min((t.total - 1) / p.chunk + 1, p.splits);
+    float mm = kNegInf;
+    for (int k = 0; k < n; k++) mm = fmaxf(mm, p.ws_ml[2 * (k * rows + id)]);
+    float ll = 0.0f;
+    for (int k = 0; k < n; k++) {
+        const float mk = p.ws_ml[2 * (k * rows + id)];
+        const float wt = mk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk - mm);
+        ll = __builtin_fmaf(wt, p.ws_ml[2 * (k * rows + id) + 1], ll);
+    }
+    const float scale = ll == 0.0f ? 0.0f : (p.gscale[1] ? *p.gscale[1] : 1.0f) / ll;
+    for (int d = 4 * lane; d < p.hs; d += 4 * kWave) {
+        f32x4 acc = {0, 0, 0, 0};
+        for (int k = 0; k < n; k++) {
+            const float mk = p.ws_ml[2 * (k * rows + id)];
+            const float wt = mk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk - mm);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(p.ws_o + (k * rows + id) * p.hs + d);
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(wt, x[i], acc[i]);
+        }
+        *reinterpret_cast<u32x2*>(p.out + (int64_t)token * p.o_ts + (int64_t)head * p.o_hs + d) =
+            u32x2{pack_bf16x2(acc[0] * scale, acc[1] * scale), pack_bf16x2(acc[2] * scale, acc[3] * scale)};
+    }
+    if (lane == 0 && p.lse)
+        p.lse[(int64_t)token * p.lse_ts + head] =
+            row_lse(mm, ll);
+}
+
+AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t dp, int32_t dv,
+                        int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail) {
+    AttnPlan a;
+    const int64_t group = hq / hk, rows = total_q * group;
+    const int64_t mean = (rows + batch - 1) / batch;     // rows of a request and kv head
+    a.row_tiles = mean <= 16 || (dp >= 256 && mean <= 32) ? 1 : mean <= 32 ? 2 : dp > 256 ? 4 : 8;
+    const int64_t rt = 16 * a.row_tiles;
+    a.tiles = (int32_t)(rows / rt + batch);
+    // 32-key tiles that a row tile can see (a bound; only the split depends on it)
+    int64_t keys = max_seq_len;
+    if (window > 0) {
+        const int64_t seen = (int64_t)window + rt / group + 1 + sinks + 2 * kTileKeys;
+        if (seen < keys) keys = seen;
+    }
+    const int64_t kt = (keys + kTileKeys - 1) / kTileKeys + 1;
+    const int64_t groups = (int64_t)a.tiles * hk;
+    const int64_t want = 1024;
+    int64_t splits = want / groups;
+    if (splits > kt / 8) splits = kt / 8;                // at least two tiles for a wave
+    if (splits > 256) splits = 256;
+    const int64_t per = total_q * hq * (dv + 2);
+    if (per > 0 && splits > ws_floats_avail / per) splits = ws_floats_avail / per;
+    if (splits < 1) splits = 1;
+    int64_t chunk = (kt + splits - 1) / splits;
+    chunk = (chunk + 4 - 1) / 4 * 4;
+    splits = (kt + chunk - 1) / chunk;
+    a.splits = (int32_t)splits;
+    a.chunk = splits == 1 ? INT32_MAX : (int32_t)chunk;
+    a.ws_floats = splits > 1 ? splits * per : 0;
+    return a;
+}
+
+
+// 16 keys of one page, with the head and side offsets, within 32 bits.
+bool uniform_pages(const AttnParams& p) {
+    const int64_t room = INT32_MAX / 4;
+    return p.div.size % 16 == 0 && p.L.data_offset < room && p.L.scale_offset < room &&
+           p.L.data_token_stride < room / p.div.size && p.L.scale_token_stride < room / p.div.size &&
+           p.L.data_head_stride < room / p.hk && p.L.scale_head_stride < room / p.hk && p.L.side_stride < room;
+}
+
+hipError_t launch_attention_parts(void (*kernel)(AttnParams, int64_t), int waves, int row_tile, const AttnParams& in,
+                                  hipStream_t s) {
+    AttnParams p = in;
+    p.blocks = (int32_t)(p.num_blocks < INT32_MAX ? p.num_blocks : INT32_MAX);
+    p.data_offset = (uint32_t)p.L.data_offset;
+    p.scale_offset = (uint32_t)p.L.scale_offset;
+    p.data_token = (uint32_t)p.L.data_token_stride;
+    p.scale_token = (uint32_t)p.L.scale_token_stride;
+    p.row_tile = row_tile;
+    const int64_t units = (int64_t)p.tiles * p.splits;
+    const bool join = p.splits > 1;
+    const hipError_t e = launch_span(kernel, (units + 7) / 8 * 8 * p.hk, waves * kWave, s, true, !join, p);
+    if (e != hipSuccess || !join) return e;
+    const int64_t rows = (int64_t)p.total_q * p.hq;
+    return launch_span(k_attention_join, (rows + kWavesPerBlock - 1) / kWavesPerBlock, kBlockThreads, s, false, true, p);
+}
+
+}  // namespace gcache

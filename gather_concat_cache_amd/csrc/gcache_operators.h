@@ -22,7 +22,11 @@ struct AttnParams {
     int32_t hq, hk, group, hs;   // group = hq / hk
     int64_t num_blocks;
     BlockDiv div;                // block_size
-    KvLayout L;                  // per-head; DS-MLA uses block_stride and data_token_stride
+    KvLayout L;                  // DS-MLA: entries are the data rows, their scales 320 bytes in
+    // set by the launcher: num_blocks clamped to int32, strides that fit 32
+    // bits where pages are walked 16 keys at a time
+    int32_t blocks;
+    uint32_t data_offset, scale_offset, data_token, scale_token;
     const float* gscale[2];      // per-head: k_scale, v_scale; nullptr otherwise
     float scale_log2;            // softmax_scale * log2(e)
     int32_t window;              // > 0: keys behind pos - window are hidden unless sinks
@@ -34,7 +38,7 @@ struct AttnParams {
     int32_t splits, chunk;       // key splits (upper bound), 32-key tiles in each
     float* ws_o;                 // [splits, total_q * hq, dv]
     float* ws_ml;                // [splits, total_q * hq, 2]
-    int32_t row_tile;            // rows of a row tile (set for the join)
+    int32_t row_tile;            // rows of a row tile (set by the launcher, for the join)
 };
 
 // Rows per workgroup (16, 32 or 64) and key splits of a call; filled by

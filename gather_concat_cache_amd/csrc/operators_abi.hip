@@ -311,7 +311,7 @@ int gcache_tree_attention_nvfp4_ds_mla(const gcache_attention_args* a, const voi
     if (!aligned(kv_cache, 16) || block_stride % 16 || entry_stride % 16) return GCACHE_ERR_ALIGN;
     if ((rc = check_device())) return rc;
     p.cache = static_cast<const uint8_t*>(kv_cache);
-    p.L = KvLayout{0, entry_stride, 0, 0, entry_stride, 0, 0, block_stride};
+    p.L = KvLayout{0, entry_stride, 0, kNvScaleOff, entry_stride, 0, 0, block_stride};
     p.mask = tree_mask;
     p.mask_ts = tree_mask_stride;
     p.mask_cols = tree_mask ? mask_columns : 0;
