@@ -30,71 +30,79 @@ template <bool UNI>
 struct LaneParts {               // 32-bit offsets of the lane's parts of rows
     uint32_t kd, ks, rope, vd[4], vs[4];
 };
+// UNI kernels take head sizes of exactly DP; the others take any up to DP:
+// dims behind head_size read the row's first bytes with a zero scale.
 template <int DP, bool MLA, bool UNI>
 __device__ __forceinline__ LaneParts<UNI> lane_parts(const AttnParams& p, int kvh, int lane) {
     const int c = lane & 15, g = lane >> 4;
     const uint32_t hd = (uint32_t)(kvh * p.L.data_head_stride), hs = (uint32_t)(kvh * p.L.scale_head_stride);
     const uint32_t side = (uint32_t)p.L.side_stride;
+    const bool in = UNI || MLA || (DP / 16) * c < p.hs;
     LaneParts<UNI> o;
     o.kd = data_part<UNI>(p, c, hd + (DP / 8) * g);
     o.ks = scale_part<UNI>(p, c, hs + (DP / 64) * g);
     o.rope = MLA ? data_part<UNI>(p, c, kNvRopeOff + 16 * g) : 0;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        o.vd[j] = data_part<UNI>(p, 4 * g + j, side + hd + (DP / 32) * c);
-        o.vs[j] = scale_part<UNI>(p, 4 * g + j, side + hs + (DP * c) / 256);
+        o.vd[j] = data_part<UNI>(p, 4 * g + j, side + hd + (in ? (DP / 32) * c : 0));
+        o.vs[j] = scale_part<UNI>(p, 4 * g + j, side + hs + (in ? (DP * c) / 256 : 0));
     }
     return o;
+}
+
+// One key's quarter row: DP / 32 data words and the DP / 64 scales.
+template <int DP, bool MLA, bool UNI>
+__device__ __forceinline__ void load_k_row(const AttnParams& p, const RowBytes& b, const LaneParts<UNI>& lo, int g,
+                                           uint32_t* k, uint32_t* sc) {
+    constexpr int KB = DP / 8;                           // data bytes
+    const uint8_t *kd = b.d + lo.kd, *sd = b.s + lo.ks;
+    if (UNI || MLA) {
+        if (KB == 8) {
+            const u32x2 w = *reinterpret_cast<const u32x2_a8*>(kd);
+            k[0] = w.x;
+            k[1] = w.y;
+        } else {
+#pragma unroll
+            for (int u = 0; u < KB / 16; u++) {
+                const u32x4 w = *reinterpret_cast<const u32x4_a8*>(kd + 16 * u);
+#pragma unroll
+                for (int i = 0; i < 4; i++) k[(4 * u + i) % (DP / 32)] = w[i];
+            }
+        }
+        if (DP == 64) sc[0] = *sd;
+        if (DP == 128) sc[0] = *reinterpret_cast<const u16_a1*>(sd);
+        if (DP == 256) sc[0] = *reinterpret_cast<const u32_a1*>(sd);
+        if (DP == 512) {
+            const u32x2 w = *reinterpret_cast<const u32x2*>(sd);
+            sc[0] = w.x;
+            sc[DP == 512 ? 1 : 0] = w.y;
+        }
+    } else {                                             // units of 16 dims
+        uint32_t x = 0;
+#pragma unroll
+        for (int u = 0; u < KB / 8; u++) {
+            const bool in = (DP / 4) * g + 16 * u < p.hs;
+            const u32x2 w = *reinterpret_cast<const u32x2_a8*>(in ? kd + 8 * u : b.d + lo.kd - KB * g);
+            const uint32_t y = in ? sd[u] : 0u;
+            x |= y << (8 * u);
+            k[2 * u] = w.x;
+            k[2 * u + 1] = w.y;
+        }
+        sc[0] = x;
+    }
 }
 
 template <int DP, bool MLA, bool UNI>
 __device__ __forceinline__ void load_k(const AttnParams& p, const KeyPages& pg, const RowBytes* gb, const LaneParts<UNI>& lo,
                                        int lane, RawK<DP, MLA>& r) {
-    constexpr int KB = DP / 8;                           // data bytes per lane and key
-    const int c = lane & 15, g = lane >> 4;
-    const bool full = MLA || p.hs == DP;
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-        const RowBytes b = UNI ? gb[t] : row_bytes<UNI>(p, pg, t, c);
-        const uint8_t *kd = b.d + lo.kd, *sd = b.s + lo.ks;
-        if (full) {
-            if (KB == 8) {
-                const u32x2 w = *reinterpret_cast<const u32x2_a8*>(kd);
-                r.k[t][0] = w.x;
-                r.k[t][1] = w.y;
-            } else {
+        const RowBytes b = UNI ? gb[t] : row_bytes<UNI>(p, pg, t, lane & 15);
+        load_k_row<DP, MLA, UNI>(p, b, lo, lane >> 4, r.k[t], r.s[t]);
+        if (MLA) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(b.d + lo.rope);
 #pragma unroll
-                for (int u = 0; u < KB / 16; u++) {
-                    const u32x4 w = *reinterpret_cast<const u32x4_a8*>(kd + 16 * u);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) r.k[t][(4 * u + i) % (DP / 32)] = w[i];
-                }
-            }
-            if (DP == 64) r.s[t][0] = *sd;
-            if (DP == 128) r.s[t][0] = *reinterpret_cast<const u16_a1*>(sd);
-            if (DP == 256) r.s[t][0] = *reinterpret_cast<const u32_a1*>(sd);
-            if (DP == 512) {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(sd);
-                r.s[t][0] = w.x;
-                r.s[t][RawK<DP, MLA>::SW - 1] = w.y;
-            }
-            if (MLA) {
-                const u32x4 w = *reinterpret_cast<const u32x4*>(b.d + lo.rope);
-#pragma unroll
-                for (int i = 0; i < 4; i++) r.rope[t][i % (MLA ? 4 : 1)] = w[i];
-            }
-        } else {                                         // head_size below DP: units of 16 dims
-            r.s[t][0] = 0;
-#pragma unroll
-            for (int u = 0; u < KB / 8; u++) {
-                u32x2 w = {0, 0};
-                if ((DP / 4) * g + 16 * u < p.hs) {
-                    w = *reinterpret_cast<const u32x2_a8*>(kd + 8 * u);
-                    r.s[t][0] |= (uint32_t)sd[u] << (8 * u);
-                }
-                r.k[t][2 * u] = w.x;
-                r.k[t][2 * u + 1] = w.y;
-            }
+            for (int i = 0; i < 4; i++) r.rope[t][i % (MLA ? 4 : 1)] = w[i];
         }
     }
 }
@@ -103,30 +111,25 @@ template <int DP, bool MLA, bool UNI>
 __device__ __forceinline__ void load_v(const AttnParams& p, const KeyPages& pg, const RowBytes* gb, const LaneParts<UNI>& lo,
                                        int lane, RawV<DP>& r) {
     const int c = lane & 15, g = lane >> 4;
-    const bool in = MLA || p.hs == DP || (DP / 16) * c < p.hs;
+    const bool in = UNI || MLA || (DP / 16) * c < p.hs;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         const RowBytes b = UNI ? gb[j >> 2] : row_bytes<UNI>(p, pg, j >> 2, 4 * g + (j & 3));
         const uint8_t *vd = b.d + lo.vd[j & 3], *sd = b.s + lo.vs[j & 3];
-        if (in) {
-            if (DP == 64) r.v[j][0] = *reinterpret_cast<const uint16_t*>(vd);
-            if (DP == 128) r.v[j][0] = *reinterpret_cast<const uint32_t*>(vd);
-            if (DP == 256) {
-                const u32x2 w = *reinterpret_cast<const u32x2_a8*>(vd);
-                r.v[j][0] = w.x;
-                r.v[j][RawV<DP>::W > 1 ? 1 : 0] = w.y;
-            }
-            if (DP == 512) {
-                const u32x4 w = *reinterpret_cast<const u32x4*>(vd);
-#pragma unroll
-                for (int i = 0; i < 4; i++) r.v[j][i % RawV<DP>::W] = w[i];
-            }
-            r.s[j] = DP == 512 ? (uint32_t)*reinterpret_cast<const uint16_t*>(sd) : (uint32_t)*sd;
-        } else {
-#pragma unroll
-            for (int i = 0; i < RawV<DP>::W; i++) r.v[j][i] = 0;
-            r.s[j] = 0;
+        if (DP == 64) r.v[j][0] = *reinterpret_cast<const uint16_t*>(vd);
+        if (DP == 128) r.v[j][0] = *reinterpret_cast<const uint32_t*>(vd);
+        if (DP == 256) {
+            const u32x2 w = *reinterpret_cast<const u32x2_a8*>(vd);
+            r.v[j][0] = w.x;
+            r.v[j][RawV<DP>::W > 1 ? 1 : 0] = w.y;
         }
+        if (DP == 512) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(vd);
+#pragma unroll
+            for (int i = 0; i < 4; i++) r.v[j][i % RawV<DP>::W] = w[i];
+        }
+        const uint32_t x = DP == 512 ? (uint32_t)*reinterpret_cast<const uint16_t*>(sd) : (uint32_t)*sd;
+        r.s[j] = in ? x : 0u;
     }
 }
 
@@ -400,7 +403,7 @@ void k_attention_few(AttnParams p, int64_t wg0) {
 
 template <int DP, bool MLA, int R>
 hipError_t launch_few(const AttnParams& p, hipStream_t s) {
-    const bool uni = uniform_pages(p);
+    const bool uni = uniform_pages(p) && p.hs == DP;
     return launch_attention_parts(
         p.mask ? (uni ? k_attention_few<DP, MLA, R, true, true> : k_attention_few<DP, MLA, R, false, true>)
                : (uni ? k_attention_few<DP, MLA, R, true, false> : k_attention_few<DP, MLA, R, false, false>),

@@ -30,57 +30,23 @@ struct Share {
 template <int DP, bool UNI>
 __device__ __forceinline__ void load_share(const AttnParams& p, const KeyPages& pg, const LaneParts<UNI>& lo, int lane, int w,
                                            Share<DP>& r) {
-    constexpr int KB = DP / 8;
     const int c = lane & 15, g = lane >> 4;
-    const bool full = p.hs == DP;
     // wave w: the K rows of keys 16 w .. 16 w + 15; V of keys 32 (w / 2) .. + 31, half w % 2 of the lane's dims
     const int vh = w & 2;                                // V's first group
     const RowBytes gb[2] = {group_bytes<UNI>(p, pg, vh), group_bytes<UNI>(p, pg, vh + 1)};
     const RowBytes kb = UNI ? RowBytes{w & 1 ? gb[1].d : gb[0].d, w & 1 ? gb[1].s : gb[0].s} : row_bytes<UNI>(p, pg, w, c);
-    const uint8_t *kd = kb.d + lo.kd, *sd = kb.s + lo.ks;
-    if (full) {
-        if (KB == 8) {
-            const u32x2 x = *reinterpret_cast<const u32x2_a8*>(kd);
-            r.k[0] = x.x;
-            r.k[1] = x.y;
-        } else {
-#pragma unroll
-            for (int u = 0; u < KB / 16; u++) {
-                const u32x4 x = *reinterpret_cast<const u32x4_a8*>(kd + 16 * u);
-#pragma unroll
-                for (int i = 0; i < 4; i++) r.k[(4 * u + i) % (DP / 32)] = x[i];
-            }
-        }
-        if (DP == 64) r.ks = *sd;
-        if (DP == 128) r.ks = *reinterpret_cast<const u16_a1*>(sd);
-        if (DP == 256) r.ks = *reinterpret_cast<const u32_a1*>(sd);
-    } else {
-        r.ks = 0;
-#pragma unroll
-        for (int u = 0; u < KB / 8; u++) {
-            u32x2 x = {0, 0};
-            if ((DP / 4) * g + 16 * u < p.hs) {
-                x = *reinterpret_cast<const u32x2_a8*>(kd + 8 * u);
-                r.ks |= (uint32_t)sd[u] << (8 * u);
-            }
-            r.k[2 * u] = x.x;
-            r.k[2 * u + 1] = x.y;
-        }
-    }
-    const bool in = full || (DP / 16) * c < p.hs;
+    load_k_row<DP, false, UNI>(p, kb, lo, g, r.k, &r.ks);
+    const bool in = UNI || (DP / 16) * c < p.hs;
     const uint32_t half = (w & 1) * (DP / 64);           // bytes: half of the lane's DP / 32
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         const RowBytes b = UNI ? gb[j >> 2] : row_bytes<UNI>(p, pg, vh + (j >> 2), 4 * g + (j & 3));
-        const uint8_t *vd = b.d + half + lo.vd[j & 3], *sv = b.s + lo.vs[j & 3];
-        r.v[j] = 0;
-        r.vs[j] = 0;
-        if (in) {
-            if (DP == 64) r.v[j] = *vd;
-            if (DP == 128) r.v[j] = *reinterpret_cast<const uint16_t*>(vd);
-            if (DP == 256) r.v[j] = *reinterpret_cast<const uint32_t*>(vd);
-            r.vs[j] = *sv;
-        }
+        const uint8_t *vd = b.d + (half + lo.vd[j & 3]), *sv = b.s + lo.vs[j & 3];
+        if (DP == 64) r.v[j] = *vd;
+        if (DP == 128) r.v[j] = *reinterpret_cast<const uint16_t*>(vd);
+        if (DP == 256) r.v[j] = *reinterpret_cast<const uint32_t*>(vd);
+        const uint32_t x = *sv;
+        r.vs[j] = in ? x : 0u;
     }
 }
 
@@ -140,6 +106,7 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
 #pragma unroll
     for (int r = 0; r < R; r++)
         load_query<DP, false>(p, t, kvh, 16 * (R * w + r), lane, q[r], fac[r], pos[r], tok[r]);
+    const bool busy = 16 * R * w < t.rows;               // the other waves of a partly filled tile only convert
     const int row_a = min(t.row0 + 16 * R * w, t.row0 + t.rows - 1);
     const int row_b = min(t.row0 + 16 * R * w + 16 * R - 1, t.row0 + t.rows - 1);
     const int pos_lo = t.ctx + row_a / p.group, pos_hi = t.ctx + row_b / p.group;   // of the wave's rows
@@ -190,61 +157,63 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
             }
         }
         const f16x8* fr = s_frag[buf] + lane;
-        const bool all = lv == 0xFFFFu && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kStepKeys);
-        f32x4 s[R][4];
-#pragma unroll
-        for (int r = 0; r < R; r++)
-#pragma unroll
-            for (int kt = 0; kt < 4; kt++) s[r][kt] = f32x4{0, 0, 0, 0};
-        stream_fragments<S::KF, kDepth>(fr, [&](int i, const f16x8& a) {
+        if (busy) {                                      // wave-uniform
+            const bool all = lv == 0xFFFFu && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kStepKeys);
+            f32x4 s[R][4];
 #pragma unroll
             for (int r = 0; r < R; r++)
-                s[r][i / KS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][i % KS], s[r][i / KS], 0, 0, 0);
-        });
 #pragma unroll
-        for (int r = 0; r < R; r++)
+                for (int kt = 0; kt < 4; kt++) s[r][kt] = f32x4{0, 0, 0, 0};
+            stream_fragments<S::KF, kDepth>(fr, [&](int i, const f16x8& a) {
 #pragma unroll
-            for (int kt = 0; kt < 4; kt++) s[r][kt] *= fac[r];
-        if (!__all(all)) {
+                for (int r = 0; r < R; r++)
+                    s[r][i / KS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][i % KS], s[r][i / KS], 0, 0, 0);
+            });
 #pragma unroll
-            for (int r = 0; r < R; r++) hide<TREE, 4>(p, t, pos[r], tok[r], key0 + 4 * g, lv, s[r]);
-        }
-        float top[R];
-        bool late = false;
+            for (int r = 0; r < R; r++)
 #pragma unroll
-        for (int r = 0; r < R; r++) {
-            top[r] = group_max(fmaxf(max8(s[r][0], s[r][1]), max8(s[r][2], s[r][3])));
-            late = late || top[r] > m[r] + kLag;
-        }
-        if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first tiles
+                for (int kt = 0; kt < 4; kt++) s[r][kt] *= fac[r];
+            if (!__all(all)) {
+#pragma unroll
+                for (int r = 0; r < R; r++) hide<TREE, 4>(p, t, pos[r], tok[r], key0 + 4 * g, lv, s[r]);
+            }
+            float top[R];
+            bool late = false;
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                const float mn = fmaxf(m[r], top[r]);
-                const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
-                m[r] = mn;
-                l[r] *= al;
-#pragma unroll
-                for (int d = 0; d < DT; d++) o[r][d] *= al;
+                top[r] = group_max(fmaxf(max8(s[r][0], s[r][1]), max8(s[r][2], s[r][3])));
+                late = late || top[r] > m[r] + kLag;
             }
-        }
-        f16x8 pw[R][2];
+            if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first tiles
 #pragma unroll
-        for (int r = 0; r < R; r++) {
-            const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
-            float sum = 0.0f;
+                for (int r = 0; r < R; r++) {
+                    const float mn = fmaxf(m[r], top[r]);
+                    const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
+                    m[r] = mn;
+                    l[r] *= al;
 #pragma unroll
-            for (int j = 0; j < 16; j++) {
-                const float e = __builtin_amdgcn_exp2f(s[r][j >> 2][j & 3] + sub);
-                sum += e;
-                pw[r][j >> 3][j & 7] = (_Float16)e;
+                    for (int d = 0; d < DT; d++) o[r][d] *= al;
+                }
             }
-            l[r] += sum;
-        }
-        stream_fragments<S::VF, kDepth>(fr + S::KF * kWave, [&](int i, const f16x8& a) {
+            f16x8 pw[R][2];
 #pragma unroll
-            for (int r = 0; r < R; r++)
-                o[r][i % DT] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw[r][i / DT], o[r][i % DT], 0, 0, 0);
-        });
+            for (int r = 0; r < R; r++) {
+                const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    const float e = __builtin_amdgcn_exp2f(s[r][j >> 2][j & 3] + sub);
+                    sum += e;
+                    pw[r][j >> 3][j & 7] = (_Float16)e;
+                }
+                l[r] += sum;
+            }
+            stream_fragments<S::VF, kDepth>(fr + S::KF * kWave, [&](int i, const f16x8& a) {
+#pragma unroll
+                for (int r = 0; r < R; r++)
+                    o[r][i % DT] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw[r][i / DT], o[r][i % DT], 0, 0, 0);
+            });
+        }
         v = vn;
         vn = vnn;
         vnn = vp;
@@ -296,7 +265,7 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
 
 template <int DP>
 static hipError_t launch_rows(const AttnParams& p, hipStream_t s) {
-    const bool uni = uniform_pages(p);
+    const bool uni = uniform_pages(p) && p.hs == DP;
     return launch_attention_parts(
         p.mask ? (uni ? k_attention_rows<DP, kRowsR, true, true> : k_attention_rows<DP, kRowsR, false, true>)
                : (uni ? k_attention_rows<DP, kRowsR, true, false> : k_attention_rows<DP, kRowsR, false, false>),

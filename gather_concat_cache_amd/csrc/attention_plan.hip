@@ -72,7 +72,9 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     }
     const int64_t kt = (keys + kTileKeys - 1) / kTileKeys + 1;
     const int64_t groups = (int64_t)a.tiles * hk;
-    const int64_t want = 1024;
+    // workgroups: some rounds of what the device holds at once (three, two and
+    // one a CU), against the ragged ends of lengths and rounds
+    const int64_t want = a.row_tiles <= 2 ? 2048 : dp > 256 ? 1024 : 4096;
     int64_t splits = want / groups;
     if (splits > kt / 8) splits = kt / 8;                // at least two tiles for a wave
     if (splits > 256) splits = 256;
