@@ -66,7 +66,8 @@ struct QkNormRopeParams {
     int32_t cs_bf16;
     float eps;
     int64_t num_tokens;
-    int32_t lph_shift, waves_per_token;   // set by the launcher
+    int32_t waves_per_token;     // set by the launcher, as is
+    float inv_hs;
 };
 hipError_t launch_qk_norm_rope(const QkNormRopeParams& p, hipStream_t s);
 
@@ -100,8 +101,7 @@ struct GrantParams {
     int32_t* free_ids;           // [num_blocks] the lowest free pages
 };
 hipError_t launch_fork_plan(const GrantParams& g, hipStream_t s);
-hipError_t launch_fork_rows(const GrantParams& g, hipStream_t s, bool last);
-hipError_t launch_fork_copy(const GrantParams& g, const CacheList& c, hipStream_t s, bool last);
+hipError_t launch_fork_apply(const GrantParams& g, const CacheList& c, bool rows, hipStream_t s, bool last);
 hipError_t launch_extend(const GrantParams& g, hipStream_t s);
 hipError_t launch_free(const PageTable& t, const int32_t* rows, int32_t n, hipStream_t s);
 

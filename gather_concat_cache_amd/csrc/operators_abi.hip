@@ -358,9 +358,8 @@ int gcache_fork_requests(const gcache_page_state* state, const gcache_page_cache
     if ((rc = check_device())) return rc;
     hipError_t e = launch_fork_plan(g, stream);
     const int n = caches->page_bytes > 0 ? caches->num_caches : 0;
-    if (e == hipSuccess) e = launch_fork_rows(g, stream, n == 0);
-    for (int at = 0; at < n && e == hipSuccess; at += kMaxCaches)
-        e = launch_fork_copy(g, cache_list(caches, t.num_blocks, at), stream, at + kMaxCaches >= n);
+    for (int at = 0; (at < n || at == 0) && e == hipSuccess; at += kMaxCaches)
+        e = launch_fork_apply(g, cache_list(caches, n ? t.num_blocks : 0, at), at == 0, stream, at + kMaxCaches >= n);
     return launched(e);
 }
 

@@ -48,11 +48,85 @@ __device__ __forceinline__ int64_t wg_exclusive(int v, int64_t* s, int64_t* tota
     return before + x - v;
 }
 
-// One workgroup: which requests are valid (the lowest-numbered one of a row
-// wins), how many pages each needs, the lowest free pages for all of them.
-// FORK: a = parent rows, b = child rows; else a = rows, b = new lengths.
-// Grants are decided in request order: request i is granted when the pages
-// of requests 0..i all fit the free ones.
+// Tokens the row of request f would get, -1: refused.
+template <bool FORK>
+__device__ __forceinline__ int grant_len(const GrantParams& p, int row, int arg) {
+    const int rows = p.t.num_rows;
+    if (row < 0 || row >= rows) return -1;
+    const int have = p.t.lens[row];
+    int len = arg;
+    if (FORK) {                                          // arg: the parent row
+        if (arg < 0 || arg >= rows || arg == row || have != 0) return -1;
+        len = p.t.lens[arg];
+    } else if (have < 0 || len < have) {
+        return -1;
+    }
+    return len >= 0 && pages_of(len, p.t.block_size) <= p.t.stride ? len : -1;
+}
+
+// The lowest `want` free pages (all of them when there are fewer) into
+// free_ids; returns how many there are.
+__device__ __forceinline__ int64_t list_free(const GrantParams& p, int64_t want, int64_t* s_scan) {
+    constexpr int kIds = 4;
+    int64_t found = 0;
+    for (int64_t b0 = 0; b0 < p.t.num_blocks && found < want; b0 += kIds * kPlanThreads) {
+        const int64_t id0 = b0 + kIds * threadIdx.x;
+        bool fr[kIds];
+        int cnt = 0;
+#pragma unroll
+        for (int i = 0; i < kIds; i++) {
+            fr[i] = id0 + i < p.t.num_blocks && p.t.refs[id0 + i] == 0;
+            cnt += fr[i];
+        }
+        int64_t sum;
+        int64_t at = found + wg_exclusive(cnt, s_scan, &sum);
+#pragma unroll
+        for (int i = 0; i < kIds; i++)
+            if (fr[i]) p.free_ids[at++] = (int)(id0 + i);
+        found += sum;
+    }
+    return found;
+}
+
+// One workgroup, at most a request a thread: which requests are valid (the
+// lowest-numbered one of a row wins), how many pages each needs, the lowest
+// free pages for all of them.  FORK: a = parent rows, b = child rows; else a =
+// rows, b = new lengths.  Grants are decided in request order: request i is
+// granted when the pages of requests 0..i all fit the free ones.  Everything
+// stays in registers and LDS: three dependent memory round trips.
+template <bool FORK>
+__global__ __launch_bounds__(kPlanThreads) void k_grant_small(GrantParams p, int64_t) {
+    __shared__ int64_t s_scan[kPlanWaves];
+    __shared__ __align__(16) int s_row[kPlanThreads];
+    const int f = threadIdx.x, bs = p.t.block_size;
+    const int a = f < p.n ? p.a[f] : -1, b = f < p.n ? p.b[f] : -1;
+    const int row = FORK ? b : a;
+    int len = f < p.n ? grant_len<FORK>(p, row, FORK ? a : b) : -1;
+    s_row[f] = len >= 0 ? row : -1;
+    __syncthreads();
+    bool again = false;                                  // an earlier valid request names the row
+#pragma unroll 4
+    for (int e = 0; e < (p.n + 3) / 4; e++) {
+        const int4 x = reinterpret_cast<const int4*>(s_row)[e];
+        again |= (x.x == row && 4 * e < f) || (x.y == row && 4 * e + 1 < f) || (x.z == row && 4 * e + 2 < f) ||
+                 (x.w == row && 4 * e + 3 < f);
+    }
+    if (again) len = -1;
+    int need = 0;
+    if (len >= 0) need = FORK ? len % bs != 0 : min(pages_of(len, bs) - pages_of(p.t.lens[row], bs), p.t.num_blocks);
+    int64_t all;
+    const int64_t upto = wg_exclusive(need, s_scan, &all) + need;
+    const int64_t found = list_free(p, all, s_scan);
+    if (f < p.n) {
+        const bool ok = len >= 0 && upto <= found;
+        p.status[f] = ok;
+        p.len[f] = ok ? len : -1;
+        // needs past int32 cannot be met: num_blocks + 1 pages say as much
+        p.upto[f] = (int)min(upto, (int64_t)p.t.num_blocks + 1);
+    }
+}
+
+// The same for any number of requests, with the claims of rows in memory.
 template <bool FORK>
 __global__ __launch_bounds__(kPlanThreads) void k_grant_plan(GrantParams p, int64_t) {
     __shared__ int64_t s_scan[kPlanWaves];
@@ -63,20 +137,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_grant_plan(GrantParams p, int6
         if (r >= 0 && r < rows) atomicExch(&p.claim[r], INT32_MAX);
     }
     plan_sync();
-    const auto valid_len = [&](int f) -> int {           // tokens the row would get, -1: refused
-        const int r = row_of(f);
-        if (r < 0 || r >= rows) return -1;
-        int len, have = p.t.lens[r];
-        if (FORK) {
-            const int par = p.a[f];
-            if (par < 0 || par >= rows || par == r || have != 0) return -1;
-            len = p.t.lens[par];
-        } else {
-            len = p.b[f];
-            if (have < 0 || len < have) return -1;
-        }
-        return len >= 0 && pages_of(len, bs) <= p.t.stride ? len : -1;
-    };
+    const auto valid_len = [&](int f) { return grant_len<FORK>(p, row_of(f), FORK ? p.a[f] : p.b[f]); };
     for (int f = tid; f < p.n; f += kPlanThreads)
         if (valid_len(f) >= 0) atomicMin(&p.claim[row_of(f)], f);
     plan_sync();
@@ -99,25 +160,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_grant_plan(GrantParams p, int6
         if (f < p.n) p.upto[f] = (int)min(upto, (int64_t)p.t.num_blocks + 1);
         need_all += sum;
     }
-    // the lowest need_all free pages (all of them when there are fewer)
-    int64_t found = 0;
-    constexpr int kIds = 4;
-    for (int64_t b0 = 0; b0 < p.t.num_blocks && found < need_all; b0 += kIds * kPlanThreads) {
-        const int64_t id0 = b0 + kIds * tid;
-        bool fr[kIds];
-        int cnt = 0;
-#pragma unroll
-        for (int i = 0; i < kIds; i++) {
-            fr[i] = id0 + i < p.t.num_blocks && p.t.refs[id0 + i] == 0;
-            cnt += fr[i];
-        }
-        int64_t sum;
-        int64_t at = found + wg_exclusive(cnt, s_scan, &sum);
-#pragma unroll
-        for (int i = 0; i < kIds; i++)
-            if (fr[i]) p.free_ids[at++] = (int)(id0 + i);
-        found += sum;
-    }
+    const int64_t found = list_free(p, need_all, s_scan);
     for (int f = tid; f < p.n; f += kPlanThreads) {
         const bool ok = p.len[f] >= 0 && p.upto[f] <= found;
         p.status[f] = ok;
@@ -128,10 +171,8 @@ __global__ __launch_bounds__(kPlanThreads) void k_grant_plan(GrantParams p, int6
 // Request f's first page in free_ids (its need is upto[f] - upto[f - 1]).
 __device__ __forceinline__ int first_page(const GrantParams& p, int f) { return f > 0 ? p.upto[f - 1] : 0; }
 
-// Rows of a fork: one workgroup a request.
-__global__ __launch_bounds__(kBlockThreads) void k_fork_rows(GrantParams p, int64_t wg0) {
-    const int64_t f = wg0 + blockIdx.x;
-    if (f >= p.n) return;
+// The row of fork f, by one workgroup.
+__device__ __forceinline__ void fork_row(const GrantParams& p, int f) {
     const int len = p.len[f];
     if (len < 0) return;
     const int full = len / p.t.block_size;
@@ -144,7 +185,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_fork_rows(GrantParams p, int6
     }
     if (threadIdx.x == 0) {
         if (len % p.t.block_size) {
-            const int id = p.free_ids[first_page(p, (int)f)];
+            const int id = p.free_ids[first_page(p, f)];
             dst[full] = id;
             atomicAdd(&p.t.refs[id], 1);
         }
@@ -206,13 +247,11 @@ __device__ __forceinline__ void copy_page(const uint8_t* __restrict__ src, uint8
     for (int64_t i = n * (int64_t)sizeof(V) + threadIdx.x; i < bytes; i += kBlockThreads) dst[i] = src[i];
 }
 
-struct PairList {                // explicit pairs, a fork's partial pages, or a compaction's moves
+struct PairList {                // explicit pairs, or a compaction's moves
     const int32_t* src;
     const int32_t* dst;
     const int32_t* count;        // device count, or nullptr: n
     int64_t n;
-    GrantParams fork;
-    bool is_fork;
 };
 struct CopyParams {
     CacheList c;
@@ -226,31 +265,93 @@ __global__ __launch_bounds__(kBlockThreads) void k_copy_pages(CopyParams p, int6
     for (int64_t it = wg0 + blockIdx.x; it < items; it += step) {
         const int64_t k = it % n;
         const int cache = (int)(it / n);
-        int64_t a, b;
-        if (p.l.is_fork) {
-            const GrantParams& g = p.l.fork;
-            const int len = g.len[k];
-            if (len < 0 || len % g.t.block_size == 0) continue;
-            a = g.t.table[(int64_t)g.a[k] * g.t.stride + len / g.t.block_size];
-            b = g.free_ids[first_page(g, (int)k)];
-        } else {
-            a = p.l.src[k];
-            b = p.l.dst[k];
-        }
+        const int64_t a = p.l.src[k], b = p.l.dst[k];
         if (a < 0 || a >= p.c.num_blocks || b < 0 || b >= p.c.num_blocks || a == b) continue;
         uint8_t* base = p.c.base[cache];
         copy_page<V>(base + a * p.c.block_stride, base + b * p.c.block_stride, p.c.page_bytes);
     }
 }
 
+// The rows of the forks, then their partial pages.  Up to kForkBlock
+// consecutive forks of one cache go to a workgroup, which reads a page once for
+// the forks of the same parent that follow each other: samples of one prompt
+// then cost one read and their writes (one 8-fold fork of 64 prompts over 32
+// caches: 83 us against 157 us with a read for every copy).
+constexpr int kForkBlock = 8;
+struct ForkCopyParams {
+    CacheList c;
+    GrantParams g;
+    int32_t block;               // forks of a workgroup, <= kForkBlock
+    bool rows;                   // this launch also does the rows
+};
+
+template <typename V>
+__global__ __launch_bounds__(kBlockThreads) void k_fork_apply(ForkCopyParams p, int64_t wg0) {
+    constexpr int U = 6;                                 // loads in flight a thread
+    __shared__ int s_src[kForkBlock], s_dst[kForkBlock];
+    const GrantParams& g = p.g;
+    if (p.rows)
+        for (int64_t f = wg0 + blockIdx.x; f < g.n; f += gridDim.x) fork_row(g, (int)f);
+    const int64_t blocks = (g.n + p.block - 1) / p.block, items = blocks * p.c.n;
+    const int tid = threadIdx.x;
+    for (int64_t it = wg0 + blockIdx.x; it < items; it += gridDim.x) {   // workgroup-uniform
+        const int64_t k0 = it % blocks * p.block;
+        __syncthreads();
+        if (tid < p.block) {
+            int src = -1, dst = -1;
+            const int64_t k = k0 + tid;
+            const int len = k < g.n ? g.len[k] : -1;
+            if (len >= 0 && len % g.t.block_size) {
+                src = g.t.table[(int64_t)g.a[k] * g.t.stride + len / g.t.block_size];
+                dst = g.free_ids[first_page(g, (int)k)];
+                if (src < 0 || src >= p.c.num_blocks || src == dst) src = -1;
+            }
+            s_src[tid] = src;
+            s_dst[tid] = dst;
+        }
+        __syncthreads();
+        uint8_t* base = p.c.base[it / blocks];
+        const int64_t n = p.c.page_bytes / (int64_t)sizeof(V);
+        for (int64_t i0 = tid; i0 < n; i0 += U * kBlockThreads) {
+            V v[U];
+            int have = -1;
+            for (int k = 0; k < p.block; k++) {
+                const int src = s_src[k];
+                if (src < 0) continue;
+                if (src != have) {
+                    const V* s = reinterpret_cast<const V*>(base + (int64_t)src * p.c.block_stride);
+#pragma unroll
+                    for (int u = 0; u < U; u++)
+                        if (i0 + u * kBlockThreads < n) v[u] = __builtin_nontemporal_load(s + i0 + u * kBlockThreads);
+                    have = src;
+                }
+                V* d = reinterpret_cast<V*>(base + (int64_t)s_dst[k] * p.c.block_stride);
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    if (i0 + u * kBlockThreads < n) __builtin_nontemporal_store(v[u], d + i0 + u * kBlockThreads);
+            }
+        }
+        for (int64_t i = n * (int64_t)sizeof(V) + tid; i < p.c.page_bytes; i += kBlockThreads)
+            for (int k = 0; k < p.block; k++)
+                if (s_src[k] >= 0)
+                    base[(int64_t)s_dst[k] * p.c.block_stride + i] = base[(int64_t)s_src[k] * p.c.block_stride + i];
+    }
+}
+
+// Widest access that every page of the caches is aligned to, in bytes.
+static int page_align(const CacheList& c) {
+    uintptr_t bits = (uintptr_t)c.block_stride;
+    for (int i = 0; i < c.n; i++) bits |= reinterpret_cast<uintptr_t>(c.base[i]);
+    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 1;
+}
+// A fixed grid that fills the device eight workgroups a CU deep.
+static int64_t copy_grid(int64_t items) { return items < 1 ? 1 : items < 2048 ? items : 2048; }
+
 static hipError_t copy_pairs(const CopyParams& p, int64_t items, hipStream_t s, bool first, bool last) {
-    uintptr_t bits = (uintptr_t)p.c.block_stride;
-    for (int i = 0; i < p.c.n; i++) bits |= reinterpret_cast<uintptr_t>(p.c.base[i]);
-    // a fixed grid that fills the device eight workgroups a CU deep
-    const int64_t grid = items < 2048 ? (items > 0 ? items : 1) : 2048;
-    auto k = bits % 16 == 0 ? k_copy_pages<u32x4> : bits % 8 == 0 ? k_copy_pages<u32x2>
-             : bits % 4 == 0 ? k_copy_pages<uint32_t> : k_copy_pages<uint8_t>;
-    return launch_span(k, grid, kBlockThreads, s, first, last, p);
+    const int al = page_align(p.c);
+    return launch_span(al == 16 ? k_copy_pages<u32x4> : al == 8 ? k_copy_pages<u32x2> : al == 4 ? k_copy_pages<uint32_t>
+                                                                                                : k_copy_pages<uint8_t>,
+                       copy_grid(items), kBlockThreads, s, first, last, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -364,21 +465,28 @@ __global__ __launch_bounds__(kBlockThreads) void k_compact_finish(CompactParams 
 // ---------------------------------------------------------------------------
 hipError_t launch_copy_pages(const CacheList& c, const int32_t* src, const int32_t* dst, int64_t n, hipStream_t s,
                              bool first, bool last) {
-    CopyParams p{c, {src, dst, nullptr, n, {}, false}};
+    CopyParams p{c, {src, dst, nullptr, n}};
     return copy_pairs(p, n * c.n, s, first, last);
 }
-hipError_t launch_fork_plan(const GrantParams& g, hipStream_t s) {
-    return launch_span(k_grant_plan<true>, 1, kPlanThreads, s, true, false, g);
+static hipError_t launch_plan(bool fork, const GrantParams& g, hipStream_t s) {
+    auto k = g.n <= kPlanThreads ? (fork ? k_grant_small<true> : k_grant_small<false>)
+                                 : (fork ? k_grant_plan<true> : k_grant_plan<false>);
+    return launch_span(k, 1, kPlanThreads, s, true, false, g);
 }
-hipError_t launch_fork_rows(const GrantParams& g, hipStream_t s, bool last) {
-    return launch_span(k_fork_rows, g.n, kBlockThreads, s, false, last, g);
-}
-hipError_t launch_fork_copy(const GrantParams& g, const CacheList& c, hipStream_t s, bool last) {
-    CopyParams p{c, {nullptr, nullptr, nullptr, g.n, g, true}};
-    return copy_pairs(p, (int64_t)g.n * c.n, s, false, last);
+hipError_t launch_fork_plan(const GrantParams& g, hipStream_t s) { return launch_plan(true, g, s); }
+hipError_t launch_fork_apply(const GrantParams& g, const CacheList& c, bool rows, hipStream_t s, bool last) {
+    // as many forks a workgroup as still leave the device full
+    int64_t block = (int64_t)g.n * c.n / 2048;
+    block = block < 1 ? 1 : block > kForkBlock ? kForkBlock : block;
+    ForkCopyParams p{c, g, (int32_t)block, rows};
+    const int64_t items = (g.n + block - 1) / block * c.n, wgs = rows && g.n > items ? g.n : items;
+    const int al = page_align(c);
+    return launch_span(al == 16 ? k_fork_apply<u32x4> : al == 8 ? k_fork_apply<u32x2> : al == 4 ? k_fork_apply<uint32_t>
+                                                                                                : k_fork_apply<uint8_t>,
+                       copy_grid(wgs), kBlockThreads, s, false, last, p);
 }
 hipError_t launch_extend(const GrantParams& g, hipStream_t s) {
-    const hipError_t e = launch_span(k_grant_plan<false>, 1, kPlanThreads, s, true, false, g);
+    const hipError_t e = launch_plan(false, g, s);
     return e != hipSuccess ? e : launch_span(k_extend_rows, g.n, kBlockThreads, s, false, true, g);
 }
 hipError_t launch_free(const PageTable& t, const int32_t* rows, int32_t n, hipStream_t s) {
@@ -391,7 +499,7 @@ hipError_t launch_compact_plan(const CompactParams& c, hipStream_t s) {
     return e != hipSuccess ? e : launch_span(k_compact_rank, wgs, kBlockThreads, s, false, false, c);
 }
 hipError_t launch_compact_move(const CompactParams& c, const CacheList& l, hipStream_t s) {
-    CopyParams p{l, {c.movers, c.holes, c.moves, 0, {}, false}};
+    CopyParams p{l, {c.movers, c.holes, c.moves, 0}};
     // at most half of the pages move; the count itself is on the device
     return copy_pairs(p, (int64_t)(c.t.num_blocks / 2 + 1) * l.n, s, false, false);
 }

@@ -8,70 +8,133 @@
 // Memory bound: 4 bytes moved a value.  A wave takes one token and several
 // of its heads, 8 values (16 bytes) a lane, so cos, sin and the weights are
 // loaded once for up to kHeadSets * 64 / lanes-per-head heads and all data
-// loads are in flight before the first is used.  The half-split pairing needs
-// the chunk rot/2 values away: the partner lane's raw words come by cross-lane
-// reads (4 dwords a head) rather than by a second load.
+// loads are in flight before the first is used.  Sums over a head's lanes and
+// the partner values of the half-split pairing (rot/2 away) come by lane
+// permutes inside the vector unit where the head has 16 lanes, the common
+// 128-value head rotated whole; the first form, with LDS-routed shuffles,
+// scalar table loads and IEEE division, took 120 us for 16384 tokens of 40
+// heads, this one 80 us (4.2 TB/s).
 #include "gcache_operators.h"
 
 namespace gcache {
 
 constexpr int kHeadSets = 4;     // heads a lane works on
 
-// q's lanes hold heads [0, heads[0]), k's the ones behind.
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+// Sum over aligned groups of 2^SH lanes.
+template <int SH>
+__device__ __forceinline__ float head_sum(float v) {
+    if (SH >= 1) v += __uint_as_float(dpp<0xB1>(__float_as_uint(v)));    // lane ^ 1
+    if (SH >= 2) v += __uint_as_float(dpp<0x4E>(__float_as_uint(v)));    // lane ^ 2
+    if (SH >= 3) v += __uint_as_float(dpp<0x141>(__float_as_uint(v)));   // mirror in 8: the other 4
+    if (SH >= 4) v += __uint_as_float(dpp<0x140>(__float_as_uint(v)));   // mirror in 16: the other 8
+    if (SH >= 5) v += __shfl_xor(v, 16);
+    if (SH >= 6) v += __shfl_xor(v, 32);
+    return v;
+}
+
+// N consecutive table values as floats.
+template <int N, bool BF16>
+__device__ __forceinline__ void table_values(const void* row, int at, float* out) {
+    if (BF16) {
+        const uint16_t* r = static_cast<const uint16_t*>(row) + at;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (N == 8) {
+            const u32x4 x = *reinterpret_cast<const u32x4_a2*>(r);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else {
+            const u32x2 x = *reinterpret_cast<const u32x2_a2*>(r);
+            w[0] = x.x, w[1] = x.y;
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) {
+            out[2 * i] = bf16_lo(w[i]);
+            out[2 * i + 1] = bf16_hi(w[i]);
+        }
+    } else {
+        const float* r = static_cast<const float*>(row) + at;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const u32x4 x = *reinterpret_cast<const u32x4_a4*>(r + i);
+            out[i] = __uint_as_float(x.x);
+            out[i + 1] = __uint_as_float(x.y);
+            out[i + 2] = __uint_as_float(x.z);
+            out[i + 3] = __uint_as_float(x.w);
+        }
+    }
+}
+
+// SH: log2 of the lanes of a head.  WHOLE: 16 lanes, half-split over all 128
+// values (the partner is lane ^ 8).  q's heads come first, k's behind.
+template <int SH, bool INTER, bool BF16, bool WHOLE>
 __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams p, int64_t wg0) {
+    constexpr int LPH = 1 << SH, HPW = 64 >> SH;         // lanes of a head, heads a wave's load holds
     const int lane = lane_id();
     const int64_t wave = (wg0 + blockIdx.x) * kWavesPerBlock + wave_id();
     const int64_t token = wave / p.waves_per_token;
     if (token >= p.num_tokens) return;
-    const int lph = 1 << p.lph_shift;                    // lanes of one head
-    const int sub = lane & (lph - 1), dim = 8 * sub;     // the lane's values dim .. dim + 7
-    const int head0 = (int)(wave - token * p.waves_per_token) * (kHeadSets << (6 - p.lph_shift)) + (lane >> p.lph_shift);
+    const int sub = lane & (LPH - 1), dim = 8 * sub;     // the lane's values dim .. dim + 7
+    const int head0 = (int)(wave - token * p.waves_per_token) * (kHeadSets * HPW) + (lane >> SH);
     const int total = p.heads[0] + p.heads[1];
-    const bool in_dim = dim < p.hs;
+    const bool in_dim = WHOLE || dim < p.hs;
+    const int64_t pos = p.rot > 0 ? p.positions[token] : 0;
 
     uint4 x[kHeadSets];
 #pragma unroll
     for (int u = 0; u < kHeadSets; u++) {
-        const int h = head0 + (u << (6 - p.lph_shift));
+        const int h = head0 + u * HPW;
         x[u] = make_uint4(0, 0, 0, 0);
         if (h < total && in_dim) {
             const int kk = h >= p.heads[0];
             x[u] = ld_stream16(p.x[kk] + token * p.x_ts[kk] + (int64_t)(h - (kk ? p.heads[0] : 0)) * p.x_hs[kk] + dim);
         }
     }
-    const int64_t pos = p.rot > 0 ? p.positions[token] : 0;
     const bool pos_ok = p.rot == 0 || (pos >= 0 && pos < p.max_pos);
-    const bool turn = dim < p.rot && pos_ok;
+    const bool turn = (WHOLE || dim < p.rot) && pos_ok;
     const int half = p.rot / 2;
-    const int partner = dim < half ? sub + half / 8 : sub - half / 8;   // half-split pairing
-    // cos and sin of the lane's values: 8 of each, or 4 for the interleaved pairs
-    float cs[8], sn[8];
+    const bool low = dim < half;
+    const int partner = low ? sub + half / 8 : sub - half / 8;          // half-split pairing
+    // cos and sin of the lane's values (of its four pairs when interleaved), the weights of both sides
+    constexpr int N = INTER ? 4 : 8;
+    float cs[N], sn[N];
 #pragma unroll
-    for (int i = 0; i < 8; i++) cs[i] = 1.0f, sn[i] = 0.0f;
+    for (int i = 0; i < N; i++) cs[i] = 1.0f, sn[i] = 0.0f;
     if (turn) {
-        const int at = p.interleaved ? dim / 2 : dim < half ? dim : dim - half;
-        const int n = p.interleaved ? 4 : 8;
-        if (p.cs_bf16) {
-            const uint16_t* row = static_cast<const uint16_t*>(p.cos_sin) + pos * p.cs_stride;
+        const int at = INTER ? dim / 2 : low ? dim : dim - half;
+        const void* row = static_cast<const uint8_t*>(p.cos_sin) + pos * p.cs_stride * (BF16 ? 2 : 4);
+        table_values<N, BF16>(row, at, cs);
+        table_values<N, BF16>(row, half + at, sn);
+        if (!INTER)
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (i < n) {
-                    cs[i] = __uint_as_float((uint32_t)row[at + i] << 16);
-                    sn[i] = __uint_as_float((uint32_t)row[half + at + i] << 16);
-                }
-        } else {
-            const float* row = static_cast<const float*>(p.cos_sin) + pos * p.cs_stride;
+            for (int i = 0; i < N; i++) sn[i] = low ? -sn[i] : sn[i];
+    }
+    float w[2][8], wp[2][8];                             // of the lane's values, of the partner's
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (i < n) {
-                    cs[i] = row[at + i];
-                    sn[i] = row[half + at + i];
-                }
+    for (int kk = 0; kk < 2; kk++) {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (p.heads[kk] > 0 && in_dim) {
+            a = *reinterpret_cast<const uint4*>(p.w[kk] + dim);
+            if (!INTER && turn) b = *reinterpret_cast<const uint4*>(p.w[kk] + 8 * partner);
+        }
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            w[kk][2 * i] = bf16_lo(aw[i]);
+            w[kk][2 * i + 1] = bf16_hi(aw[i]);
+            wp[kk][2 * i] = bf16_lo(bw[i]);
+            wp[kk][2 * i + 1] = bf16_hi(bw[i]);
         }
     }
 #pragma unroll
     for (int u = 0; u < kHeadSets; u++) {
-        const int h = head0 + (u << (6 - p.lph_shift));
+        const int h = head0 + u * HPW;
         const int kk = h >= p.heads[0];
         const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
         float v[8], ss = 0.0f;
@@ -82,22 +145,21 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
         }
 #pragma unroll
         for (int i = 0; i < 8; i++) ss = __builtin_fmaf(v[i], v[i], ss);
-        for (int st = 1; st < lph; st <<= 1) ss += __shfl_xor(ss, st);
-        const float inv = 1.0f / __builtin_sqrtf(ss / (float)p.hs + p.eps);
+        ss = head_sum<SH>(ss);
+        // v_rsq_f32: one ulp, against the bf16 rounding at the end
+        const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_hs, p.eps));
         uint32_t pw[4];
+        if (!INTER)
 #pragma unroll
-        for (int i = 0; i < 4; i++) pw[i] = __shfl(xw[i], (lane & ~(lph - 1)) | (partner & (lph - 1)));
+            for (int i = 0; i < 4; i++)
+                pw[i] = WHOLE ? dpp<0x128>(xw[i])        // row_ror:8 is lane ^ 8
+                              : (uint32_t)__shfl((int)xw[i], (lane & ~(LPH - 1)) | (partner & (LPH - 1)));
         if (h >= total || !in_dim) continue;
-        const uint4 wl = *reinterpret_cast<const uint4*>(p.w[kk] + dim);
-        const uint32_t ww[4] = {wl.x, wl.y, wl.z, wl.w};
         float y[8];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            y[2 * i] = v[2 * i] * inv * bf16_lo(ww[i]);
-            y[2 * i + 1] = v[2 * i + 1] * inv * bf16_hi(ww[i]);
-        }
+        for (int i = 0; i < 8; i++) y[i] = v[i] * inv * (kk ? w[1][i] : w[0][i]);
         if (turn) {
-            if (p.interleaved) {
+            if (INTER) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const float a = y[2 * i], b = y[2 * i + 1];
@@ -105,14 +167,10 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
                     y[2 * i + 1] = b * cs[i] + a * sn[i];
                 }
             } else {
-                const uint4 wp = *reinterpret_cast<const uint4*>(p.w[kk] + 8 * partner);
-                const uint32_t wq[4] = {wp.x, wp.y, wp.z, wp.w};
-                const float sign = dim < half ? -1.0f : 1.0f;
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float a = bf16_lo(pw[i]) * inv * bf16_lo(wq[i]), b = bf16_hi(pw[i]) * inv * bf16_hi(wq[i]);
-                    y[2 * i] = y[2 * i] * cs[2 * i] + sign * a * sn[2 * i];
-                    y[2 * i + 1] = y[2 * i + 1] * cs[2 * i + 1] + sign * b * sn[2 * i + 1];
+                for (int i = 0; i < 8; i++) {
+                    const float b = (i & 1 ? bf16_hi(pw[i / 2]) : bf16_lo(pw[i / 2])) * inv * (kk ? wp[1][i] : wp[0][i]);
+                    y[i] = y[i] * cs[i % N] + b * sn[i % N];
                 }
             }
         }
@@ -123,14 +181,24 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
     }
 }
 
-hipError_t launch_qk_norm_rope(const QkNormRopeParams& in, hipStream_t s) {
+template <int SH>
+static hipError_t launch_lanes(const QkNormRopeParams& in, hipStream_t s) {
     QkNormRopeParams p = in;
-    p.lph_shift = 1;                                     // hs >= 16: two lanes at least
-    while ((8 << p.lph_shift) < p.hs) p.lph_shift++;
-    const int per_wave = kHeadSets << (6 - p.lph_shift);
+    const int per_wave = kHeadSets * (64 >> SH);
     p.waves_per_token = (p.heads[0] + p.heads[1] + per_wave - 1) / per_wave;
-    const int64_t waves = p.num_tokens * p.waves_per_token;
-    return launch_span(k_qk_norm_rope, (waves + kWavesPerBlock - 1) / kWavesPerBlock, kBlockThreads, s, true, true, p);
+    p.inv_hs = 1.0f / (float)p.hs;
+    const int64_t wgs = (p.num_tokens * p.waves_per_token + kWavesPerBlock - 1) / kWavesPerBlock;
+    auto k = p.interleaved ? (p.cs_bf16 ? k_qk_norm_rope<SH, true, true, false> : k_qk_norm_rope<SH, true, false, false>)
+                           : (p.cs_bf16 ? k_qk_norm_rope<SH, false, true, false> : k_qk_norm_rope<SH, false, false, false>);
+    if constexpr (SH == 4)
+        if (!p.interleaved && p.hs == 128 && p.rot == 128)
+            k = p.cs_bf16 ? k_qk_norm_rope<4, false, true, true> : k_qk_norm_rope<4, false, false, true>;
+    return launch_span(k, wgs, kBlockThreads, s, true, true, p);
+}
+
+hipError_t launch_qk_norm_rope(const QkNormRopeParams& p, hipStream_t s) {
+    return p.hs <= 16 ? launch_lanes<1>(p, s) : p.hs <= 32 ? launch_lanes<2>(p, s) : p.hs <= 64 ? launch_lanes<3>(p, s)
+           : p.hs <= 128 ? launch_lanes<4>(p, s) : p.hs <= 256 ? launch_lanes<5>(p, s) : launch_lanes<6>(p, s);
 }
 
 }  // namespace gcache
