@@ -4,8 +4,13 @@
 
 namespace gcache {
 
-// Join the key splits of a row: one wave per (token, head).
+// Join the key splits of a row: one wave per (token, head).  The splits'
+// maxima and sums are read by a lane each and reduced across the wave; the
+// weighted rows follow with four loads in flight.
+constexpr int kMaxSplits = 256;
+
 __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, int64_t wg0) {
+    __shared__ float s_w[kWavesPerBlock][kMaxSplits];
     const int lane = lane_id();
     const int RT = p.row_tile;
     const int64_t id = (wg0 + blockIdx.x) * kWavesPerBlock + wave_id();
@@ -30,23 +35,51 @@ __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, 
     tile_range(p, t);
     if (t.total <= p.chunk) return;                      // written by its only workgroup
     const int n = min((t.total - 1) / p.chunk + 1, p.splits);
-    float mm = kNegInf;
-    for (int k = 0; k < n; k++) mm = fmaxf(mm, p.ws_ml[2 * (k * rows + id)]);
-    float ll = 0.0f;
-    for (int k = 0; k < n; k++) {
-        const float mk = p.ws_ml[2 * (k * rows + id)];
-        const float wt = mk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk - mm);
-        ll = __builtin_fmaf(wt, p.ws_ml[2 * (k * rows + id) + 1], ll);
+    float* wts = s_w[wave_id()];                         // this wave's own
+    float mk[kMaxSplits / kWave], lk[kMaxSplits / kWave], mm = kNegInf, ll = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / kWave; i++) {
+        const int k = i * kWave + lane;
+        mk[i] = kNegInf;
+        lk[i] = 0.0f;
+        if (k < n) {
+            const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + 2 * (k * rows + id));
+            mk[i] = ml.x;
+            lk[i] = ml.y;
+        }
+        mm = fmaxf(mm, mk[i]);
     }
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / kWave; i++) {
+        const float wt = mk[i] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk[i] - mm);
+        ll = __builtin_fmaf(wt, lk[i], ll);
+        if (i * kWave + lane < n) wts[i * kWave + lane] = wt;
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) ll += __shfl_xor(ll, d);
     const float scale = ll == 0.0f ? 0.0f : (p.gscale[1] ? *p.gscale[1] : 1.0f) / ll;
+    __builtin_amdgcn_wave_barrier();
     for (int d = 4 * lane; d < p.hs; d += 4 * kWave) {
         f32x4 acc = {0, 0, 0, 0};
-        for (int k = 0; k < n; k++) {
-            const float mk = p.ws_ml[2 * (k * rows + id)];
-            const float wt = mk == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk - mm);
-            const f32x4 x = *reinterpret_cast<const f32x4*>(p.ws_o + (k * rows + id) * p.hs + d);
+        const float* src = p.ws_o + id * p.hs + d;
+        int k = 0;
+        for (; k + 4 <= n; k += 4) {
+            f32x4 x[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(wt, x[i], acc[i]);
+            for (int u = 0; u < 4; u++) x[u] = *reinterpret_cast<const f32x4*>(src + (k + u) * rows * p.hs);
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                const float wt = wts[k + u];
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(wt, x[u][i], acc[i]);
+            }
+        }
+        for (; k < n; k++) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(src + k * rows * p.hs);
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(wts[k], x[i], acc[i]);
         }
         *reinterpret_cast<u32x2*>(p.out + (int64_t)token * p.o_ts + (int64_t)head * p.o_hs + d) =
             u32x2{pack_bf16x2(acc[0] * scale, acc[1] * scale), pack_bf16x2(acc[2] * scale, acc[3] * scale)};
@@ -76,8 +109,8 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     // one a CU), against the ragged ends of lengths and rounds
     const int64_t want = a.row_tiles <= 2 ? 2048 : dp > 256 ? 1024 : 4096;
     int64_t splits = want / groups;
-    if (splits > kt / 8) splits = kt / 8;                // at least two tiles for a wave
-    if (splits > 256) splits = 256;
+    if (splits > kt / 4) splits = kt / 4;                // at least a tile for each of four waves
+    if (splits > kMaxSplits) splits = kMaxSplits;
     const int64_t per = total_q * hq * (dv + 2);
     if (per > 0 && splits > ws_floats_avail / per) splits = ws_floats_avail / per;
     if (splits < 1) splits = 1;

@@ -97,21 +97,30 @@ __device__ __forceinline__ int64_t list_free(const GrantParams& p, int64_t want,
 template <bool FORK>
 __global__ __launch_bounds__(kPlanThreads) void k_grant_small(GrantParams p, int64_t) {
     __shared__ int64_t s_scan[kPlanWaves];
-    __shared__ __align__(16) int s_row[kPlanThreads];
+    constexpr int kSlots = 2 * kPlanThreads;             // 2048: the hash takes 11 bits
+    __shared__ int s_row[kSlots], s_first[kSlots];
     const int f = threadIdx.x, bs = p.t.block_size;
     const int a = f < p.n ? p.a[f] : -1, b = f < p.n ? p.b[f] : -1;
     const int row = FORK ? b : a;
     int len = f < p.n ? grant_len<FORK>(p, row, FORK ? a : b) : -1;
-    s_row[f] = len >= 0 ? row : -1;
-    __syncthreads();
-    bool again = false;                                  // an earlier valid request names the row
-#pragma unroll 4
-    for (int e = 0; e < (p.n + 3) / 4; e++) {
-        const int4 x = reinterpret_cast<const int4*>(s_row)[e];
-        again |= (x.x == row && 4 * e < f) || (x.y == row && 4 * e + 1 < f) || (x.z == row && 4 * e + 2 < f) ||
-                 (x.w == row && 4 * e + 3 < f);
+    // the lowest request of each row, by a hash table at most half full
+    for (int i = f; i < kSlots; i += kPlanThreads) {
+        s_row[i] = -1;
+        s_first[i] = INT32_MAX;
     }
-    if (again) len = -1;
+    __syncthreads();
+    int slot = 0;
+    if (len >= 0) {
+        slot = (int)((uint32_t)row * 2654435761u >> 21);
+        for (;;) {                                       // ends: more slots than rows
+            const int old = atomicCAS(&s_row[slot], -1, row);
+            if (old == -1 || old == row) break;
+            slot = (slot + 1) & (kSlots - 1);
+        }
+        atomicMin(&s_first[slot], f);
+    }
+    __syncthreads();
+    if (len >= 0 && s_first[slot] != f) len = -1;
     int need = 0;
     if (len >= 0) need = FORK ? len % bs != 0 : min(pages_of(len, bs) - pages_of(p.t.lens[row], bs), p.t.num_blocks);
     int64_t all;

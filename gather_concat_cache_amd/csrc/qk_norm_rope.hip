@@ -18,7 +18,7 @@
 
 namespace gcache {
 
-constexpr int kHeadSets = 4;     // heads a lane works on
+constexpr int kHeadSets = 5;     // heads a lane works on: 40 heads of 128 values fill two waves
 
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -93,7 +93,8 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
         x[u] = make_uint4(0, 0, 0, 0);
         if (h < total && in_dim) {
             const int kk = h >= p.heads[0];
-            x[u] = ld_stream16(p.x[kk] + token * p.x_ts[kk] + (int64_t)(h - (kk ? p.heads[0] : 0)) * p.x_hs[kk] + dim);
+            x[u] = *reinterpret_cast<const uint4*>(p.x[kk] + token * p.x_ts[kk] +
+                                                  (int64_t)(h - (kk ? p.heads[0] : 0)) * p.x_hs[kk] + dim);
         }
     }
     const bool pos_ok = p.rot == 0 || (pos >= 0 && pos < p.max_pos);
