@@ -133,19 +133,84 @@ __device__ __forceinline__ void tile_range(const AttnParams& p, RowTile& t) {
     t.total = p1 < 0 ? 0 : t.sink_tiles + max(0, end - t.win_tile0);
 }
 
-// Row tile `tile` of the call: request b owns the tile numbers from
-// qs[b] * group / RT + b on, which leaves it at least ceil(rows / RT).
-__device__ __forceinline__ bool find_tile(const AttnParams& p, int tile, int RT, RowTile& t) {
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)query_start(p, mid) * p.group / RT + mid <= tile) lo = mid;
-        else hi = mid;
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int scan_lanes(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);   // row_shr 1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // last lane of rows 0 and 2 to rows 1 and 3
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // last lane of the lower half to the upper
+    return x;
+}
+
+// Row tile and key split of work unit `unit` = place * splits + k.  The host
+// knows the packed rows but not how they fall into requests, so it launches
+// places for ceil(rows / RT) tiles of each request at worst, and workgroups
+// count the tiles themselves: up to 4096 requests as a sum over the lanes
+// (batch / 64 requests each, then the requests of one lane), so that unused
+// places are the last ones.  (Numbering tiles by a bound left every second
+// place unused for requests of one full tile; workgroups go to XCDs and their
+// shader engines round robin, and half of the engines had no work.)
+// Tiles run from the last to the first: causal tiles grow along a request, and
+// the longest start first.  The split is rotated by the request, or a split
+// number, empty for short requests, would stay on one XCD.
+constexpr int kDenseBatch = kWave * kWave;
+__device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int RT, RowTile& t, int& split) {
+    const int place = (int)(unit / p.splits);
+    const int lane = lane_id();
+    const auto tiles_of = [&](int rows) { return (max(rows, 0) + RT - 1) / RT; };
+    int tile, before;
+    if (p.batch <= kDenseBatch) {
+        const int per = (p.batch + kWave - 1) / kWave;
+        int b = min(lane * per, p.batch), q = query_start(p, b), n = 0;
+        const int end = min(b + per, p.batch), q_first = q;
+        for (; b < end; b++) {
+            const int next = query_start(p, b + 1);
+            n += tiles_of((next - q) * p.group);
+            q = next;
+        }
+        int upto = scan_lanes(n);
+        tile = __builtin_amdgcn_readlane(upto, kWave - 1) - 1 - place;
+        if (tile < 0) return false;
+        int at = __builtin_ctzll(__ballot(upto > tile));
+        before = __builtin_amdgcn_readlane(upto - n, at);
+        if (per == 1) {
+            t.b = at;
+            t.q0 = __builtin_amdgcn_readlane(q_first, at);
+            t.qlen = __builtin_amdgcn_readlane(q, at) - t.q0;
+        } else {
+            const int first = at * per;
+            b = min(first + min(lane, per), p.batch);
+            q = query_start(p, b);
+            const int next = query_start(p, min(b + 1, p.batch));
+            n = lane < per ? tiles_of((next - q) * p.group) : 0;
+            upto = scan_lanes(n);
+            const uint64_t over = __ballot(before + upto > tile);
+            if (over == 0) return false;                 // (query starts that changed meanwhile)
+            at = __builtin_ctzll(over);
+            t.b = first + at;
+            before += __builtin_amdgcn_readlane(upto - n, at);
+            t.q0 = __builtin_amdgcn_readlane(q, at);
+            t.qlen = __builtin_amdgcn_readlane(next, at) - t.q0;
+        }
+    } else {                                             // request b from tile floor((qs[b] group + b (RT - 1)) / RT) on
+        const auto first_tile = [&](int b) { return (int)(((int64_t)query_start(p, b) * p.group + (int64_t)b * (RT - 1)) / RT); };
+        tile = p.tiles - 1 - place;
+        if (tile < 0) return false;
+        int lo = 0, hi = p.batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first_tile(mid) <= tile) lo = mid;
+            else hi = mid;
+        }
+        t.b = lo;
+        before = first_tile(lo);
+        t.q0 = query_start(p, lo);
+        t.qlen = query_start(p, lo + 1) - t.q0;
     }
-    t.b = lo;
-    t.q0 = query_start(p, lo);
-    t.qlen = query_start(p, lo + 1) - t.q0;
-    const int64_t row0 = (tile - ((int64_t)t.q0 * p.group / RT + lo)) * RT;
+    split = (int)((uint32_t)(unit - (int64_t)place * p.splits + t.b) % (uint32_t)p.splits);
+    const int64_t row0 = (int64_t)(tile - before) * RT;
     const int64_t rows = (int64_t)t.qlen * p.group;
     if (t.qlen <= 0 || row0 < 0 || row0 >= rows) return false;
     t.row0 = (int)row0;

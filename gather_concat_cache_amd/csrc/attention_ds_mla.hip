@@ -69,10 +69,9 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
     __shared__ int s_flag[3];
 
     const int64_t unit = wg0 + blockIdx.x;
-    if (unit >= (int64_t)p.tiles * p.splits) return;
-    const int tile = (int)(unit / p.splits), split = (int)(unit % p.splits);
     RowTile t;
-    if (!find_tile(p, tile, kLatentRows, t)) return;
+    int split;
+    if (!find_tile(p, unit, kLatentRows, t, split)) return;
     const int v0 = split * p.chunk;
     if (split > 0 && v0 >= t.total) return;
     const int v1 = split == p.splits - 1 ? t.total : min(t.total, v0 + p.chunk);
@@ -223,9 +222,194 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few query rows over the latent cache: four waves and 16 rows.  In a step of
+// 64 keys wave w multiplies the rows with keys 16 w .. 16 w + 15; the four
+// waves agree on the rows' maxima and leave the weights in LDS; wave w then
+// adds dims 128 w .. 128 w + 127 of all 64 keys.  A wave so holds 32
+// accumulator registers instead of 128, and two workgroups fit a CU: one's
+// loads and barriers pass under the other's conversions.
+// ---------------------------------------------------------------------------
+constexpr int kTokenWaves = 4, kTokenKeys = 16 * kTokenWaves;
+
+template <bool UNI, bool TREE>
+__global__ __launch_bounds__(kTokenWaves * kWave, 2) void k_attention_latent_token(AttnParams p, int64_t wg0) {
+    constexpr int KF = 18;                               // K fragments of a key tile
+    __shared__ f16x4 s_p[kTokenKeys / kTileKeys][kWave][2];   // weights: tile, lane, half
+    __shared__ float s_top[kTokenWaves][16], s_l[kTokenWaves][16];
+
+    const int64_t unit = wg0 + blockIdx.x;
+    RowTile t;
+    int split;
+    if (!find_tile(p, unit, 16, t, split)) return;
+    const int t0 = split * p.chunk;                      // 32-key tiles; chunk is even
+    if (split > 0 && t0 >= t.total) return;
+    const int t1 = split == p.splits - 1 ? t.total : min(t.total, t0 + p.chunk);
+    const int v0 = t0 / 2, v1 = t1 / 2 + (t1 & 1);       // (keys behind an odd last tile are hidden from every row)
+
+    const int lane = lane_id(), w = wave_id();
+    const int c = lane & 15, g = lane >> 4;
+    const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
+    const auto look_up = [&](int x) { return find_pages<UNI, kTokenKeys>(p, bt_row, (x < v1 ? x : v0) * kTokenKeys, lane); };
+    // the lane's parts of its K row, and of its V rows: dims 128 w + 8 c .. + 7
+    const uint32_t kd = data_part<UNI>(p, c, 64 * g), ks = scale_part<UNI>(p, c, 8 * g);
+    const uint32_t rope = data_part<UNI>(p, c, kNvRopeOff + 16 * g);
+    uint32_t vd[4], vs[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        vd[j] = data_part<UNI>(p, 4 * g + j, 64 * w + 4 * c);
+        vs[j] = scale_part<UNI>(p, 4 * g + j, 8 * w + (c >> 1));
+    }
+    u32x4 rk[5];                                         // raw K: data, RoPE
+    u32x2 rs;
+    uint32_t rv[2][8], vsb[2][8];                        // raw V, scale bytes
+    const auto load_k = [&](const KeyPages& pg) {
+        const RowBytes b = row_bytes<UNI>(p, pg, w, c);
+#pragma unroll
+        for (int i = 0; i < 4; i++) rk[i] = *reinterpret_cast<const u32x4*>(b.d + kd + 16 * i);
+        rs = *reinterpret_cast<const u32x2*>(b.s + ks);
+        rk[4] = *reinterpret_cast<const u32x4*>(b.d + rope);
+    };
+    const auto load_v = [&](const KeyPages& pg) {
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+            const RowBytes gb[2] = {group_bytes<UNI>(p, pg, 2 * x), group_bytes<UNI>(p, pg, 2 * x + 1)};
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const RowBytes b = UNI ? gb[j >> 2] : row_bytes<UNI>(p, pg, 2 * x + (j >> 2), 4 * g + (j & 3));
+                rv[x][j] = *reinterpret_cast<const uint32_t*>(b.d + vd[j & 3]);
+                vsb[x][j] = b.s[vs[j & 3]];
+            }
+        }
+    };
+    KeyPages pg, pg_next;
+    if (v0 < v1) {
+        pg = look_up(v0);
+        pg_next = look_up(v0 + 1);
+        load_k(pg);
+    }
+    f16x8 q[KF];
+    float fac;
+    int pos, tok;
+    load_query<512, true>(p, t, 0, 0, lane, q, fac, pos, tok);
+    if (v0 < v1) load_v(pg);                             // (the query's raw words are 72 registers)
+    const int pos_lo = t.ctx + t.row0 / p.group, pos_hi = t.ctx + (t.row0 + t.rows - 1) / p.group;
+
+    f32x4 o[8];
+    float m = kNegInf, l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < 8; d++) o[d] = f32x4{0, 0, 0, 0};
+
+    for (int v = v0; v < v1; v++) {
+        // ---- S^T = K Q^T, two chains
+        const uint32_t live = live_keys<UNI, kTokenKeys>(p, pg, lane) >> (4 * w) & 0xF;
+        f32x4 s = {0, 0, 0, 0}, s2 = {0, 0, 0, 0};
+        f16x2 sc[8];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint32_t x = drop_nan_e4m3x4(rs[i]);
+            const f16x2 a = e4m3x2_f16<false>(x), b = e4m3x2_f16<true>(x);
+            sc[4 * i] = f16x2{a.x, a.x};
+            sc[4 * i + 1] = f16x2{a.y, a.y};
+            sc[4 * i + 2] = f16x2{b.x, b.x};
+            sc[4 * i + 3] = f16x2{b.y, b.y};
+        }
+#pragma unroll
+        for (int i = 0; i < KF; i++) {
+            const f16x8 a = i < 16 ? k_operand(rk[i / 4][i % 4], sc[i / 2 % 8]) : rope_operand(rk[4][2 * (i % 2)], rk[4][2 * (i % 2) + 1]);
+            f32x4& acc = i & 1 ? s2 : s;
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[i], acc, 0, 0, 0);
+        }
+        // ---- the next step's K takes the registers just used.  (Behind the last: the first step's page, unused.)
+        pg = pg_next;
+        pg_next = look_up(v + 2);
+        load_k(pg);
+        const int key0 = v * kTokenKeys + 16 * w;
+        s = (s + s2) * fac;
+        if (!__all(live == 0xF && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, 16)))
+            hide<TREE, 1>(p, t, pos, tok, key0 + 4 * g, live, &s);
+        // ---- the waves' common maximum; the accumulators follow it with a lag
+        const float top = group_max(fmaxf(max3(s[0], s[1], s[2]), s[3]));
+        if (g == 0) s_top[w][c] = top;
+        __syncthreads();
+        const float mn = fmaxf(fmaxf(fmaxf(m, s_top[0][c]), fmaxf(s_top[1][c], s_top[2][c])), s_top[3][c]);
+        if (__builtin_expect(__any(mn > m + kLag), 0)) { // workgroup-uniform
+            const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= al;
+#pragma unroll
+            for (int d = 0; d < 8; d++) o[d] *= al;
+        }
+        const float sub = m == kNegInf ? 0.0f : kShift - m;
+        f32x4 e;
+#pragma unroll
+        for (int i = 0; i < 4; i++) e[i] = __builtin_amdgcn_exp2f(s[i] + sub);
+        s_p[w >> 1][lane][w & 1] = f16x4{(_Float16)e[0], (_Float16)e[1], (_Float16)e[2], (_Float16)e[3]};
+        l += (e[0] + e[1]) + (e[2] + e[3]);
+        __syncthreads();
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+            const f16x8 pw = *reinterpret_cast<const f16x8*>(&s_p[x][lane][0]);
+            f16x2 vsc[4];
+            v_scales(vsb[x], vsc);
+            const PairedCodes y = pair_codes(rv[x]);
+            const auto mul = [&](int d, const f16x8& a) { o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw, o[d], 0, 0, 0); };
+            mul(0, v_operand<0>(y, vsc));
+            mul(1, v_operand<1>(y, vsc));
+            mul(2, v_operand<2>(y, vsc));
+            mul(3, v_operand<3>(y, vsc));
+            mul(4, v_operand<4>(y, vsc));
+            mul(5, v_operand<5>(y, vsc));
+            mul(6, v_operand<6>(y, vsc));
+            mul(7, v_operand<7>(y, vsc));
+        }
+        load_v(pg);
+    }
+
+    // ---- sums of the waves' keys, then each wave writes its 128 dims of every row
+    l = group_sum(l);
+    if (g == 0) s_l[w][c] = l;
+    __syncthreads();
+    if (c >= t.rows) return;
+    const bool partial = p.splits > 1 && t.total > p.chunk;
+    const float ll = (s_l[0][c] + s_l[1][c]) + (s_l[2][c] + s_l[3][c]);
+    const int row = t.row0 + c, tl = row / p.group, head = row - tl * p.group;
+    const int64_t id = (int64_t)(t.q0 + tl) * p.hq + head;
+    const float scale = partial ? 1.0f : ll == 0.0f ? 0.0f : 1.0f / ll;
+    if (g == 0 && w == 0) {
+        if (partial) {
+            float* ml = p.ws_ml + 2 * ((int64_t)split * p.total_q * p.hq + id);
+            ml[0] = m;
+            ml[1] = ll;
+        } else if (p.lse) {
+            p.lse[(int64_t)(t.q0 + tl) * p.lse_ts + head] = row_lse(m, ll);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const int dim = 128 * w + 8 * (4 * g + j);
+        if (partial) {
+            float* dst = p.ws_o + ((int64_t)split * p.total_q * p.hq + id) * kNope + dim;
+            *reinterpret_cast<f32x4*>(dst) = f32x4{o[0][j], o[1][j], o[2][j], o[3][j]};
+            *reinterpret_cast<f32x4*>(dst + 4) = f32x4{o[4][j], o[5][j], o[6][j], o[7][j]};
+        } else {
+            uint32_t pk[4];
+#pragma unroll
+            for (int d = 0; d < 4; d++) pk[d] = pack_bf16x2(o[2 * d][j] * scale, o[2 * d + 1][j] * scale);
+            *reinterpret_cast<u32x4*>(p.out + (int64_t)(t.q0 + tl) * p.o_ts + (int64_t)head * p.o_hs + dim) =
+                u32x4{pk[0], pk[1], pk[2], pk[3]};
+        }
+    }
+}
+
 hipError_t launch_attention_ds_mla(const AttnParams& p, int row_tiles, hipStream_t s) {
-    if (row_tiles == 1) return launch_few<512, true, 1>(p, s);
     const bool uni = uniform_pages(p);
+    if (row_tiles == 1)
+        return launch_attention_parts(
+            p.mask ? (uni ? k_attention_latent_token<true, true> : k_attention_latent_token<false, true>)
+                   : (uni ? k_attention_latent_token<true, false> : k_attention_latent_token<false, false>),
+            kTokenWaves, 16, p, s);
     return launch_attention_parts(p.mask ? (uni ? k_attention_latent<true, true> : k_attention_latent<false, true>)
                                          : (uni ? k_attention_latent<true, false> : k_attention_latent<false, false>),
                                   kLatentWaves, kLatentRows, p, s);

@@ -151,10 +151,9 @@ void k_attention_few(AttnParams p, int64_t wg0) {
     const int rem = (int)(wg % per);
     const int64_t unit = wg / per * 8 + rem % 8;
     const int kvh = rem / 8;
-    if (unit >= (int64_t)p.tiles * p.splits) return;
-    const int tile = (int)(unit / p.splits), split = (int)(unit % p.splits);
     RowTile t;
-    if (!find_tile(p, tile, RT, t)) return;
+    int split;
+    if (!find_tile(p, unit, RT, t, split)) return;
     const int v0 = split * p.chunk;                      // chunk * splits fits int32 (host)
     if (split > 0 && v0 >= t.total) return;
     // a sequence longer than the planned bound: the last split takes the rest

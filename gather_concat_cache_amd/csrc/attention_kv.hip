@@ -89,10 +89,9 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
     const int rem = (int)(wg % per);
     const int64_t unit = wg / per * 8 + rem % 8;
     const int kvh = rem / 8;
-    if (unit >= (int64_t)p.tiles * p.splits) return;
-    const int tile = (int)(unit / p.splits), split = (int)(unit % p.splits);
     RowTile t;
-    if (!find_tile(p, tile, RT, t)) return;
+    int split;
+    if (!find_tile(p, unit, RT, t, split)) return;
     const int v0 = split * p.chunk;                      // 32-key tiles, as in k_attention; chunk is even
     if (split > 0 && v0 >= t.total) return;
     const int v1 = split == p.splits - 1 ? t.total : min(t.total, v0 + p.chunk);

@@ -96,14 +96,14 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     const int64_t mean = (rows + batch - 1) / batch;     // rows of a request and kv head
     a.row_tiles = mean <= 16 || (dp >= 256 && mean <= 32) ? 1 : mean <= 32 ? 2 : dp > 256 ? 4 : 8;
     const int64_t rt = 16 * a.row_tiles;
-    a.tiles = (int32_t)(rows / rt + batch);
+    a.tiles = (int32_t)((rows + (rt - 1) * batch) / rt);
     // 32-key tiles that a row tile can see (a bound; only the split depends on it)
-    int64_t keys = max_seq_len;
+    int64_t kt = (max_seq_len + kTileKeys - 1) / kTileKeys;
     if (window > 0) {
-        const int64_t seen = (int64_t)window + rt / group + 1 + sinks + 2 * kTileKeys;
-        if (seen < keys) keys = seen;
+        const int64_t seen = ((int64_t)window + rt / group + 1 + sinks) / kTileKeys + 3;
+        if (seen < kt) kt = seen;
     }
-    const int64_t kt = (keys + kTileKeys - 1) / kTileKeys + 1;
+    if (kt < 1) kt = 1;
     const int64_t groups = (int64_t)a.tiles * hk;
     // workgroups: some rounds of what the device holds at once (three, two and
     // one a CU), against the ragged ends of lengths and rounds
