@@ -104,6 +104,7 @@ struct RowTile {
     int q0;                      // first packed query token of the request
     int qlen, ctx, kv_len;       // ctx = position of the request's first query
     int sink_tiles, win_tile0, total;   // 32-key tiles: [0, sink_tiles) then from win_tile0
+    int split, splits, chunk;    // the unit's key split, splits of the request, key tiles of one
 };
 
 __device__ __forceinline__ int query_start(const AttnParams& p, int b) {
@@ -144,64 +145,100 @@ __device__ __forceinline__ int scan_lanes(int x) {
     return x;
 }
 
-// Row tile and key split of work unit `unit` = place * splits + k.  The host
-// knows the packed rows but not how they fall into requests, so it launches
-// places for ceil(rows / RT) tiles of each request at worst, and workgroups
-// count the tiles themselves: up to 4096 requests as a sum over the lanes
-// (batch / 64 requests each, then the requests of one lane), so that unused
-// places are the last ones.  (Numbering tiles by a bound left every second
-// place unused for requests of one full tile; workgroups go to XCDs and their
-// shader engines round robin, and half of the engines had no work.)
-// Tiles run from the last to the first: causal tiles grow along a request, and
-// the longest start first.  The split is rotated by the request, or a split
-// number, empty for short requests, would stay on one XCD.
+// Key splits of a request: as many as its length gives in pieces of `chunk`
+// 32-key tiles (a multiple of 4), at least one.
+__device__ __forceinline__ int request_work(const AttnParams& p, int b) {
+    return min((int)(((uint32_t)max(p.seq_lens[b], 0) + kTileKeys - 1) / kTileKeys), p.key_tiles);
+}
+__device__ __forceinline__ int request_splits(int work, int chunk) { return max(1, (work + chunk - 1) / chunk); }
+
+// What work unit `unit` of a kv head is.  The host knows the packed rows and
+// the longest sequence, but not how rows fall into requests nor how long each
+// is.  It launches p.units workgroups a head, and each counts for itself: the
+// size of a split is the smallest (in steps of about 1/16) for which all
+// requests' splits fit the launched units, so that every unit has work of the
+// same size whatever the lengths are.  Counts are sums over the lanes, each with
+// batch / 64 requests, then over the requests of one lane.  Units run from the
+// last to the first: causal tiles grow along a request, and the longest start
+// first.  The split is rotated by the request, or the short last splits of
+// equal requests would share an XCD.
+// (With a fixed split size and row tiles numbered by a bound, every second
+// number was unused for requests of one full tile; workgroups go to XCDs and
+// their shader engines round robin, and half of the engines had no work.)
+// Batches over kDenseBatch requests are numbered by that bound; they are not split.
 constexpr int kDenseBatch = kWave * kWave;
-__device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int RT, RowTile& t, int& split) {
-    const int place = (int)(unit / p.splits);
+__device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int RT, RowTile& t) {
     const int lane = lane_id();
     const auto tiles_of = [&](int rows) { return (max(rows, 0) + RT - 1) / RT; };
-    int tile, before;
+    int index, before;
+    t.splits = 1;
+    t.chunk = INT32_MAX;
     if (p.batch <= kDenseBatch) {
+        const bool split = p.splits > 1;
         const int per = (p.batch + kWave - 1) / kWave;
-        int b = min(lane * per, p.batch), q = query_start(p, b), n = 0;
-        const int end = min(b + per, p.batch), q_first = q;
-        for (; b < end; b++) {
-            const int next = query_start(p, b + 1);
-            n += tiles_of((next - q) * p.group);
-            q = next;
+        const int b0 = min(lane * per, p.batch), b1 = min(b0 + per, p.batch);
+        const int q_first = query_start(p, b0), q_last = query_start(p, b1);
+        const int tiles1 = b0 < b1 ? tiles_of((q_last - q_first) * p.group) : 0;    // where a lane has one request
+        const int work1 = split && b0 < b1 ? request_work(p, b0) : 0;
+        const auto sum = [&](auto of) {                  // of(row tiles, work) over the lane's requests
+            if (per == 1) return of(tiles1, work1);
+            decltype(of(0, 0)) n = 0;
+            int q = q_first;
+            for (int b = b0; b < b1; b++) {
+                const int next = query_start(p, b + 1);
+                n += of(tiles_of((next - q) * p.group), split ? request_work(p, b) : 0);
+                q = next;
+            }
+            return n;
+        };
+        int n, upto, all;
+        if (split) {
+            float work = sum([](int tiles, int w) { return (float)tiles * (float)w; });
+#pragma unroll
+            for (int d = 1; d < kWave; d <<= 1) work += __shfl_xor(work, d);
+            const int least = max((int)(work / (float)p.units), (p.key_tiles - 1) / p.splits + 1);
+            t.chunk = __builtin_amdgcn_readfirstlane((max(least, 1) + 3) / 4 * 4);
         }
-        int upto = scan_lanes(n);
-        tile = __builtin_amdgcn_readlane(upto, kWave - 1) - 1 - place;
-        if (tile < 0) return false;
-        int at = __builtin_ctzll(__ballot(upto > tile));
+        for (;;) {
+            const int chunk = t.chunk;
+            n = sum([&](int tiles, int w) { return split ? tiles * request_splits(w, chunk) : tiles; });
+            upto = scan_lanes(n);
+            all = __builtin_amdgcn_readlane(upto, kWave - 1);
+            if (!split || all <= p.units || chunk >= p.key_tiles) break;
+            t.chunk += max(4, chunk >> 4 & ~3);
+        }
+        if (split && unit == 0 && threadIdx.x == 0) *p.ws_chunk = t.chunk;
+        if (unit >= all) return false;
+        index = all - 1 - (int)unit;
+        int at = __builtin_ctzll(__ballot(upto > index));
         before = __builtin_amdgcn_readlane(upto - n, at);
+        int work = work1;
         if (per == 1) {
             t.b = at;
             t.q0 = __builtin_amdgcn_readlane(q_first, at);
-            t.qlen = __builtin_amdgcn_readlane(q, at) - t.q0;
+            t.qlen = __builtin_amdgcn_readlane(q_last, at) - t.q0;
         } else {
-            const int first = at * per;
-            b = min(first + min(lane, per), p.batch);
-            q = query_start(p, b);
-            const int next = query_start(p, min(b + 1, p.batch));
-            n = lane < per ? tiles_of((next - q) * p.group) : 0;
+            const int first = at * per, b = min(first + min(lane, per), p.batch);
+            const int q = query_start(p, b), next = query_start(p, min(b + 1, p.batch));
+            work = split && lane < per && b < p.batch ? request_work(p, b) : 0;
+            const int tiles = lane < per ? tiles_of((next - q) * p.group) : 0;
+            n = split ? tiles * request_splits(work, t.chunk) : tiles;
             upto = scan_lanes(n);
-            const uint64_t over = __ballot(before + upto > tile);
-            if (over == 0) return false;                 // (query starts that changed meanwhile)
-            at = __builtin_ctzll(over);
+            at = __builtin_ctzll(__ballot(before + upto > index));
             t.b = first + at;
             before += __builtin_amdgcn_readlane(upto - n, at);
             t.q0 = __builtin_amdgcn_readlane(q, at);
             t.qlen = __builtin_amdgcn_readlane(next, at) - t.q0;
         }
+        if (split) t.splits = request_splits(__builtin_amdgcn_readlane(work, at), t.chunk);
     } else {                                             // request b from tile floor((qs[b] group + b (RT - 1)) / RT) on
         const auto first_tile = [&](int b) { return (int)(((int64_t)query_start(p, b) * p.group + (int64_t)b * (RT - 1)) / RT); };
-        tile = p.tiles - 1 - place;
-        if (tile < 0) return false;
+        if (unit >= p.tiles) return false;
+        index = p.tiles - 1 - (int)unit;
         int lo = 0, hi = p.batch;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (first_tile(mid) <= tile) lo = mid;
+            if (first_tile(mid) <= index) lo = mid;
             else hi = mid;
         }
         t.b = lo;
@@ -209,14 +246,21 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int
         t.q0 = query_start(p, lo);
         t.qlen = query_start(p, lo + 1) - t.q0;
     }
-    split = (int)((uint32_t)(unit - (int64_t)place * p.splits + t.b) % (uint32_t)p.splits);
-    const int64_t row0 = (int64_t)(tile - before) * RT;
-    const int64_t rows = (int64_t)t.qlen * p.group;
+    const int in = index - before, tile = in / t.splits;
+    t.split = (int)((uint32_t)(in - tile * t.splits + t.b) % (uint32_t)t.splits);
+    const int64_t row0 = (int64_t)tile * RT, rows = (int64_t)t.qlen * p.group;
     if (t.qlen <= 0 || row0 < 0 || row0 >= rows) return false;
     t.row0 = (int)row0;
     t.rows = (int)min((int64_t)RT, rows - row0);
     tile_range(p, t);
     return true;
+}
+// Key tiles [v0, v1) of the unit; false: the split is behind the tile's last key.
+__device__ __forceinline__ bool key_range(const RowTile& t, int& v0, int& v1) {
+    v0 = t.split > 0 ? t.split * t.chunk : 0;
+    // a sequence longer than the call's bound: the last split takes the rest
+    v1 = t.split == t.splits - 1 ? t.total : min(t.total, v0 + t.chunk);
+    return t.split == 0 || v0 < t.total;
 }
 
 // Block and offset of a position; positions are below 2^31.

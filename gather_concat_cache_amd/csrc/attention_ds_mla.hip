@@ -70,11 +70,9 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
 
     const int64_t unit = wg0 + blockIdx.x;
     RowTile t;
-    int split;
-    if (!find_tile(p, unit, kLatentRows, t, split)) return;
-    const int v0 = split * p.chunk;
-    if (split > 0 && v0 >= t.total) return;
-    const int v1 = split == p.splits - 1 ? t.total : min(t.total, v0 + p.chunk);
+    if (!find_tile(p, unit, kLatentRows, t)) return;
+    int v0, v1;
+    if (!key_range(t, v0, v1)) return;
 
     const int lane = lane_id(), w = wave_id();
     const int c = lane & 15, g = lane >> 4;
@@ -189,7 +187,7 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
     l = group_sum(l);
     if (g == 0) s_l[kt][rt][c] = l;
     __syncthreads();
-    const bool partial = p.splits > 1 && t.total > p.chunk;
+    const bool partial = p.splits > 1 && t.total > t.chunk;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int off = 16 * i + c;
@@ -200,7 +198,7 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
         const float scale = partial ? 1.0f : ll == 0.0f ? 0.0f : 1.0f / ll;
         if (g == 0 && w == i) {
             if (partial) {
-                float* ml = p.ws_ml + 2 * ((int64_t)split * p.total_q * p.hq + id);
+                float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
                 ml[0] = m[i];
                 ml[1] = ll;
             } else if (p.lse) {
@@ -213,7 +211,7 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
             const int dim = 64 * w + 4 * (4 * g + j);
             const f32x4 x = {o[i][0][j], o[i][1][j], o[i][2][j], o[i][3][j]};
             if (partial) {
-                *reinterpret_cast<f32x4*>(p.ws_o + ((int64_t)split * p.total_q * p.hq + id) * kNope + dim) = x;
+                *reinterpret_cast<f32x4*>(p.ws_o + ((int64_t)t.split * p.total_q * p.hq + id) * kNope + dim) = x;
             } else {
                 *reinterpret_cast<u32x2*>(p.out + (int64_t)(t.q0 + tl) * p.o_ts + (int64_t)head * p.o_hs + dim) =
                     u32x2{pack_bf16x2(x[0] * scale, x[1] * scale), pack_bf16x2(x[2] * scale, x[3] * scale)};
@@ -240,11 +238,9 @@ __global__ __launch_bounds__(kTokenWaves * kWave, 2) void k_attention_latent_tok
 
     const int64_t unit = wg0 + blockIdx.x;
     RowTile t;
-    int split;
-    if (!find_tile(p, unit, 16, t, split)) return;
-    const int t0 = split * p.chunk;                      // 32-key tiles; chunk is even
-    if (split > 0 && t0 >= t.total) return;
-    const int t1 = split == p.splits - 1 ? t.total : min(t.total, t0 + p.chunk);
+    if (!find_tile(p, unit, 16, t)) return;
+    int t0, t1;                                    // 32-key tiles; an even number but for the last split
+    if (!key_range(t, t0, t1)) return;
     const int v0 = t0 / 2, v1 = t1 / 2 + (t1 & 1);       // (keys behind an odd last tile are hidden from every row)
 
     const int lane = lane_id(), w = wave_id();
@@ -372,14 +368,14 @@ __global__ __launch_bounds__(kTokenWaves * kWave, 2) void k_attention_latent_tok
     if (g == 0) s_l[w][c] = l;
     __syncthreads();
     if (c >= t.rows) return;
-    const bool partial = p.splits > 1 && t.total > p.chunk;
+    const bool partial = p.splits > 1 && t.total > t.chunk;
     const float ll = (s_l[0][c] + s_l[1][c]) + (s_l[2][c] + s_l[3][c]);
     const int row = t.row0 + c, tl = row / p.group, head = row - tl * p.group;
     const int64_t id = (int64_t)(t.q0 + tl) * p.hq + head;
     const float scale = partial ? 1.0f : ll == 0.0f ? 0.0f : 1.0f / ll;
     if (g == 0 && w == 0) {
         if (partial) {
-            float* ml = p.ws_ml + 2 * ((int64_t)split * p.total_q * p.hq + id);
+            float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
             ml[0] = m;
             ml[1] = ll;
         } else if (p.lse) {
@@ -390,7 +386,7 @@ __global__ __launch_bounds__(kTokenWaves * kWave, 2) void k_attention_latent_tok
     for (int j = 0; j < 4; j++) {
         const int dim = 128 * w + 8 * (4 * g + j);
         if (partial) {
-            float* dst = p.ws_o + ((int64_t)split * p.total_q * p.hq + id) * kNope + dim;
+            float* dst = p.ws_o + ((int64_t)t.split * p.total_q * p.hq + id) * kNope + dim;
             *reinterpret_cast<f32x4*>(dst) = f32x4{o[0][j], o[1][j], o[2][j], o[3][j]};
             *reinterpret_cast<f32x4*>(dst + 4) = f32x4{o[4][j], o[5][j], o[6][j], o[7][j]};
         } else {

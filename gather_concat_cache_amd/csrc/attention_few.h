@@ -152,12 +152,9 @@ void k_attention_few(AttnParams p, int64_t wg0) {
     const int64_t unit = wg / per * 8 + rem % 8;
     const int kvh = rem / 8;
     RowTile t;
-    int split;
-    if (!find_tile(p, unit, RT, t, split)) return;
-    const int v0 = split * p.chunk;                      // chunk * splits fits int32 (host)
-    if (split > 0 && v0 >= t.total) return;
-    // a sequence longer than the planned bound: the last split takes the rest
-    const int v1 = split == p.splits - 1 ? t.total : min(t.total, v0 + p.chunk);
+    if (!find_tile(p, unit, RT, t)) return;
+    int v0, v1;                                    // 32-key tiles; an even number but for the last split
+    if (!key_range(t, v0, v1)) return;
 
     const int lane = lane_id(), w = wave_id();
     const int c = lane & 15, g = lane >> 4;
@@ -324,7 +321,7 @@ void k_attention_few(AttnParams p, int64_t wg0) {
     }
 
     // ---- join the four waves, 16 rows and 16 * DW dims at a time
-    const bool partial = p.splits > 1 && t.total > p.chunk;
+    const bool partial = p.splits > 1 && t.total > t.chunk;
     const float gv = MLA ? 1.0f : *p.gscale[1];
     const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;   // the row and dim column this thread writes
 #pragma unroll
@@ -364,7 +361,7 @@ void k_attention_few(AttnParams p, int64_t wg0) {
                 scale = partial ? 1.0f : ll == 0.0f ? 0.0f : gv / ll;
                 if (in && jc == 0) {
                     if (partial) {
-                        float* ml = p.ws_ml + 2 * ((int64_t)split * p.total_q * p.hq + id);
+                        float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
                         ml[0] = mm;
                         ml[1] = ll;
                     } else if (p.lse) {
@@ -382,7 +379,7 @@ void k_attention_few(AttnParams p, int64_t wg0) {
             const int dim = jc * DT + ch * DW;
             if (in && (MLA || dim < p.hs)) {
                 if (partial) {
-                    float* dst = p.ws_o + ((int64_t)split * p.total_q * p.hq + id) * p.hs + dim;
+                    float* dst = p.ws_o + ((int64_t)t.split * p.total_q * p.hq + id) * p.hs + dim;
 #pragma unroll
                     for (int d = 0; d < DW; d += 4)
                         *reinterpret_cast<f32x4*>(dst + d) = f32x4{acc[d], acc[d + 1], acc[d + 2], acc[d + 3]};

@@ -90,11 +90,9 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
     const int64_t unit = wg / per * 8 + rem % 8;
     const int kvh = rem / 8;
     RowTile t;
-    int split;
-    if (!find_tile(p, unit, RT, t, split)) return;
-    const int v0 = split * p.chunk;                      // 32-key tiles, as in k_attention; chunk is even
-    if (split > 0 && v0 >= t.total) return;
-    const int v1 = split == p.splits - 1 ? t.total : min(t.total, v0 + p.chunk);
+    if (!find_tile(p, unit, RT, t)) return;
+    int v0, v1;                                    // 32-key tiles; an even number but for the last split
+    if (!key_range(t, v0, v1)) return;
 
     const int lane = lane_id(), w = wave_id();
     const int c = lane & 15, g = lane >> 4;
@@ -221,7 +219,7 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
     }
 
     // ---- each lane holds 4 runs of DT dims of its row
-    const bool partial = p.splits > 1 && t.total > p.chunk;
+    const bool partial = p.splits > 1 && t.total > t.chunk;
     const float gv = *p.gscale[1];
 #pragma unroll
     for (int r = 0; r < R; r++) {
@@ -233,7 +231,7 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
         const float scale = partial ? 1.0f : ll == 0.0f ? 0.0f : gv / ll;
         if (g == 0) {
             if (partial) {
-                float* ml = p.ws_ml + 2 * ((int64_t)split * p.total_q * p.hq + id);
+                float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
                 ml[0] = m[r];
                 ml[1] = ll;
             } else if (p.lse) {
@@ -246,7 +244,7 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
             const int dim = (4 * g + i) * DT;
             if (dim >= p.hs) continue;
             if (partial) {
-                float* dst = p.ws_o + ((int64_t)split * p.total_q * p.hq + id) * p.hs + dim;
+                float* dst = p.ws_o + ((int64_t)t.split * p.total_q * p.hq + id) * p.hs + dim;
 #pragma unroll
                 for (int d = 0; d < DT; d += 4)
                     *reinterpret_cast<f32x4*>(dst + d) = f32x4{o[r][d][i], o[r][d + 1][i], o[r][d + 2][i], o[r][d + 3][i]};

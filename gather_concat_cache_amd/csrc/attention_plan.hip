@@ -8,6 +8,9 @@ namespace gcache {
 // maxima and sums are read by a lane each and reduced across the wave; the
 // weighted rows follow with four loads in flight.
 constexpr int kMaxSplits = 256;
+// Larger batches are not split: each workgroup counts their requests (and 1024
+// requests fill the device once or more).
+constexpr int kSplitBatch = 1024;
 
 __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, int64_t wg0) {
     __shared__ float s_w[kWavesPerBlock][kMaxSplits];
@@ -33,8 +36,9 @@ __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, 
     t.row0 = row / RT * RT;
     t.rows = (int)min((int64_t)RT, (int64_t)t.qlen * p.group - t.row0);
     tile_range(p, t);
-    if (t.total <= p.chunk) return;                      // written by its only workgroup
-    const int n = min((t.total - 1) / p.chunk + 1, p.splits);
+    const int chunk = *p.ws_chunk;
+    if (t.total <= chunk) return;                        // written by its only workgroup
+    const int n = min((t.total - 1) / chunk + 1, request_splits(request_work(p, t.b), chunk));
     float* wts = s_w[wave_id()];                         // this wave's own
     float mk[kMaxSplits / kWave], lk[kMaxSplits / kWave], mm = kNegInf, ll = 0.0f;
 #pragma unroll
@@ -103,26 +107,46 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
         const int64_t seen = ((int64_t)window + rt / group + 1 + sinks) / kTileKeys + 3;
         if (seen < kt) kt = seen;
     }
+    if (kt > INT32_MAX / kTileKeys) kt = INT32_MAX / kTileKeys;
     if (kt < 1) kt = 1;
-    const int64_t groups = (int64_t)a.tiles * hk;
-    // workgroups: some rounds of what the device holds at once (three, two and
-    // one a CU), against the ragged ends of lengths and rounds
-    const int64_t want = a.row_tiles <= 2 ? 2048 : dp > 256 ? 1024 : 4096;
-    int64_t splits = want / groups;
-    if (splits > kt / 4) splits = kt / 4;                // at least a tile for each of four waves
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    const int64_t per = total_q * hq * (dv + 2);
-    if (per > 0 && splits > ws_floats_avail / per) splits = ws_floats_avail / per;
-    if (splits < 1) splits = 1;
-    int64_t chunk = (kt + splits - 1) / splits;
-    chunk = (chunk + 4 - 1) / 4 * 4;
-    splits = (kt + chunk - 1) / chunk;
-    a.splits = (int32_t)splits;
-    a.chunk = splits == 1 ? INT32_MAX : (int32_t)chunk;
-    a.ws_floats = splits > 1 ? splits * per : 0;
+    // Work units: rounds of resident workgroups x (key tiles of a split + what a
+    // split costs besides: its start, and its part of the output, written and
+    // read again) + half a split for the ragged end, in units of one tile's
+    // time, for requests of equal length; the kernels size the splits so that
+    // other lengths give as many.  Per-head kernels for few rows are bound by
+    // HBM, which half a round of workgroups already fills, so their rounds are
+    // not counted whole.
+    const int64_t groups = (mean + rt - 1) / rt * batch * hk;
+    const bool few = a.row_tiles <= 2, whole = !few || dp > 256;
+    const int64_t slots = 256 * (!few ? (dp <= 128 ? 2 : 1) : a.row_tiles * dp <= 128 ? 3 : 2);
+    const int64_t extra = !few ? 12 : dp > 256 ? 6 : 8;
+    const auto cost_of = [&](int64_t units, int64_t tiles) {
+        return whole ? (units + slots - 1) / slots * tiles : units > slots ? units * tiles / slots : tiles;
+    };
+    const int64_t per = total_q * hq * (dv + 2);         // floats of a split; one more split's room holds the chunk
+    const int64_t room = per > 0 ? ws_floats_avail / per - 1 : 0;
+    int64_t top = kt / 4 < kMaxSplits ? kt / 4 : kMaxSplits;    // at least a tile for each of four waves
+    if (top > room) top = room;
+    int64_t most = top;
+    if (most > 8 * slots / groups) most = 8 * slots / groups;   // eight rounds are even enough
+    if (batch > kSplitBatch) most = 1;
+    int64_t splits = 1, best = cost_of(groups, kt) + kt / 2;
+    for (int64_t n = 2; n <= most; n += n < 16 ? 1 : n / 16) {
+        const int64_t c = ((kt + n - 1) / n + 3) / 4 * 4, m = (kt + c - 1) / c;
+        const int64_t cost = cost_of(groups * m, c + extra) + c / 2;
+        if (cost < best) {
+            best = cost;
+            splits = m;
+        }
+    }
+    a.key_tiles = (int32_t)kt;
+    a.units = a.tiles;
+    if (splits > 1 && splits * groups / hk > a.tiles) a.units = (int32_t)(splits * groups / hk);
+    // requests longer than the mean are split further
+    a.splits = (int32_t)(splits == 1 ? 1 : 2 * splits < top ? 2 * splits : top);
+    a.ws_floats = splits > 1 ? (a.splits + 1) * per : 0;
     return a;
 }
-
 
 // 16 keys of one page, with the head and side offsets, within 32 bits.
 bool uniform_pages(const AttnParams& p) {
@@ -141,7 +165,7 @@ hipError_t launch_attention_parts(void (*kernel)(AttnParams, int64_t), int waves
     p.data_token = (uint32_t)p.L.data_token_stride;
     p.scale_token = (uint32_t)p.L.scale_token_stride;
     p.row_tile = row_tile;
-    const int64_t units = (int64_t)p.tiles * p.splits;
+    const int64_t units = p.units;
     const bool join = p.splits > 1;
     const hipError_t e = launch_span(kernel, (units + 7) / 8 * 8 * p.hk, waves * kWave, s, true, !join, p);
     if (e != hipSuccess || !join) return e;

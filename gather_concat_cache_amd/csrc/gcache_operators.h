@@ -35,17 +35,20 @@ struct AttnParams {
     int64_t mask_ts;
     int32_t mask_cols;
     int32_t tiles;               // row tiles of one kv head (upper bound)
-    int32_t splits, chunk;       // key splits (upper bound), 32-key tiles in each
+    int32_t units;               // work units of one kv head (>= tiles)
+    int32_t splits;              // key splits of a request (upper bound)
+    int32_t key_tiles;           // 32-key tiles that a row tile sees (bound from max_seq_len and the window)
     float* ws_o;                 // [splits, total_q * hq, dv]
     float* ws_ml;                // [splits, total_q * hq, 2]
+    int32_t* ws_chunk;           // [1] key tiles of a split, from the attention kernel to the join
     int32_t row_tile;            // rows of a row tile (set by the launcher, for the join)
 };
 
-// Rows per workgroup (16, 32 or 64) and key splits of a call; filled by
-// plan_attention from sizes that the host knows.
+// Rows per workgroup (16 to 128), work units and key splits of a call; filled
+// by plan_attention from sizes that the host knows.
 struct AttnPlan {
     int32_t row_tiles;           // 16-row tiles per workgroup
-    int32_t tiles, splits, chunk;
+    int32_t tiles, units, splits, key_tiles;
     int64_t ws_floats;           // workspace of that many splits
 };
 AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t dp, int32_t dv,

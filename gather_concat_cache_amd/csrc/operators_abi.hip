@@ -104,10 +104,13 @@ AttnPlan set_plan(const gcache_attention_args* a, int dp, AttnParams* p) {
     const AttnPlan plan = plan_attention(p->total_q, p->batch, p->hq, p->hk, dp, p->hs, a->max_seq_len, p->window,
                                          p->sinks, have);
     p->tiles = plan.tiles;
+    p->units = plan.units;
     p->splits = plan.splits;
-    p->chunk = plan.chunk;
+    p->key_tiles = plan.key_tiles;
     p->ws_o = static_cast<float*>(a->workspace);
-    p->ws_ml = p->ws_o ? p->ws_o + (int64_t)plan.splits * p->total_q * p->hq * p->hs : nullptr;
+    const int64_t rows = (int64_t)plan.splits * p->total_q * p->hq;
+    p->ws_ml = p->ws_o ? p->ws_o + rows * p->hs : nullptr;
+    p->ws_chunk = p->ws_o ? reinterpret_cast<int32_t*>(p->ws_ml + 2 * rows) : nullptr;
     return plan;
 }
 
