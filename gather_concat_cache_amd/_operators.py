@@ -261,6 +261,9 @@ def _attention(fn, extra, q, dk, dv, hk, num_blocks, block_size, block_table, qu
     return (out, lse) if return_lse else out
 
 
+_NO_COLUMNS = 16                 # stands for a mask that no byte of is read
+
+
 def _tree_mask(mask, T, dev):
     if not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.bool, _U8):
         raise TypeError("tree_mask must be a bool or uint8 tensor")
@@ -271,8 +274,8 @@ def _tree_mask(mask, T, dev):
     row, unit = mask.stride()
     if (cols > 1 and unit != 1) or (T > 1 and row < cols):
         raise ValueError("tree_mask must be [T, columns] with unit last stride and rows that do not overlap")
-    # a mask without columns or rows has no memory; the library wants a pointer
-    return mask.data_ptr() or None, max(row, cols), cols
+    # a mask without columns has no memory, and no pointer would mean a chain
+    return mask.data_ptr() or _NO_COLUMNS, max(row, cols), cols
 
 
 _split_layout = functools.lru_cache(maxsize=64)(nvfp4_kv_split_layout)     # of sizes; not handed out

@@ -372,6 +372,106 @@ def test_mla_key_split(g, longest):
     check_mla(g, rng, batch, 16, max_seq_len=longest)
 
 
+def test_tree_mask_without_columns(g):
+    """A mask of no columns hides every drafted token: rows see the context
+    alone, and nothing at all without one."""
+    rng = np.random.default_rng(14)
+    batch = Batch(rng, [3, 2, 40], [50, 2, 100], 16)
+    none = np.zeros((batch.T, 0), bool)
+    out, lse = check_kv(g, rng, batch, 1, 2, 64, mask=none)
+    assert (out[3:5] == 0).all() and torch.isneginf(lse[3:5]).all()
+    check_mla(g, rng, batch, 4, mask=none)
+
+
+# The kernels count the requests of a batch over 64 lanes: one a lane, several a
+# lane, and (over 4096) by the packed rows alone.
+@pytest.mark.parametrize("requests", [64, 65, 200, 1025, 4096, 4097])
+def test_many_requests(g, requests):
+    """Ragged batches with requests without queries, and keys, in between."""
+    rng = np.random.default_rng(requests)
+    qlens = rng.choice([0, 1, 1, 2, 9], requests)
+    lens = qlens + rng.choice([0, 0, 1, 5], requests) - (rng.random(requests) < 0.1)
+    batch = Batch(rng, qlens.tolist(), np.maximum(lens, 0).tolist(), 16)
+    check_kv(g, rng, batch, 1, 3, 16, window=4, sinks=1)
+    if requests < 1000:
+        check_mla(g, rng, batch, 5)
+
+
+@pytest.mark.parametrize("requests,qlen", [(3, 2), (70, 1), (130, 1), (5, 20), (4, 40)])
+@pytest.mark.parametrize("hs", [64, 576])
+def test_key_split_of_uneven_batches(g, requests, qlen, hs):
+    """One long request among short ones: splits are sized by the batch's work,
+    so it is split further than a batch of its length would be."""
+    rng = np.random.default_rng(requests)
+    lens = rng.integers(qlen, 60, requests)
+    lens[requests // 2] = 1900
+    batch = Batch(rng, [qlen] * requests, lens.tolist(), 16)
+    if hs == 576:
+        check_mla(g, rng, batch, 3)
+    else:
+        check_kv(g, rng, batch, 1, 2, hs)
+
+
+@pytest.mark.parametrize("qlen,window,sinks", [(1, 500, 70), (40, 300, 70), (70, 333, 33), (129, 64, 100)])
+def test_sinks_and_window_split(g, qlen, window, sinks):
+    """Odd numbers of sink tiles before a window that is split over workgroups."""
+    rng = np.random.default_rng(qlen)
+    batch = Batch(rng, [qlen, 1], [900, 700], 16)
+    check_kv(g, rng, batch, 1, 2, 128, window=window, sinks=sinks)
+
+
+def test_rows_of_infinities_and_nan(g):
+    """A query row that holds NaN or an infinity spoils its own output only."""
+    rng = np.random.default_rng(15)
+    batch = Batch(rng, [12], [300], 16)
+    _, cache, L = kv_cache(g, rng, batch, 1, 64, "split")
+    q, _ = queries(rng, batch.T, 4, 64)
+    bt, starts, lens = batch.metadata()
+    one = torch.ones(1, device="cuda")
+    call = lambda x: g.attention_nvfp4_kv(x, cache, one, one, bt, starts, lens, 300, 0.1)        # noqa: E731
+    want, bad = call(q), q.clone()
+    bad[3, 1, 5], bad[7, 0, 0], bad[8, 2, 63] = float("nan"), float("inf"), -float("inf")
+    got = call(bad)
+    keep = torch.ones(12, 4, dtype=torch.bool, device="cuda")
+    keep[3, 1] = keep[7, 0] = keep[8, 2] = False
+    assert torch.equal(got[keep], want[keep])
+
+
+def test_lengths_that_grow_under_a_graph(g):
+    """A captured call follows the lengths and block tables of each replay, up
+    to its max_seq_len, and two captured calls keep their own scratch."""
+    rng = np.random.default_rng(16)
+    batch = Batch(rng, [1, 1, 2], [2000, 1500, 700], 16)
+    _, cache, L = kv_cache(g, rng, batch, 1, 128, "split")
+    flat = torch.randint(0, 0x38, (batch.nb, 16, 352), dtype=torch.uint8, device="cuda")
+    q, _ = queries(rng, batch.T, 8, 128)
+    ql, _ = queries(rng, batch.T, 16, 576)
+    bt, starts, full = batch.metadata()
+    one = torch.ones(1, device="cuda")
+    lens = full.clone()
+
+    def both():
+        return (g.attention_nvfp4_kv(q, cache, one, one, bt, starts, lens, 2000, 0.09),
+                g.tree_attention_nvfp4_ds_mla(ql, flat, bt, starts, lens, None, 2000, 0.07))
+
+    both()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(both())
+        graphs.append(graph)
+    for now in ([2000, 1500, 700], [3, 1, 2], [1, 900, 2], [0, 0, 0], [1999, 33, 700]):
+        lens.copy_(dev(np.array(now, np.int32)))
+        want = both()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1]), now
+
+
 def test_offsets_past_32_bits(g):
     """Pages that start beyond 4 GiB of the cache."""
     rng = np.random.default_rng(21)
@@ -480,6 +580,23 @@ def test_fork_extend_free_compact(g, rows, nb, bs, stride, layers, page):
                         lambda t, l, r, c: ref.free(t, l, r, gone, bs), state, caches)
     check_pages(lambda t, l, r, c: g.compact_pages(c, bs, t, l, r),
                 lambda t, l, r, c: ref.compact(t, l, r, bs, c), state, caches)
+
+
+@pytest.mark.parametrize("n", [1024, 1025, 5000])
+def test_many_grants(g, n):
+    """Calls of more requests than one workgroup's: duplicates and rows that are
+    taken among them, free pages for some."""
+    rng = np.random.default_rng(n)
+    rows, nb, bs, stride = 3 * n // 2, 2 * n, 8, 3
+    state = random_state(rng, rows, nb, bs, stride)
+    caches = [rng.integers(0, 256, (nb, 24), dtype=np.uint8)]
+    parents, children = (rng.integers(-1, rows + 1, n).astype(np.int32) for _ in range(2))
+    state = check_pages(lambda t, l, r, c: g.fork_requests(c, bs, t, l, r, dev(parents), dev(children)),
+                        lambda t, l, r, c: ref.fork(t, l, r, parents, children, bs, c), state, caches)
+    which = rng.integers(-1, rows + 1, n).astype(np.int32)
+    new = (state[1][np.clip(which, 0, rows - 1)] + rng.integers(0, 2 * bs, n)).astype(np.int32)
+    check_pages(lambda t, l, r, c: g.extend_requests(bs, t, l, r, dev(which), dev(new)),
+                lambda t, l, r, c: ref.extend(t, l, r, which, new, bs), state, caches)
 
 
 @pytest.mark.parametrize("live", ["none", "all", "low", "high"])
