@@ -162,31 +162,40 @@ __device__ __forceinline__ int request_splits(int work, int chunk) { return max(
 // last to the first: causal tiles grow along a request, and the longest start
 // first.  The split is rotated by the request, or the short last splits of
 // equal requests would share an XCD.
-// (With a fixed split size and row tiles numbered by a bound, every second
-// number was unused for requests of one full tile; workgroups go to XCDs and
-// their shader engines round robin, and half of the engines had no work.)
-// Batches over kDenseBatch requests are numbered by that bound; they are not split.
-constexpr int kDenseBatch = kWave * kWave;
+// The count costs each workgroup a load for every 64 requests.  Batches with
+// many requests and heads are not split, and their row tiles are numbered by a
+// bound, which leaves unused numbers at even distances (every second one for
+// requests of one full tile: workgroups go to XCDs and their shader engines
+// round robin, and half of the engines have no work).  Counted against numbered:
+//   128 x 1 token, 16 heads, 2048 latent keys        51 us against 73
+//   512 x 1 token, 16 heads, 512 latent keys         39 against 52
+//   1024 x 1 token, 16 heads, 256 latent keys        59 against 53
+//   256 x 32 tokens, 8 kv heads, 512 per-head keys  135 against 149
+//   512 x 1 token, 8 kv heads, 256 per-head keys     64 against 55
+__host__ __device__ __forceinline__ bool counts_requests(int batch, int kv_heads) {
+    return batch <= 256 || (batch <= 512 && batch * kv_heads <= 512);
+}
 __device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int RT, RowTile& t) {
     const int lane = lane_id();
     const auto tiles_of = [&](int rows) { return (max(rows, 0) + RT - 1) / RT; };
     int index, before;
     t.splits = 1;
     t.chunk = INT32_MAX;
-    if (p.batch <= kDenseBatch) {
+    if (counts_requests(p.batch, p.hk)) {
         const bool split = p.splits > 1;
         const int per = (p.batch + kWave - 1) / kWave;
-        const int b0 = min(lane * per, p.batch), b1 = min(b0 + per, p.batch);
-        const int q_first = query_start(p, b0), q_last = query_start(p, b1);
-        const int tiles1 = b0 < b1 ? tiles_of((q_last - q_first) * p.group) : 0;    // where a lane has one request
-        const int work1 = split && b0 < b1 ? request_work(p, b0) : 0;
+        const int b0 = lane * per;                       // requests behind the last have no rows
+        const int q_first = query_start(p, min(b0, p.batch)), q_last = query_start(p, min(b0 + 1, p.batch));
+        const int tiles1 = tiles_of((q_last - q_first) * p.group);                  // where a lane has one request
+        const int work1 = split ? request_work(p, min(b0, p.batch - 1)) : 0;
         const auto sum = [&](auto of) {                  // of(row tiles, work) over the lane's requests
             if (per == 1) return of(tiles1, work1);
             decltype(of(0, 0)) n = 0;
             int q = q_first;
-            for (int b = b0; b < b1; b++) {
-                const int next = query_start(p, b + 1);
-                n += of(tiles_of((next - q) * p.group), split ? request_work(p, b) : 0);
+#pragma unroll 4
+            for (int i = 0; i < per; i++) {
+                const int next = query_start(p, min(b0 + i + 1, p.batch));
+                n += of(tiles_of((next - q) * p.group), split ? request_work(p, min(b0 + i, p.batch - 1)) : 0);
                 q = next;
             }
             return n;

@@ -8,9 +8,6 @@ namespace gcache {
 // maxima and sums are read by a lane each and reduced across the wave; the
 // weighted rows follow with four loads in flight.
 constexpr int kMaxSplits = 256;
-// Larger batches are not split: each workgroup counts their requests (and 1024
-// requests fill the device once or more).
-constexpr int kSplitBatch = 1024;
 
 __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, int64_t wg0) {
     __shared__ float s_w[kWavesPerBlock][kMaxSplits];
@@ -129,7 +126,7 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     if (top > room) top = room;
     int64_t most = top;
     if (most > 8 * slots / groups) most = 8 * slots / groups;   // eight rounds are even enough
-    if (batch > kSplitBatch) most = 1;
+    if (!counts_requests(batch, hk)) most = 1;
     int64_t splits = 1, best = cost_of(groups, kt) + kt / 2;
     for (int64_t n = 2; n <= most; n += n < 16 ? 1 : n / 16) {
         const int64_t c = ((kt + n - 1) / n + 3) / 4 * 4, m = (kt + c - 1) / c;

@@ -384,15 +384,15 @@ def test_tree_mask_without_columns(g):
 
 
 # The kernels count the requests of a batch over 64 lanes: one a lane, several a
-# lane, and (over 4096) by the packed rows alone.
-@pytest.mark.parametrize("requests", [64, 65, 200, 1025, 4096, 4097])
+# lane, and, in large batches, by the packed rows alone.
+@pytest.mark.parametrize("requests", [64, 65, 200, 256, 257, 512, 513, 1025, 4097])
 def test_many_requests(g, requests):
     """Ragged batches with requests without queries, and keys, in between."""
     rng = np.random.default_rng(requests)
     qlens = rng.choice([0, 1, 1, 2, 9], requests)
     lens = qlens + rng.choice([0, 0, 1, 5], requests) - (rng.random(requests) < 0.1)
     batch = Batch(rng, qlens.tolist(), np.maximum(lens, 0).tolist(), 16)
-    check_kv(g, rng, batch, 1, 3, 16, window=4, sinks=1)
+    check_kv(g, rng, batch, 1 + (requests == 257), 3, 16, window=4, sinks=1)
     if requests < 1000:
         check_mla(g, rng, batch, 5)
 
