@@ -1,7 +1,7 @@
 // attention_ds_mla.hip -- tree attention over the nvfp4_ds_mla cache in
 // absorbed form (scores over 576 values of an entry, values are its first
 // 512): the few-rows kernel, and the kernel for many query rows.
-#include "attention_few.h"
+#include "attention_device.h"
 
 namespace gcache {
 

@@ -14,11 +14,10 @@ constexpr int kFewWaves = 4;
 
 // Cache bytes of one 32-key tile as a lane needs them: its quarter of K rows
 // lane % 16 and 16 + lane % 16; its DP / 16 dims of eight V rows.
-template <int DP, bool MLA>
+template <int DP>
 struct RawK {
     static constexpr int W = DP / 32;                    // data words of a quarter row
-    static constexpr int SW = DP > 256 ? 2 : 1;          // words holding its DP / 64 scales
-    uint32_t k[2][W], s[2][SW], rope[2][MLA ? 4 : 1];
+    uint32_t k[2][W], s[2];                              // and a word with its DP / 64 scales
 };
 template <int DP>
 struct RawV {
@@ -28,20 +27,19 @@ struct RawV {
 
 template <bool UNI>
 struct LaneParts {               // 32-bit offsets of the lane's parts of rows
-    uint32_t kd, ks, rope, vd[4], vs[4];
+    uint32_t kd, ks, vd[4], vs[4];
 };
 // UNI kernels take head sizes of exactly DP; the others take any up to DP:
 // dims behind head_size read the row's first bytes with a zero scale.
-template <int DP, bool MLA, bool UNI>
+template <int DP, bool UNI>
 __device__ __forceinline__ LaneParts<UNI> lane_parts(const AttnParams& p, int kvh, int lane) {
     const int c = lane & 15, g = lane >> 4;
     const uint32_t hd = (uint32_t)(kvh * p.L.data_head_stride), hs = (uint32_t)(kvh * p.L.scale_head_stride);
     const uint32_t side = (uint32_t)p.L.side_stride;
-    const bool in = UNI || MLA || (DP / 16) * c < p.hs;
+    const bool in = UNI || (DP / 16) * c < p.hs;
     LaneParts<UNI> o;
     o.kd = data_part<UNI>(p, c, hd + (DP / 8) * g);
     o.ks = scale_part<UNI>(p, c, hs + (DP / 64) * g);
-    o.rope = MLA ? data_part<UNI>(p, c, kNvRopeOff + 16 * g) : 0;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         o.vd[j] = data_part<UNI>(p, 4 * g + j, side + hd + (in ? (DP / 32) * c : 0));
@@ -51,12 +49,12 @@ __device__ __forceinline__ LaneParts<UNI> lane_parts(const AttnParams& p, int kv
 }
 
 // One key's quarter row: DP / 32 data words and the DP / 64 scales.
-template <int DP, bool MLA, bool UNI>
+template <int DP, bool UNI>
 __device__ __forceinline__ void load_k_row(const AttnParams& p, const RowBytes& b, const LaneParts<UNI>& lo, int g,
                                            uint32_t* k, uint32_t* sc) {
     constexpr int KB = DP / 8;                           // data bytes
     const uint8_t *kd = b.d + lo.kd, *sd = b.s + lo.ks;
-    if (UNI || MLA) {
+    if (UNI) {
         if (KB == 8) {
             const u32x2 w = *reinterpret_cast<const u32x2_a8*>(kd);
             k[0] = w.x;
@@ -72,11 +70,6 @@ __device__ __forceinline__ void load_k_row(const AttnParams& p, const RowBytes& 
         if (DP == 64) sc[0] = *sd;
         if (DP == 128) sc[0] = *reinterpret_cast<const u16_a1*>(sd);
         if (DP == 256) sc[0] = *reinterpret_cast<const u32_a1*>(sd);
-        if (DP == 512) {
-            const u32x2 w = *reinterpret_cast<const u32x2*>(sd);
-            sc[0] = w.x;
-            sc[DP == 512 ? 1 : 0] = w.y;
-        }
     } else {                                             // units of 16 dims
         uint32_t x = 0;
 #pragma unroll
@@ -92,26 +85,21 @@ __device__ __forceinline__ void load_k_row(const AttnParams& p, const RowBytes& 
     }
 }
 
-template <int DP, bool MLA, bool UNI>
+template <int DP, bool UNI>
 __device__ __forceinline__ void load_k(const AttnParams& p, const KeyPages& pg, const RowBytes* gb, const LaneParts<UNI>& lo,
-                                       int lane, RawK<DP, MLA>& r) {
+                                       int lane, RawK<DP>& r) {
 #pragma unroll
     for (int t = 0; t < 2; t++) {
         const RowBytes b = UNI ? gb[t] : row_bytes<UNI>(p, pg, t, lane & 15);
-        load_k_row<DP, MLA, UNI>(p, b, lo, lane >> 4, r.k[t], r.s[t]);
-        if (MLA) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(b.d + lo.rope);
-#pragma unroll
-            for (int i = 0; i < 4; i++) r.rope[t][i % (MLA ? 4 : 1)] = w[i];
-        }
+        load_k_row<DP, UNI>(p, b, lo, lane >> 4, r.k[t], &r.s[t]);
     }
 }
 
-template <int DP, bool MLA, bool UNI>
+template <int DP, bool UNI>
 __device__ __forceinline__ void load_v(const AttnParams& p, const KeyPages& pg, const RowBytes* gb, const LaneParts<UNI>& lo,
                                        int lane, RawV<DP>& r) {
     const int c = lane & 15, g = lane >> 4;
-    const bool in = UNI || MLA || (DP / 16) * c < p.hs;
+    const bool in = UNI || (DP / 16) * c < p.hs;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         const RowBytes b = UNI ? gb[j >> 2] : row_bytes<UNI>(p, pg, j >> 2, 4 * g + (j & 3));
@@ -123,21 +111,14 @@ __device__ __forceinline__ void load_v(const AttnParams& p, const KeyPages& pg, 
             r.v[j][0] = w.x;
             r.v[j][RawV<DP>::W > 1 ? 1 : 0] = w.y;
         }
-        if (DP == 512) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(vd);
-#pragma unroll
-            for (int i = 0; i < 4; i++) r.v[j][i % RawV<DP>::W] = w[i];
-        }
-        const uint32_t x = DP == 512 ? (uint32_t)*reinterpret_cast<const uint16_t*>(sd) : (uint32_t)*sd;
-        r.s[j] = in ? x : 0u;
+        r.s[j] = in ? *sd : 0u;
     }
 }
 
-template <int DP, bool MLA, int R, bool UNI, bool TREE>
+template <int DP, int R, bool UNI, bool TREE>
 __global__ __launch_bounds__(kFewWaves * kWave, R * DP <= 128 ? 3 : R * DP <= 256 ? 2 : 1)
 void k_attention_few(AttnParams p, int64_t wg0) {
     constexpr int KS = DP / 32;                          // head-dim steps of the first product
-    constexpr int RS = MLA ? 2 : 0;                      // RoPE steps
     constexpr int DT = DP / 16;                          // 16-dim tiles of the output
     constexpr int DW = DT < 8 ? DT : 8;                  // dims of a V word
     constexpr int RT = 16 * R;
@@ -161,11 +142,11 @@ void k_attention_few(AttnParams p, int64_t wg0) {
     const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
     const auto tile_key = [&](int v) { return (v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0) * kTileKeys; };
     const auto look_up = [&](int v) { return find_pages<UNI, kTileKeys>(p, bt_row, tile_key(v < v1 ? v : v0), lane); };
-    const LaneParts<UNI> lo = lane_parts<DP, MLA, UNI>(p, kvh, lane);
+    const LaneParts<UNI> lo = lane_parts<DP, UNI>(p, kvh, lane);
 
     // Loads return in order: page ids are asked for before the bytes of the
     // tile ahead, so waiting for ids leaves bytes in flight.
-    RawK<DP, MLA> rk;
+    RawK<DP> rk;
     RawV<DP> rv;
     KeyPages pg, pg_next;
     int v = v0 + w;
@@ -173,15 +154,15 @@ void k_attention_few(AttnParams p, int64_t wg0) {
         pg = look_up(v);
         pg_next = look_up(v + kFewWaves);
         const RowBytes gb[2] = {group_bytes<UNI>(p, pg, 0), group_bytes<UNI>(p, pg, 1)};
-        load_k<DP, MLA, UNI>(p, pg, gb, lo, lane, rk);
-        load_v<DP, MLA, UNI>(p, pg, gb, lo, lane, rv);
+        load_k<DP, UNI>(p, pg, gb, lo, lane, rk);
+        load_v<DP, UNI>(p, pg, gb, lo, lane, rv);
     }
 
-    f16x8 q[R][KS + RS];
+    f16x8 q[R][KS];
     float fac[R];
     int pos[R], tok[R];
 #pragma unroll
-    for (int r = 0; r < R; r++) load_query<DP, MLA>(p, t, kvh, 16 * r, lane, q[r], fac[r], pos[r], tok[r]);
+    for (int r = 0; r < R; r++) load_query<DP, false>(p, t, kvh, 16 * r, lane, q[r], fac[r], pos[r], tok[r]);
     const int pos_lo = t.ctx + t.row0 / p.group, pos_hi = t.ctx + (t.row0 + t.rows - 1) / p.group;
 
     f32x4 o[R][DT];
@@ -204,28 +185,14 @@ void k_attention_few(AttnParams p, int64_t wg0) {
         for (int kk = 0; kk < 2; kk++) {
 #pragma unroll
             for (int r = 0; r < R; r++) s[r][kk] = f32x4{0, 0, 0, 0};
-            f16x2 sc[RawK<DP, MLA>::SW * 4];
-#pragma unroll
-            for (int i = 0; i < RawK<DP, MLA>::SW; i++) {
-                const uint32_t x = drop_nan_e4m3x4(rk.s[kk][i]);
-                const f16x2 a = e4m3x2_f16<false>(x), b = e4m3x2_f16<true>(x);
-                sc[4 * i] = f16x2{a.x, a.x};
-                sc[4 * i + 1] = f16x2{a.y, a.y};
-                sc[4 * i + 2] = f16x2{b.x, b.x};
-                sc[4 * i + 3] = f16x2{b.y, b.y};
-            }
+            const uint32_t x = drop_nan_e4m3x4(rk.s[kk]);
+            const f16x2 x0 = e4m3x2_f16<false>(x), x1 = e4m3x2_f16<true>(x);
+            const f16x2 sc[4] = {{x0.x, x0.x}, {x0.y, x0.y}, {x1.x, x1.x}, {x1.y, x1.y}};
 #pragma unroll
             for (int st = 0; st < KS; st++) {
                 const f16x8 a = k_operand(rk.k[kk][st], sc[st / 2]);
 #pragma unroll
                 for (int r = 0; r < R; r++) s[r][kk] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][st], s[r][kk], 0, 0, 0);
-            }
-#pragma unroll
-            for (int st = 0; st < RS; st++) {
-                const f16x8 a = rope_operand(rk.rope[kk][2 * st], rk.rope[kk][2 * st + 1]);
-#pragma unroll
-                for (int r = 0; r < R; r++)
-                    s[r][kk] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][KS + st], s[r][kk], 0, 0, 0);
             }
         }
         // ---- the next tile's K takes the registers just used
@@ -235,7 +202,7 @@ void k_attention_few(AttnParams p, int64_t wg0) {
             pg_next = look_up(v + 2 * kFewWaves);
             gb[0] = group_bytes<UNI>(p, pg, 0);
             gb[1] = group_bytes<UNI>(p, pg, 1);
-            load_k<DP, MLA, UNI>(p, pg, gb, lo, lane, rk);
+            load_k<DP, UNI>(p, pg, gb, lo, lane, rk);
         }
         // ---- logits, mask
         const bool all = live == 0xFFu && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kTileKeys);
@@ -281,48 +248,36 @@ void k_attention_few(AttnParams p, int64_t wg0) {
             l[r] += sum;
         }
         // ---- O^T += V^T P^T
-        f16x2 vsc[DP == 512 ? 2 : 1][4];
-        if (DP == 512) {                                 // the lane's dims span two blocks
-            uint32_t lo8[8], hi8[8];
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                lo8[j] = rv.s[j] & 0xFF;
-                hi8[j] = rv.s[j] >> 8;
-            }
-            v_scales(lo8, vsc[0]);
-            v_scales(hi8, vsc[DP == 512 ? 1 : 0]);
-        } else {
-            v_scales(rv.s, vsc[0]);
-        }
+        f16x2 vsc[4];
+        v_scales(rv.s, vsc);
 #pragma unroll
         for (int vw = 0; vw < RawV<DP>::W; vw++) {
             uint32_t word[8];
 #pragma unroll
             for (int j = 0; j < 8; j++) word[j] = rv.v[j][vw];
             const PairedCodes x = pair_codes(word);
-            const f16x2* sc = vsc[DP == 512 ? vw / 2 : 0];
             const auto mul = [&](int d, const f16x8& a) {
 #pragma unroll
                 for (int r = 0; r < R; r++)
                     o[r][8 * vw + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw[r], o[r][8 * vw + d], 0, 0, 0);
             };
-            mul(0, v_operand<0>(x, sc));
-            mul(1, v_operand<1>(x, sc));
-            mul(2, v_operand<2>(x, sc));
-            mul(3, v_operand<3>(x, sc));
+            mul(0, v_operand<0>(x, vsc));
+            mul(1, v_operand<1>(x, vsc));
+            mul(2, v_operand<2>(x, vsc));
+            mul(3, v_operand<3>(x, vsc));
             if (DW > 4) {
-                mul(4 % DT, v_operand<4>(x, sc));
-                mul(5 % DT, v_operand<5>(x, sc));
-                mul(6 % DT, v_operand<6>(x, sc));
-                mul(7 % DT, v_operand<7>(x, sc));
+                mul(4 % DT, v_operand<4>(x, vsc));
+                mul(5 % DT, v_operand<5>(x, vsc));
+                mul(6 % DT, v_operand<6>(x, vsc));
+                mul(7 % DT, v_operand<7>(x, vsc));
             }
         }
-        if (more) load_v<DP, MLA, UNI>(p, pg, gb, lo, lane, rv);
+        if (more) load_v<DP, UNI>(p, pg, gb, lo, lane, rv);
     }
 
     // ---- join the four waves, 16 rows and 16 * DW dims at a time
     const bool partial = p.splits > 1 && t.total > t.chunk;
-    const float gv = MLA ? 1.0f : *p.gscale[1];
+    const float gv = *p.gscale[1];
     const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;   // the row and dim column this thread writes
 #pragma unroll
     for (int r = 0; r < R; r++) {
@@ -377,7 +332,7 @@ void k_attention_few(AttnParams p, int64_t wg0) {
 #pragma unroll
                 for (int d = 0; d < DW; d++) acc[d] = __builtin_fmaf(wt[k], s_o[k][jr][jc * DW + d], acc[d]);
             const int dim = jc * DT + ch * DW;
-            if (in && (MLA || dim < p.hs)) {
+            if (in && dim < p.hs) {
                 if (partial) {
                     float* dst = p.ws_o + ((int64_t)t.split * p.total_q * p.hq + id) * p.hs + dim;
 #pragma unroll
@@ -397,12 +352,12 @@ void k_attention_few(AttnParams p, int64_t wg0) {
     }
 }
 
-template <int DP, bool MLA, int R>
+template <int DP, int R>
 hipError_t launch_few(const AttnParams& p, hipStream_t s) {
     const bool uni = uniform_pages(p) && p.hs == DP;
     return launch_attention_parts(
-        p.mask ? (uni ? k_attention_few<DP, MLA, R, true, true> : k_attention_few<DP, MLA, R, false, true>)
-               : (uni ? k_attention_few<DP, MLA, R, true, false> : k_attention_few<DP, MLA, R, false, false>),
+        p.mask ? (uni ? k_attention_few<DP, R, true, true> : k_attention_few<DP, R, false, true>)
+               : (uni ? k_attention_few<DP, R, true, false> : k_attention_few<DP, R, false, false>),
         kFewWaves, 16 * R, p, s);
 }
 

@@ -13,7 +13,7 @@ namespace gcache {
 // i + 2's bytes are in flight.  Against dequantizing in every wave this takes
 // the converters' share of the vector instructions from 58 to 25 per cent.
 // ---------------------------------------------------------------------------
-constexpr int kStepKeys = 64, kRowsWaves = 4, kRowsR = 2;
+constexpr int kStepKeys = 64, kRowsWaves = 4, kRowsTile = 128;
 
 template <int DP>
 struct Share {
@@ -35,7 +35,7 @@ __device__ __forceinline__ void load_share(const AttnParams& p, const KeyPages& 
     const int vh = w & 2;                                // V's first group
     const RowBytes gb[2] = {group_bytes<UNI>(p, pg, vh), group_bytes<UNI>(p, pg, vh + 1)};
     const RowBytes kb = UNI ? RowBytes{w & 1 ? gb[1].d : gb[0].d, w & 1 ? gb[1].s : gb[0].s} : row_bytes<UNI>(p, pg, w, c);
-    load_k_row<DP, false, UNI>(p, kb, lo, g, r.k, &r.ks);
+    load_k_row<DP, UNI>(p, kb, lo, g, r.k, &r.ks);
     const bool in = UNI || (DP / 16) * c < p.hs;
     const uint32_t half = (w & 1) * (DP / 64);           // bytes: half of the lane's DP / 32
 #pragma unroll
@@ -76,23 +76,13 @@ __device__ __forceinline__ void convert_share(const Share<DP>& r, int lane, int 
     }
 }
 
+// One tile of up to 64 R rows: wave w takes 16 R of them.
 template <int DP, int R, bool UNI, bool TREE>
-__global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_attention_rows(AttnParams p, int64_t wg0) {
+__device__ __forceinline__ void attend_rows(const AttnParams& p, const RowTile& t, int kvh, int v0, int v1,
+                                            f16x8 (*s_frag)[(Share<DP>::KF + Share<DP>::VF) * kWave]) {
     typedef Share<DP> S;
     constexpr int KS = S::KS, DT = S::DT;
-    constexpr int RT = kRowsWaves * 16 * R;
     constexpr int kDepth = 4;                            // fragments in flight from LDS
-    __shared__ f16x8 s_frag[2][(S::KF + S::VF) * kWave];
-
-    const int64_t wg = wg0 + blockIdx.x;
-    const int64_t per = 8 * (int64_t)p.hk;
-    const int rem = (int)(wg % per);
-    const int64_t unit = wg / per * 8 + rem % 8;
-    const int kvh = rem / 8;
-    RowTile t;
-    if (!find_tile(p, unit, RT, t)) return;
-    int v0, v1;                                    // 32-key tiles; an even number but for the last split
-    if (!key_range(t, v0, v1)) return;
 
     const int lane = lane_id(), w = wave_id();
     const int c = lane & 15, g = lane >> 4;
@@ -109,15 +99,17 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
     const int pos_lo = t.ctx + row_a / p.group, pos_hi = t.ctx + row_b / p.group;   // of the wave's rows
 
     f32x4 o[R][DT];
-    float m[R], l[R];
+    // weights are exp2(s + sub), sub = kShift - m (0 before the first visible key); a tile whose largest
+    // exponent passes lim moves m
+    float m[R], l[R], sub[R], lim[R];
 #pragma unroll
     for (int r = 0; r < R; r++) {
-        m[r] = kNegInf;
-        l[r] = 0.0f;
+        m[r] = lim[r] = kNegInf;
+        l[r] = sub[r] = 0.0f;
 #pragma unroll
         for (int d = 0; d < DT; d++) o[r][d] = f32x4{0, 0, 0, 0};
     }
-    const LaneParts<UNI> lo = lane_parts<DP, false, UNI>(p, kvh, lane);
+    const LaneParts<UNI> lo = lane_parts<DP, UNI>(p, kvh, lane);
     // Steps of 64 keys: the tiles [v0, v1) are runs of sink tiles and window
     // tiles; a step covers two consecutive tile numbers of one run.  Keys of a
     // step behind its run (or behind v1) are hidden by `end`.
@@ -169,7 +161,9 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
 #pragma unroll
             for (int r = 0; r < R; r++)
 #pragma unroll
-                for (int kt = 0; kt < 4; kt++) s[r][kt] *= fac[r];
+                for (int kt = 0; kt < 4; kt++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) s[r][kt][i] = __builtin_fmaf(s[r][kt][i], fac[r], sub[r]);
             if (!__all(all)) {
 #pragma unroll
                 for (int r = 0; r < R; r++) hide<TREE, 4>(p, t, pos[r], tok[r], key0 + 4 * g, lv, s[r]);
@@ -179,15 +173,21 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
 #pragma unroll
             for (int r = 0; r < R; r++) {
                 top[r] = group_max(fmaxf(max8(s[r][0], s[r][1]), max8(s[r][2], s[r][3])));
-                late = late || top[r] > m[r] + kLag;
+                late = late || top[r] > lim[r];
             }
             if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first tiles
 #pragma unroll
                 for (int r = 0; r < R; r++) {
-                    const float mn = fmaxf(m[r], top[r]);
-                    const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
+                    const float mn = fmaxf(m[r], top[r] - sub[r]);
+                    const bool any = mn != kNegInf;
+                    const float al = any ? __builtin_amdgcn_exp2f(m[r] - mn) : 1.0f;
+                    const float to = any ? kShift - mn : 0.0f, by = to - sub[r];
                     m[r] = mn;
+                    sub[r] = to;
+                    lim[r] = any ? kShift + kLag : kNegInf;
                     l[r] *= al;
+#pragma unroll
+                    for (int kt = 0; kt < 4; kt++) s[r][kt] += by;
 #pragma unroll
                     for (int d = 0; d < DT; d++) o[r][d] *= al;
                 }
@@ -195,11 +195,10 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
             f16x8 pw[R][2];
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
                 float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 16; j++) {
-                    const float e = __builtin_amdgcn_exp2f(s[r][j >> 2][j & 3] + sub);
+                    const float e = __builtin_amdgcn_exp2f(s[r][j >> 2][j & 3]);
                     sum += e;
                     pw[r][j >> 3][j & 7] = (_Float16)e;
                 }
@@ -259,21 +258,39 @@ __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_atten
     }
 }
 
+// Tiles of up to 64 rows (a short request, or a request's last rows) do half of
+// the work a wave; the longer ones share each K and V fragment between two row
+// tiles.
+template <int DP, bool UNI, bool TREE>
+__global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_attention_rows(AttnParams p, int64_t wg0) {
+    __shared__ f16x8 s_frag[2][(Share<DP>::KF + Share<DP>::VF) * kWave];
+    const int64_t wg = wg0 + blockIdx.x;
+    const int64_t per = 8 * (int64_t)p.hk;
+    const int rem = (int)(wg % per);
+    const int64_t unit = wg / per * 8 + rem % 8;
+    const int kvh = rem / 8;
+    RowTile t;
+    if (!find_tile(p, unit, kRowsTile, t)) return;
+    int v0, v1;                                          // 32-key tiles; an even number but for the last split
+    if (!key_range(t, v0, v1)) return;
+    if (t.rows <= kRowsTile / 2) attend_rows<DP, 1, UNI, TREE>(p, t, kvh, v0, v1, s_frag);
+    else attend_rows<DP, 2, UNI, TREE>(p, t, kvh, v0, v1, s_frag);
+}
 
 template <int DP>
 static hipError_t launch_rows(const AttnParams& p, hipStream_t s) {
     const bool uni = uniform_pages(p) && p.hs == DP;
     return launch_attention_parts(
-        p.mask ? (uni ? k_attention_rows<DP, kRowsR, true, true> : k_attention_rows<DP, kRowsR, false, true>)
-               : (uni ? k_attention_rows<DP, kRowsR, true, false> : k_attention_rows<DP, kRowsR, false, false>),
-        kRowsWaves, 16 * kRowsR * kRowsWaves, p, s);
+        p.mask ? (uni ? k_attention_rows<DP, true, true> : k_attention_rows<DP, false, true>)
+               : (uni ? k_attention_rows<DP, true, false> : k_attention_rows<DP, false, false>),
+        kRowsWaves, kRowsTile, p, s);
 }
 
 hipError_t launch_attention_kv(const AttnParams& p, int row_tiles, hipStream_t s) {
-    if (p.hs <= 64) return row_tiles == 1 ? launch_few<64, false, 1>(p, s) : row_tiles == 2 ? launch_few<64, false, 2>(p, s) : launch_rows<64>(p, s);
+    if (p.hs <= 64) return row_tiles == 1 ? launch_few<64, 1>(p, s) : row_tiles == 2 ? launch_few<64, 2>(p, s) : launch_rows<64>(p, s);
     if (p.hs <= 128)
-        return row_tiles == 1 ? launch_few<128, false, 1>(p, s) : row_tiles == 2 ? launch_few<128, false, 2>(p, s) : launch_rows<128>(p, s);
-    return row_tiles == 1 ? launch_few<256, false, 1>(p, s) : launch_rows<256>(p, s);
+        return row_tiles == 1 ? launch_few<128, 1>(p, s) : row_tiles == 2 ? launch_few<128, 2>(p, s) : launch_rows<128>(p, s);
+    return row_tiles == 1 ? launch_few<256, 1>(p, s) : launch_rows<256>(p, s);
 }
 
 }  // namespace gcache
