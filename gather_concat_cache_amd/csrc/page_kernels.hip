@@ -219,7 +219,8 @@ __global__ __launch_bounds__(kBlockThreads) void k_extend_rows(GrantParams p, in
 }
 
 // One workgroup a listed row.  A row listed twice is freed once: each table
-// entry is taken by exchange.
+// entry is taken by exchange, and a workgroup that already reads length 0
+// leaves the row to the other, so nothing has to be ordered between the two.
 __global__ __launch_bounds__(kBlockThreads) void k_free_rows(PageTable t, const int32_t* rows, int32_t n) {
     const int row = rows[blockIdx.x];
     if (row < 0 || row >= t.num_rows) return;
@@ -230,8 +231,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_free_rows(PageTable t, const 
         const int id = atomicExch(&e[i], -1);
         if (id >= 0 && id < t.num_blocks && atomicAdd(&t.refs[id], -1) <= 0) atomicAdd(&t.refs[id], 1);
     }
-    __threadfence();
-    __syncthreads();
+    __syncthreads();                                     // every thread has read the length
     if (threadIdx.x == 0) __hip_atomic_store(&t.lens[row], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
