@@ -1,9 +1,11 @@
 // attention_few.h -- attention of few query rows (one token to a few drafted
 // ones): the four waves of a workgroup share 16 * R query rows, take every
 // fourth 32-key tile of the workgroup's key range straight into registers and
-// join through LDS.  Bound by HBM for long contexts (each wave has a tile's
-// bytes in flight while it works on another) and by the chain of dependent
-// loads for short ones.
+// join through LDS.  Bound by HBM for long contexts: each wave has a tile's
+// bytes in flight while it works on another (64 x 1 token over 8192 keys, 8
+// kv heads of 128: 169 us, 3.6 TB/s of the 4.85 that a large copy reaches); for
+// short ones by the chain of dependent loads and the launches (1038 keys: 8 us
+// and 5 for the join).
 #pragma once
 
 #include "attention_device.h"
@@ -29,8 +31,11 @@ template <bool UNI>
 struct LaneParts {               // 32-bit offsets of the lane's parts of rows
     uint32_t kd, ks, vd[4], vs[4];
 };
-// UNI kernels take head sizes of exactly DP; the others take any up to DP:
-// dims behind head_size read the row's first bytes with a zero scale.
+// UNI kernels take head sizes of exactly DP and pages of whole 16-key groups,
+// so that a group's address is wave-uniform; the others take any head size up
+// to DP (dims behind head_size read the row's first bytes with a zero scale)
+// and look up every key's page.  The general form on a UNI call: 64 x 1 token
+// over 8192 keys 240 us against 169, prefill 4 x 2048 975 against 512.
 template <int DP, bool UNI>
 __device__ __forceinline__ LaneParts<UNI> lane_parts(const AttnParams& p, int kvh, int lane) {
     const int c = lane & 15, g = lane >> 4;

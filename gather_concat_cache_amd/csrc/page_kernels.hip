@@ -93,7 +93,8 @@ __device__ __forceinline__ int64_t list_free(const GrantParams& p, int64_t want,
 // free pages for all of them.  FORK: a = parent rows, b = child rows; else a =
 // rows, b = new lengths.  Grants are decided in request order: request i is
 // granted when the pages of requests 0..i all fit the free ones.  Everything
-// stays in registers and LDS: three dependent memory round trips.
+// stays in registers and LDS: three dependent memory round trips (extending
+// and freeing 256 rows: 25 us, against 31 with the form below).
 template <bool FORK>
 __global__ __launch_bounds__(kPlanThreads) void k_grant_small(GrantParams p, int64_t) {
     __shared__ int64_t s_scan[kPlanWaves];
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_copy_pages(CopyParams p, int6
 // consecutive forks of one cache go to a workgroup, which reads a page once for
 // the forks of the same parent that follow each other: samples of one prompt
 // then cost one read and their writes (one 8-fold fork of 64 prompts over 32
-// caches: 83 us against 157 us with a read for every copy).
+// caches: 101 us against 174 us with a read for every copy).
 constexpr int kForkBlock = 8;
 struct ForkCopyParams {
     CacheList c;

@@ -8,12 +8,11 @@
 // Memory bound: 4 bytes moved a value.  A wave takes one token and several
 // of its heads, 8 values (16 bytes) a lane, so cos, sin and the weights are
 // loaded once for up to kHeadSets * 64 / lanes-per-head heads and all data
-// loads are in flight before the first is used.  Sums over a head's lanes and
-// the partner values of the half-split pairing (rot/2 away) come by lane
-// permutes inside the vector unit where the head has 16 lanes, the common
-// 128-value head rotated whole; the first form, with LDS-routed shuffles,
-// scalar table loads and IEEE division, took 120 us for 16384 tokens of 40
-// heads, this one 80 us (4.2 TB/s).
+// loads are in flight before the first is used.  Sums over a head's lanes come
+// by lane permutes inside the vector unit, the partner values of the half-split
+// pairing (rot/2 away) by one shuffle.  16384 tokens of 40 heads of 128 values,
+// data from HBM: 85 us (4.1 TB/s); the first form, with shuffles through LDS
+// for the sums, scalar table loads and IEEE division, 117 us.
 #include "gcache_operators.h"
 
 namespace gcache {
@@ -71,9 +70,8 @@ __device__ __forceinline__ void table_values(const void* row, int at, float* out
     }
 }
 
-// SH: log2 of the lanes of a head.  WHOLE: 16 lanes, half-split over all 128
-// values (the partner is lane ^ 8).  q's heads come first, k's behind.
-template <int SH, bool INTER, bool BF16, bool WHOLE>
+// SH: log2 of the lanes of a head.  q's heads come first, k's behind.
+template <int SH, bool INTER, bool BF16>
 __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams p, int64_t wg0) {
     constexpr int LPH = 1 << SH, HPW = 64 >> SH;         // lanes of a head, heads a wave's load holds
     const int lane = lane_id();
@@ -83,7 +81,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
     const int sub = lane & (LPH - 1), dim = 8 * sub;     // the lane's values dim .. dim + 7
     const int head0 = (int)(wave - token * p.waves_per_token) * (kHeadSets * HPW) + (lane >> SH);
     const int total = p.heads[0] + p.heads[1];
-    const bool in_dim = WHOLE || dim < p.hs;
+    const bool in_dim = dim < p.hs;
     const int64_t pos = p.rot > 0 ? p.positions[token] : 0;
 
     uint4 x[kHeadSets];
@@ -98,7 +96,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
         }
     }
     const bool pos_ok = p.rot == 0 || (pos >= 0 && pos < p.max_pos);
-    const bool turn = (WHOLE || dim < p.rot) && pos_ok;
+    const bool turn = dim < p.rot && pos_ok;
     const int half = p.rot / 2;
     const bool low = dim < half;
     const int partner = low ? sub + half / 8 : sub - half / 8;          // half-split pairing
@@ -153,8 +151,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
         if (!INTER)
 #pragma unroll
             for (int i = 0; i < 4; i++)
-                pw[i] = WHOLE ? dpp<0x128>(xw[i])        // row_ror:8 is lane ^ 8
-                              : (uint32_t)__shfl((int)xw[i], (lane & ~(LPH - 1)) | (partner & (LPH - 1)));
+                pw[i] = (uint32_t)__shfl((int)xw[i], (lane & ~(LPH - 1)) | (partner & (LPH - 1)));
         if (h >= total || !in_dim) continue;
         float y[8];
 #pragma unroll
@@ -189,11 +186,8 @@ static hipError_t launch_lanes(const QkNormRopeParams& in, hipStream_t s) {
     p.waves_per_token = (p.heads[0] + p.heads[1] + per_wave - 1) / per_wave;
     p.inv_hs = 1.0f / (float)p.hs;
     const int64_t wgs = (p.num_tokens * p.waves_per_token + kWavesPerBlock - 1) / kWavesPerBlock;
-    auto k = p.interleaved ? (p.cs_bf16 ? k_qk_norm_rope<SH, true, true, false> : k_qk_norm_rope<SH, true, false, false>)
-                           : (p.cs_bf16 ? k_qk_norm_rope<SH, false, true, false> : k_qk_norm_rope<SH, false, false, false>);
-    if constexpr (SH == 4)
-        if (!p.interleaved && p.hs == 128 && p.rot == 128)
-            k = p.cs_bf16 ? k_qk_norm_rope<4, false, true, true> : k_qk_norm_rope<4, false, false, true>;
+    auto k = p.interleaved ? (p.cs_bf16 ? k_qk_norm_rope<SH, true, true> : k_qk_norm_rope<SH, true, false>)
+                           : (p.cs_bf16 ? k_qk_norm_rope<SH, false, true> : k_qk_norm_rope<SH, false, false>);
     return launch_span(k, wgs, kBlockThreads, s, true, true, p);
 }
 
