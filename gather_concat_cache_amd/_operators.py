@@ -309,7 +309,8 @@ def attention_nvfp4_kv(q, kv_cache, k_scale, v_scale, block_table, query_starts,
     seq_lens[b] (int32 [B]) cached tokens.  `window`: a query sees the last
     `window` positions up to its own and the first `num_sinks`; None: all.
     max_seq_len (int): the longest sequence expected (sizes the key split
-    only).  Returns out bf16 [T, Hq, hs], with lse fp32 [T, Hq] when
+    only; the split follows all lengths of the batch, so a row's last bits may
+    change with the other requests).  Returns out bf16 [T, Hq, hs], with lse fp32 [T, Hq] when
     return_lse.  Rows of no request keep what `out` and `lse` held
     (unspecified when they are allocated here); a row that sees nothing is
     zeros with lse -inf."""

@@ -68,7 +68,9 @@ int gcache_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
  *   Hidden positions cannot reach an output, whatever their bytes: a block
  *   scale that holds the e4m3 NaN code (no write makes one) counts as 0.
  *   max_seq_len: the largest seq_lens the caller expects.  It only sizes the
- *   split of the keys; longer sequences are computed all the same.
+ *   split of the keys; longer sequences are computed all the same.  The split
+ *   follows the lengths of the whole batch: equal calls give equal bits, but
+ *   the last bits of a row may change with the other requests.
  *   workspace: gcache_attention_workspace_bytes() bytes, 16-byte aligned, or
  *   less, or NULL: with less the keys are split into fewer parts.  Its content
  *   is scratch; two calls that may run at the same time need two.
