@@ -356,46 +356,64 @@ __device__ __forceinline__ uint32_t scale_part(const AttnParams& p, int i, uint3
     return (UNI ? (uint32_t)i * p.scale_token : 0u) + part;
 }
 
-// One row of queries a column: lane l takes row t.row0 + row_off + l % 16, its
-// values as the second operand of S^T = K Q^T, and the factor from scores to
-// logits in log2 units.  Rows behind the tile are zeros at position -1.
-template <int DP, bool MLA>
-__device__ __forceinline__ void load_query(const AttnParams& p, const RowTile& t, int kvh, int row_off, int lane,
-                                           f16x8* q, float& fac, int& pos, int& tok) {
-    constexpr int KS = DP / 32, RS = MLA ? 2 : 0;
-    const int c = lane & 15, g = lane >> 4;
-    const bool in = row_off + c < t.rows;
-    const int row = in ? t.row0 + row_off + c : t.row0;
+// One row of queries a column: lane l takes row t.row0 + row_off + l % 16.
+// Rows behind the tile are zeros at position -1.
+__device__ __forceinline__ bool pos_in(const RowTile& t, int row_off, int lane) { return row_off + (lane & 15) < t.rows; }
+__device__ __forceinline__ const uint16_t* query_row(const AttnParams& p, const RowTile& t, int kvh, int row_off, int lane,
+                                                     int& pos, int& tok) {
+    const bool in = pos_in(t, row_off, lane);
+    const int row = in ? t.row0 + row_off + (lane & 15) : t.row0;
     const int tl = row / p.group;
     const int head = kvh * p.group + row - tl * p.group;
     tok = t.q0 + tl;
     pos = in ? t.ctx + tl : -1;
-    const uint16_t* src = p.q + (int64_t)tok * p.q_ts + (int64_t)head * p.q_hs;
-    u32x4 raw[KS + RS];
-    float amax = 0.0f;
+    return p.q + (int64_t)tok * p.q_ts + (int64_t)head * p.q_hs;
+}
+// First of the 8 dims of step st that lane group g holds (the last two steps of the latent form are RoPE).
+template <int DP>
+__device__ __forceinline__ int query_dim(int st, int g) {
+    return st < DP / 32 ? (DP / 4) * g + 8 * st : kNope + 16 * g + 8 * (st - DP / 32);
+}
+__device__ __forceinline__ float row_amax(const u32x4& raw, float amax) {
 #pragma unroll
-    for (int s = 0; s < KS + RS; s++) {
-        const int dim = s < KS ? (DP / 4) * g + 8 * s : kNope + 16 * g + 8 * (s - KS);
-        raw[s] = u32x4{0, 0, 0, 0};
-        if (in && (MLA || dim < p.hs)) raw[s] = *reinterpret_cast<const u32x4*>(src + dim);
-    }
-#pragma unroll
-    for (int s = 0; s < KS + RS; s++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[s][i])), fabsf(bf16_hi(raw[s][i]))));
-    amax = group_max(amax);
+    for (int i = 0; i < 4; i++) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[i])), fabsf(bf16_hi(raw[i]))));
+    return amax;
+}
+// The row's power of two, and in fac the factor from scores to logits in log2 units.
+__device__ __forceinline__ float query_scale(const AttnParams& p, float amax, float key_scale, float& fac) {
     const int e = (int)(__float_as_uint(amax) >> 23);
     const int up = min(max(264 - e, 1), 253);            // biased exponent of the row's scaling
-    const float mul = __uint_as_float((uint32_t)up << 23);
-    fac = p.scale_log2 * (MLA ? 1.0f : *p.gscale[0]) * __uint_as_float((uint32_t)(254 - up) << 23);
+    fac = p.scale_log2 * key_scale * __uint_as_float((uint32_t)(254 - up) << 23);
+    return __uint_as_float((uint32_t)up << 23);
+}
+__device__ __forceinline__ f16x8 query_operand(const u32x4& raw, float mul) {
+    f16x8 q;
 #pragma unroll
-    for (int s = 0; s < KS + RS; s++)
+    for (int i = 0; i < 4; i++) {
+        q[2 * i] = (_Float16)(bf16_lo(raw[i]) * mul);
+        q[2 * i + 1] = (_Float16)(bf16_hi(raw[i]) * mul);
+    }
+    return q;
+}
+// The whole row as the second operand of S^T = K Q^T.
+template <int DP, bool MLA>
+__device__ __forceinline__ void load_query(const AttnParams& p, const RowTile& t, int kvh, int row_off, int lane,
+                                           f16x8* q, float& fac, int& pos, int& tok) {
+    constexpr int N = DP / 32 + (MLA ? 2 : 0);
+    const uint16_t* src = query_row(p, t, kvh, row_off, lane, pos, tok);
+    u32x4 raw[N];
+    float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            q[s][2 * i] = (_Float16)(bf16_lo(raw[s][i]) * mul);
-            q[s][2 * i + 1] = (_Float16)(bf16_hi(raw[s][i]) * mul);
-        }
+    for (int s = 0; s < N; s++) {
+        const int dim = query_dim<DP>(s, lane >> 4);
+        raw[s] = u32x4{0, 0, 0, 0};
+        if (pos_in(t, row_off, lane) && (MLA || dim < p.hs)) raw[s] = *reinterpret_cast<const u32x4*>(src + dim);
+    }
+#pragma unroll
+    for (int s = 0; s < N; s++) amax = row_amax(raw[s], amax);
+    const float mul = query_scale(p, group_max(amax), MLA ? 1.0f : *p.gscale[0], fac);
+#pragma unroll
+    for (int s = 0; s < N; s++) q[s] = query_operand(raw[s], mul);
 }
 
 // A row at position pos sees the keys <= hi that are > lo or sinks, and of a

