@@ -4,8 +4,8 @@
 // join through LDS.  Bound by HBM for long contexts: each wave has a tile's
 // bytes in flight while it works on another (64 x 1 token over 8192 keys, 8
 // kv heads of 128: 169 us, 3.6 TB/s of the 4.85 that a large copy reaches); for
-// short ones by the chain of dependent loads and the launches (1038 keys: 8 us
-// and 5 for the join).
+// short ones by the chain of dependent loads and the launches (1038 keys in 9
+// splits: 8 us and 5 for the join).
 #pragma once
 
 #include "attention_device.h"

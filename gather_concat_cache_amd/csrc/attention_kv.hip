@@ -16,7 +16,7 @@ namespace gcache {
 // Bound by instruction issue: a wave's step is about 300 vector instructions
 // beside 32 or 64 matrix ones, and 32 exponentials at a quarter of the rate.
 // Causal prefill of 4 x 2048 tokens over 4096 keys, 32 heads of 128, group 4:
-// 512 us, 805 TFLOP/s of the 1360 that a large f16 product reaches.
+// 508 us, 811 TFLOP/s of the 1360 that a large f16 product reaches.
 // ---------------------------------------------------------------------------
 constexpr int kStepKeys = 64, kRowsWaves = 4, kRowsTile = 128;
 
@@ -266,7 +266,7 @@ __device__ __forceinline__ void attend_rows(const AttnParams& p, const RowTile& 
 // Tiles of up to 64 rows (a short request, or a request's last rows) give each
 // wave one 16-row tile; the longer ones two, which share each K and V fragment.
 // 32 x 16 tokens (64 rows) over 8192 keys: 185 us, against 203 with two row
-// tiles for half of the waves; head size 256: 188 against 234.
+// tiles for half of the waves, at equal splits; head size 256: 188 against 234.
 template <int DP, bool UNI, bool TREE>
 __global__ __launch_bounds__(kRowsWaves * kWave, DP <= 128 ? 2 : 1) void k_attention_rows(AttnParams p, int64_t wg0) {
     __shared__ f16x8 s_frag[2][(Share<DP>::KF + Share<DP>::VF) * kWave];

@@ -420,6 +420,16 @@ def test_sinks_and_window_split(g, qlen, window, sinks):
     check_kv(g, rng, batch, 1, 2, 128, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("qlen,window,sinks,hs", [(1, 1500, 70, 128), (9, 1601, 33, 64), (70, 1500, 70, 128), (40, 1777, 1, 256)])
+def test_long_window_split(g, qlen, window, sinks, hs):
+    """Windows long enough to be split, with sinks before them, in each kernel."""
+    rng = np.random.default_rng(qlen + 7)
+    batch = Batch(rng, [qlen, 1, qlen], [2600, 700, 1300], 16)
+    lib = g._operators._load()
+    assert lib.gcache_attention_workspace_bytes(batch.T + 2, 3, 2, 1, hs, 2600, window, sinks) > 0
+    check_kv(g, rng, batch, 1, 2, hs, window=window, sinks=sinks)
+
+
 def test_rows_of_infinities_and_nan(g):
     """A query row that holds NaN or an infinity spoils its own output only."""
     rng = np.random.default_rng(15)
