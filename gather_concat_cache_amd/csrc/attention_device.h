@@ -219,7 +219,8 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int
         if (split && unit == 0 && threadIdx.x == 0) *p.ws_chunk = t.chunk;
         if (unit >= all) return false;
         index = all - 1 - (int)unit;
-        int at = __builtin_ctzll(__ballot(upto > index));
+        // (both ballots have a bit unless the metadata is written meanwhile; the mask keeps lanes and rows in range)
+        int at = (__builtin_ffsll(__ballot(upto > index)) - 1) & (kWave - 1);
         before = __builtin_amdgcn_readlane(upto - n, at);
         int work = work1;
         if (per == 1) {
@@ -233,7 +234,7 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int
             const int tiles = lane < per ? tiles_of((next - q) * p.group) : 0;
             n = split ? tiles * request_splits(work, t.chunk) : tiles;
             upto = scan_lanes(n);
-            at = __builtin_ctzll(__ballot(before + upto > index));
+            at = (__builtin_ffsll(__ballot(before + upto > index)) - 1) & (kWave - 1);
             t.b = first + at;
             before += __builtin_amdgcn_readlane(upto - n, at);
             t.q0 = __builtin_amdgcn_readlane(q, at);
@@ -255,6 +256,7 @@ __device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int
         t.q0 = query_start(p, lo);
         t.qlen = query_start(p, lo + 1) - t.q0;
     }
+    t.b = min(t.b, p.batch - 1);
     const int in = index - before, tile = in / t.splits;
     t.split = (int)((uint32_t)(in - tile * t.splits + t.b) % (uint32_t)t.splits);
     const int64_t row0 = (int64_t)tile * RT, rows = (int64_t)t.qlen * p.group;
