@@ -146,7 +146,10 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
     }
     a.key_tiles = (int32_t)kt;
     a.units = a.tiles;
-    if (splits > 1 && splits * groups / hk > a.tiles) a.units = (int32_t)(splits * groups / hk);
+    // whole rounds: uneven requests fill them (a launch that is smaller than one stays as it is)
+    int64_t units = splits * groups;
+    if (units > slots) units = rounds(units) * slots;
+    if (splits > 1 && units / hk > a.tiles) a.units = (int32_t)(units / hk);
     // requests longer than the mean are split further
     a.splits = (int32_t)(splits == 1 ? 1 : 2 * splits < top ? 2 * splits : top);
     a.ws_floats = splits > 1 ? (a.splits + 1) * per : 0;
