@@ -9,12 +9,20 @@ namespace gcache {
 // weighted rows follow with four loads in flight.  Bound by memory: the parts
 // of 761 tokens of 32 heads of 128, seven each on average, take 26 us.
 constexpr int kMaxSplits = 256;
+// Rows and planned splits (half of the bound p.splits) for a workgroup a row: 1
+// token of 16 heads over 65536 latent keys 34 us against 54 with a wave a row, 8
+// x 1 over 32768 48 against 54; but 2048 rows of 3 splits 46 against 44.
+constexpr int kWideRows = 2048, kWideSplits = 32;
 
+// WIDE: the four waves of a workgroup share a row, each with every fourth
+// split, so a single token's many splits are not read in one wave's sequence.
+template <bool WIDE>
 __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, int64_t wg0) {
     __shared__ float s_w[kWavesPerBlock][kMaxSplits];
+    __shared__ f32x4 s_acc[WIDE ? kWavesPerBlock : 1][WIDE ? kNope / 4 : 1];
     const int lane = lane_id();
     const int RT = p.row_tile;
-    const int64_t id = (wg0 + blockIdx.x) * kWavesPerBlock + wave_id();
+    const int64_t id = WIDE ? wg0 + blockIdx.x : (wg0 + blockIdx.x) * kWavesPerBlock + wave_id();
     const int64_t rows = (int64_t)p.total_q * p.hq;
     if (id >= rows) return;
     const int token = (int)(id / p.hq), head = (int)(id % p.hq);
@@ -63,28 +71,39 @@ __global__ __launch_bounds__(kBlockThreads) void k_attention_join(AttnParams p, 
     for (int d = 1; d < kWave; d <<= 1) ll += __shfl_xor(ll, d);
     const float scale = ll == 0.0f ? 0.0f : (p.gscale[1] ? *p.gscale[1] : 1.0f) / ll;
     __builtin_amdgcn_wave_barrier();
+    constexpr int STEP = WIDE ? kWavesPerBlock : 1;
+    const auto write = [&](int d, const f32x4& x) {
+        *reinterpret_cast<u32x2*>(p.out + (int64_t)token * p.o_ts + (int64_t)head * p.o_hs + d) =
+            u32x2{pack_bf16x2(x[0] * scale, x[1] * scale), pack_bf16x2(x[2] * scale, x[3] * scale)};
+    };
     for (int d = 4 * lane; d < p.hs; d += 4 * kWave) {
         f32x4 acc = {0, 0, 0, 0};
         const float* src = p.ws_o + id * p.hs + d;
-        int k = 0;
-        for (; k + 4 <= n; k += 4) {
+        int k = WIDE ? wave_id() : 0;
+        for (; k + 3 * STEP < n; k += 4 * STEP) {
             f32x4 x[4];
 #pragma unroll
-            for (int u = 0; u < 4; u++) x[u] = *reinterpret_cast<const f32x4*>(src + (k + u) * rows * p.hs);
+            for (int u = 0; u < 4; u++) x[u] = *reinterpret_cast<const f32x4*>(src + (k + u * STEP) * rows * p.hs);
 #pragma unroll
             for (int u = 0; u < 4; u++) {
-                const float wt = wts[k + u];
+                const float wt = wts[k + u * STEP];
 #pragma unroll
                 for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(wt, x[u][i], acc[i]);
             }
         }
-        for (; k < n; k++) {
+        for (; k < n; k += STEP) {
             const f32x4 x = *reinterpret_cast<const f32x4*>(src + k * rows * p.hs);
 #pragma unroll
             for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(wts[k], x[i], acc[i]);
         }
-        *reinterpret_cast<u32x2*>(p.out + (int64_t)token * p.o_ts + (int64_t)head * p.o_hs + d) =
-            u32x2{pack_bf16x2(acc[0] * scale, acc[1] * scale), pack_bf16x2(acc[2] * scale, acc[3] * scale)};
+        if (WIDE) s_acc[wave_id()][d / 4] = acc;
+        else write(d, acc);
+    }
+    if (WIDE) {
+        __syncthreads();
+        const int c = threadIdx.x;
+        if (4 * c < p.hs) write(4 * c, (s_acc[0][c] + s_acc[WIDE ? 1 : 0][c]) + (s_acc[WIDE ? 2 : 0][c] + s_acc[WIDE ? 3 : 0][c]));
+        if (c > 0) return;
     }
     if (lane == 0 && p.lse)
         p.lse[(int64_t)token * p.lse_ts + head] =
@@ -178,7 +197,8 @@ hipError_t launch_attention_parts(void (*kernel)(AttnParams, int64_t), int waves
     const hipError_t e = launch_span(kernel, (units + 7) / 8 * 8 * p.hk, waves * kWave, s, true, !join, p);
     if (e != hipSuccess || !join) return e;
     const int64_t rows = (int64_t)p.total_q * p.hq;
-    return launch_span(k_attention_join, (rows + kWavesPerBlock - 1) / kWavesPerBlock, kBlockThreads, s, false, true, p);
+    if (rows <= kWideRows && p.splits >= kWideSplits) return launch_span(k_attention_join<true>, rows, kBlockThreads, s, false, true, p);
+    return launch_span(k_attention_join<false>, (rows + kWavesPerBlock - 1) / kWavesPerBlock, kBlockThreads, s, false, true, p);
 }
 
 }  // namespace gcache

@@ -430,6 +430,18 @@ def test_long_window_split(g, qlen, window, sinks, hs):
     check_kv(g, rng, batch, 1, 2, hs, window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("hs", [64, 80, 128, 256, 576])
+def test_many_splits_of_few_rows(g, hs):
+    """So many splits that a workgroup joins each row; short requests beside."""
+    rng = np.random.default_rng(hs + 1)
+    batch = Batch(rng, [1, 2, 1, 1], [4400, 3900, 90, 1], 16)
+    if hs == 576:
+        check_mla(g, rng, batch, 5)
+        check_mla(g, rng, batch, 1, mask=rng.random((batch.T, 2)) < 0.5)
+    else:
+        check_kv(g, rng, batch, 1, 3, hs)
+
+
 def test_rows_of_infinities_and_nan(g):
     """A query row that holds NaN or an infinity spoils its own output only."""
     rng = np.random.default_rng(15)
