@@ -358,6 +358,18 @@ __device__ __forceinline__ uint32_t scale_part(const AttnParams& p, int i, uint3
     return (UNI ? (uint32_t)i * p.scale_token : 0u) + part;
 }
 
+// Called in a loop, makes the lane's offsets look new: otherwise their zero
+// extension is hoisted, and a load's address takes a 64-bit vector add and a
+// register more, instead of a scalar base with a 32-bit offset.  (64-row latent
+// kernel 497 to 457 us, few rows 1 to 4 per cent; the kernel for many per-head
+// rows lost 2 per cent and goes without.)
+template <int N>
+__device__ __forceinline__ void renew(uint32_t (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i++) asm volatile("" : "+v"(x[i]));
+}
+__device__ __forceinline__ void renew(uint32_t& x) { asm volatile("" : "+v"(x)); }
+
 // One row of queries a column: lane l takes row t.row0 + row_off + l % 16.
 // Rows behind the tile are zeros at position -1.
 __device__ __forceinline__ bool pos_in(const RowTile& t, int row_off, int lane) { return row_off + (lane & 15) < t.rows; }

@@ -99,8 +99,8 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
     if (threadIdx.x < 3) s_flag[threadIdx.x] = 0;
     const auto look_up = [&](int x) { return find_pages<UNI, kTileKeys>(p, bt_row, (x < v1 ? x : v0) * kTileKeys, lane); };
     // the lane's parts of its K row, and of its V rows
-    const uint32_t kd = data_part<UNI>(p, c, 64 * g + 16 * (w >> 1)), ks = scale_part<UNI>(p, c, 8 * g + 2 * (w >> 1));
-    const uint32_t rope = data_part<UNI>(p, c, kNvRopeOff + 16 * g + 8 * (w >> 1));
+    uint32_t kd = data_part<UNI>(p, c, 64 * g + 16 * (w >> 1)), ks = scale_part<UNI>(p, c, 8 * g + 2 * (w >> 1));
+    uint32_t rope = data_part<UNI>(p, c, kNvRopeOff + 16 * g + 8 * (w >> 1));
     uint32_t vd[4], vs[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -121,6 +121,13 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
     }
     __syncthreads();
     for (int v = v0, n = 0, f = 0; v < v1; v++, n ^= 1, f = f == 2 ? 0 : f + 1) {
+        if (UNI) {
+            renew(kd);
+            renew(ks);
+            renew(rope);
+            renew(vd);
+            renew(vs);
+        }
         // ---- scores of step v, K of step v + 1
         const uint32_t live = live_keys<UNI, kTileKeys>(p, pg0, lane) >> (4 * kt) & 0xF;
         f32x4 s = {0, 0, 0, 0};
@@ -256,8 +263,8 @@ __global__ __launch_bounds__(kTokenWaves * kWave, 2) void k_attention_latent_tok
     const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
     const auto look_up = [&](int x) { return find_pages<UNI, kTokenKeys>(p, bt_row, (x < v1 ? x : v0) * kTokenKeys, lane); };
     // the lane's parts of its K row, and of its V rows: dims 128 w + 8 c .. + 7
-    const uint32_t kd = data_part<UNI>(p, c, 64 * g), ks = scale_part<UNI>(p, c, 8 * g);
-    const uint32_t rope = data_part<UNI>(p, c, kNvRopeOff + 16 * g);
+    uint32_t kd = data_part<UNI>(p, c, 64 * g), ks = scale_part<UNI>(p, c, 8 * g);
+    uint32_t rope = data_part<UNI>(p, c, kNvRopeOff + 16 * g);
     uint32_t vd[4], vs[4];
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -329,6 +336,13 @@ __global__ __launch_bounds__(kTokenWaves * kWave, 2) void k_attention_latent_tok
     for (int d = 0; d < 8; d++) o[d] = f32x4{0, 0, 0, 0};
 
     for (int v = v0; v < v1; v++) {
+        if (UNI) {
+            renew(kd);
+            renew(ks);
+            renew(rope);
+            renew(vd);
+            renew(vs);
+        }
         // ---- S^T = K Q^T, two chains
         const uint32_t live = live_keys<UNI, kTokenKeys>(p, pg, lane) >> (4 * w) & 0xF;
         f32x4 s = {0, 0, 0, 0}, s2 = {0, 0, 0, 0};

@@ -30,6 +30,13 @@ struct RawV {
 template <bool UNI>
 struct LaneParts {               // 32-bit offsets of the lane's parts of rows
     uint32_t kd, ks, vd[4], vs[4];
+    __device__ __forceinline__ void renew() {
+        if (!UNI) return;
+        gcache::renew(kd);
+        gcache::renew(ks);
+        gcache::renew(vd);
+        gcache::renew(vs);
+    }
 };
 // UNI kernels take head sizes of exactly DP and pages of whole 16-key groups,
 // so that a group's address is wave-uniform; the others take any head size up
@@ -147,7 +154,7 @@ void k_attention_few(AttnParams p, int64_t wg0) {
     const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
     const auto tile_key = [&](int v) { return (v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0) * kTileKeys; };
     const auto look_up = [&](int v) { return find_pages<UNI, kTileKeys>(p, bt_row, tile_key(v < v1 ? v : v0), lane); };
-    const LaneParts<UNI> lo = lane_parts<DP, UNI>(p, kvh, lane);
+    LaneParts<UNI> lo = lane_parts<DP, UNI>(p, kvh, lane);
 
     // Loads return in order: page ids are asked for before the bytes of the
     // tile ahead, so waiting for ids leaves bytes in flight.
@@ -182,6 +189,7 @@ void k_attention_few(AttnParams p, int64_t wg0) {
 
     for (; v < v1; v += kFewWaves) {
         const bool more = v + kFewWaves < v1;
+        lo.renew();
         const int key0 = tile_key(v);
         const uint32_t live = live_keys<UNI, kTileKeys>(p, pg, lane);
         // ---- S^T = K Q^T
