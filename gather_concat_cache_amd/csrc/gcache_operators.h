@@ -99,7 +99,7 @@ struct GrantParams {
     int32_t n;
     int32_t* status;             // [n]
     int32_t* claim;              // [num_rows] lowest request number of a row
-    int32_t* upto;               // [n] pages of the requests up to this one
+    int32_t* upto;               // [n] pages of the requests up to this one, -1: more than num_blocks
     int32_t* len;                // [n] the request's tokens, -1 when it is refused
     int32_t* free_ids;           // [num_blocks] the lowest free pages
 };

@@ -88,6 +88,13 @@ __device__ __forceinline__ int64_t list_free(const GrantParams& p, int64_t want,
     return found;
 }
 
+// Pages of the requests up to one as its entry of upto: -1 when they are more
+// than there are pages, so that no clipped number looks like one that fits.
+// (Sums are 64 bits; a request's own need is at most INT32_MAX.)
+__device__ __forceinline__ int upto_entry(const GrantParams& p, int64_t upto) {
+    return upto > p.t.num_blocks ? -1 : (int)upto;
+}
+
 // One workgroup, at most a request a thread: which requests are valid (the
 // lowest-numbered one of a row wins), how many pages each needs, the lowest
 // free pages for all of them.  FORK: a = parent rows, b = child rows; else a =
@@ -123,7 +130,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_grant_small(GrantParams p, int
     __syncthreads();
     if (len >= 0 && s_first[slot] != f) len = -1;
     int need = 0;
-    if (len >= 0) need = FORK ? len % bs != 0 : min(pages_of(len, bs) - pages_of(p.t.lens[row], bs), p.t.num_blocks);
+    if (len >= 0) need = FORK ? len % bs != 0 : pages_of(len, bs) - pages_of(p.t.lens[row], bs);
     int64_t all;
     const int64_t upto = wg_exclusive(need, s_scan, &all) + need;
     const int64_t found = list_free(p, all, s_scan);
@@ -131,8 +138,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_grant_small(GrantParams p, int
         const bool ok = len >= 0 && upto <= found;
         p.status[f] = ok;
         p.len[f] = ok ? len : -1;
-        // needs past int32 cannot be met: num_blocks + 1 pages say as much
-        p.upto[f] = (int)min(upto, (int64_t)p.t.num_blocks + 1);
+        p.upto[f] = upto_entry(p, upto);
     }
 }
 
@@ -160,25 +166,23 @@ __global__ __launch_bounds__(kPlanThreads) void k_grant_plan(GrantParams p, int6
             if (len >= 0 && __hip_atomic_load(&p.claim[row_of(f)], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != f)
                 len = -1;
             if (len >= 0)
-                need = FORK ? len % bs != 0
-                            : min(pages_of(len, bs) - pages_of(p.t.lens[row_of(f)], bs), p.t.num_blocks);
+                need = FORK ? len % bs != 0 : pages_of(len, bs) - pages_of(p.t.lens[row_of(f)], bs);
             p.len[f] = len;
         }
         int64_t sum;
         const int64_t upto = need_all + wg_exclusive(need, s_scan, &sum) + need;
-        // needs past int32 cannot be met: num_blocks + 1 pages say as much
-        if (f < p.n) p.upto[f] = (int)min(upto, (int64_t)p.t.num_blocks + 1);
+        if (f < p.n) p.upto[f] = upto_entry(p, upto);
         need_all += sum;
     }
     const int64_t found = list_free(p, need_all, s_scan);
     for (int f = tid; f < p.n; f += kPlanThreads) {
-        const bool ok = p.len[f] >= 0 && p.upto[f] <= found;
+        const bool ok = p.len[f] >= 0 && p.upto[f] >= 0 && p.upto[f] <= found;
         p.status[f] = ok;
         if (!ok) p.len[f] = -1;
     }
 }
 
-// Request f's first page in free_ids (its need is upto[f] - upto[f - 1]).
+// First page in free_ids of a granted request f (its need is upto[f] - upto[f - 1]; both fit).
 __device__ __forceinline__ int first_page(const GrantParams& p, int f) { return f > 0 ? p.upto[f - 1] : 0; }
 
 // The row of fork f, by one workgroup.

@@ -835,3 +835,22 @@ def test_graph_replay(g):
         assert torch.equal(out, want), seed
         for a, b in zip(state, (*fresh[0].caches, fresh[0].table, fresh[0].lens, fresh[0].refs)):
             assert torch.equal(a, b), seed
+
+
+@pytest.mark.parametrize("n", [1, 3, 1024, 1025])
+@pytest.mark.parametrize("beyond", [0, 1, 4])
+def test_extend_of_an_unused_pool(g, n, beyond):
+    """All pages free and tables wider than the pool: a request for every page
+    is granted, one for more is refused and leaves the state as it was, and so
+    do the requests behind it.  Both planning kernels."""
+    nb, bs = 6, 16
+    rows = np.arange(n, dtype=np.int32)
+    new = np.full(n, bs, np.int32)
+    new[0] = (nb + beyond) * bs - 3
+    state = (np.full((n, nb + 5), -9, np.int32), np.zeros(n, np.int32), np.zeros(nb, np.int32))
+    table, lens, refs = check_pages(lambda t, l, r, c: g.extend_requests(bs, t, l, r, dev(rows), dev(new)),
+                                    lambda t, l, r, c: ref.extend(t, l, r, rows, new, bs), state, [])
+    if beyond:
+        assert (table == -9).all() and not lens.any() and not refs.any()
+    else:
+        assert table[0, :nb].tolist() == list(range(nb)) and lens[0] == new[0]
