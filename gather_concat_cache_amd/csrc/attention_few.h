@@ -8,6 +8,8 @@
 // splits: 8 us and 5 for the join).
 #pragma once
 
+#include <type_traits>
+
 #include "attention_device.h"
 
 namespace gcache {
@@ -27,15 +29,20 @@ struct RawV {
     uint32_t v[8][W], s[8];
 };
 
+// The lane's offsets into a page of its parts of rows, the head's and the
+// side's distance among them: 32 bits where uniform_pages() says that they fit,
+// else 64 (K and V planes, or head planes, of a whole cache may lie apart).
 template <bool UNI>
-struct LaneParts {               // 32-bit offsets of the lane's parts of rows
-    uint32_t kd, ks, vd[4], vs[4];
+struct LaneParts {
+    typedef std::conditional_t<UNI, uint32_t, uint64_t> offset;
+    offset kd, ks, vd[4], vs[4];
     __device__ __forceinline__ void renew() {
-        if (!UNI) return;
-        gcache::renew(kd);
-        gcache::renew(ks);
-        gcache::renew(vd);
-        gcache::renew(vs);
+        if constexpr (UNI) {
+            gcache::renew(kd);
+            gcache::renew(ks);
+            gcache::renew(vd);
+            gcache::renew(vs);
+        }
     }
 };
 // UNI kernels take head sizes of exactly DP and pages of whole 16-key groups,
@@ -46,16 +53,17 @@ struct LaneParts {               // 32-bit offsets of the lane's parts of rows
 template <int DP, bool UNI>
 __device__ __forceinline__ LaneParts<UNI> lane_parts(const AttnParams& p, int kvh, int lane) {
     const int c = lane & 15, g = lane >> 4;
-    const uint32_t hd = (uint32_t)(kvh * p.L.data_head_stride), hs = (uint32_t)(kvh * p.L.scale_head_stride);
-    const uint32_t side = (uint32_t)p.L.side_stride;
+    typedef typename LaneParts<UNI>::offset offset;
+    const offset hd = (offset)(kvh * p.L.data_head_stride), hs = (offset)(kvh * p.L.scale_head_stride);
+    const offset side = (offset)p.L.side_stride;
     const bool in = UNI || (DP / 16) * c < p.hs;
     LaneParts<UNI> o;
-    o.kd = data_part<UNI>(p, c, hd + (DP / 8) * g);
-    o.ks = scale_part<UNI>(p, c, hs + (DP / 64) * g);
+    o.kd = hd + data_part<UNI>(p, c, (DP / 8) * g);
+    o.ks = hs + scale_part<UNI>(p, c, (DP / 64) * g);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        o.vd[j] = data_part<UNI>(p, 4 * g + j, side + hd + (in ? (DP / 32) * c : 0));
-        o.vs[j] = scale_part<UNI>(p, 4 * g + j, side + hs + (in ? (DP * c) / 256 : 0));
+        o.vd[j] = side + hd + data_part<UNI>(p, 4 * g + j, in ? (DP / 32) * c : 0);
+        o.vs[j] = side + hs + scale_part<UNI>(p, 4 * g + j, in ? (DP * c) / 256 : 0);
     }
     return o;
 }

@@ -1,6 +1,8 @@
 """GPU tests of the operators around the cache against plain 64-bit
 references (operator_refs.py), at the sizes, layouts and masks where they can
 go wrong."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
@@ -854,3 +856,52 @@ def test_extend_of_an_unused_pool(g, n, beyond):
         assert (table == -9).all() and not lens.any() and not refs.any()
     else:
         assert table[0, :nb].tolist() == list(range(nb)) and lens[0] == new[0]
+
+
+def far_cache(g, flat, L, nb, bs, hk, hs, far):
+    """The entries of `flat` (layout L) in an allocation of over 4 GiB: K and V
+    planes apart ("planes"), or the heads' data and scales ("heads")."""
+    full = hs // 2 + hs // 16
+    apart = (1 << 32) + 4096
+    d, s = bs * hs // 2, bs * hs // 16                       # a page's data and scales of one head
+    if far == "planes":
+        F = g.NvFp4KvLayout(data_offset=0, data_token_stride=hk * hs // 2, data_head_stride=hs // 2, scale_offset=hk * d,
+                     scale_token_stride=hk * hs // 16, scale_head_stride=hs // 16, side_stride=apart,
+                     block_stride=(hk * (d + s) + 7) // 8 * 8)
+    else:
+        page = (d + s + 7) // 8 * 8
+        F = g.NvFp4KvLayout(data_offset=0, data_token_stride=hs // 2, data_head_stride=apart, scale_offset=d,
+                     scale_token_stride=hs // 16, scale_head_stride=apart, side_stride=page, block_stride=2 * page)
+    big = torch.full(((hk - 1) * F.data_head_stride + F.side_stride + nb * F.block_stride + 64,), 0xFF, dtype=torch.uint8,
+                     device="cuda")
+    for side, h, (what, n) in itertools.product((0, 1), range(hk), (("data", hs // 2), ("scale", hs // 16))):
+        at = lambda X, base: torch.as_strided(               # noqa: E731
+            base, (nb, bs, n), (X.block_stride, getattr(X, what + "_token_stride"), 1),
+            getattr(X, what + "_offset") + side * X.side_stride + h * getattr(X, what + "_head_stride"))
+        at(F, big).copy_(at(L, torch.from_numpy(flat)))
+    return torch.as_strided(big, (nb, 2, bs, hk, full), (F.block_stride, F.side_stride, hk * full, full, 1)), F
+
+
+@pytest.mark.parametrize("far", ["planes", "heads"])
+@pytest.mark.parametrize("hs,bs,qlens", [(128, 16, [1, 2]), (80, 24, [1, 3]), (256, 16, [1, 1]), (64, 16, [40, 1]),
+                                         (128, 16, [70, 3]), (176, 8, [33, 1])])
+def test_strides_past_32_bits(g, hs, bs, qlens, far):
+    """Sides and heads more than 4 GiB apart, few rows and many."""
+    rng = np.random.default_rng(hs + bs)
+    hk, group, lens = 2, 4, [150, 71]
+    batch = Batch(rng, qlens, lens, bs)
+    flat, _, L = kv_cache(g, rng, batch, hk, hs, "split")
+    cache, F = far_cache(g, flat, L, batch.nb, bs, hk, hs, far)
+    q, q64 = queries(rng, batch.T, hk * group, hs)
+    bt, starts, sl = batch.metadata()
+    one = torch.ones(1, device="cuda")
+    scale = 0.0625
+    out, lse = g.attention_nvfp4_kv(q, cache, one, one, bt, starts, sl, 150, scale, layout=F, return_lse=True)
+    for b, (n, length) in enumerate(zip(qlens, lens)):
+        r0 = int(batch.starts[b])
+        see = np.repeat(ref.causal(n, length), group, 0)
+        for h in range(hk):
+            k, v, _ = ref.kv_positions(flat, L, batch.table[b], length, bs, batch.nb, h, hs)
+            o, l, ot, lt = ref.attend(q64[r0:r0 + n, h * group:(h + 1) * group].reshape(-1, hs), k, v, see, scale)
+            close(out[r0:r0 + n, h * group:(h + 1) * group].reshape(-1, hs), o, ot, f"request {b} head {h} out")
+            close(lse[r0:r0 + n, h * group:(h + 1) * group].reshape(-1), l, lt, f"request {b} head {h} lse")
