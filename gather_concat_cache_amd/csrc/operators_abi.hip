@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "../../include/gcache_attention.h"
 #include "../../include/gcache_pages.h"
@@ -41,6 +42,27 @@ BlockDiv make_div(int32_t block_size) {
     return d;
 }
 
+// Rows of n values at t * token_stride + h * head_stride (t < tokens, h <
+// heads) share no element.  Nearly always all heads of a token, or all tokens
+// of a head, end before the next begins; else two rows h heads and t tokens
+// apart meet where |h * head_stride - t * token_stride| < n.
+bool rows_apart(int64_t tokens, int64_t heads, int64_t token_stride, int64_t head_stride, int64_t n) {
+    if (tokens < 1 || heads < 1) return true;
+    if ((tokens > 1 && token_stride < n) || (heads > 1 && head_stride < n)) return false;
+    if (tokens == 1 || heads == 1) return true;
+    typedef __int128 wide;                               // products of two 64-bit sizes
+    if ((wide)(heads - 1) * head_stride + n <= token_stride || (wide)(tokens - 1) * token_stride + n <= head_stride) return true;
+    if (heads > tokens) {                                // step over the fewer
+        std::swap(heads, tokens);
+        std::swap(head_stride, token_stride);
+    }
+    for (int64_t h = 1; h < heads; h++) {
+        const wide at = (wide)h * head_stride, t = at / token_stride;    // the rows around `at` are t and t + 1
+        if ((t < tokens && at - t * token_stride < n) || (t + 1 < tokens && (t + 1) * token_stride - at < n)) return false;
+    }
+    return true;
+}
+
 // Head dims a kernel works with: 64, 128, 256, or 512 for the latent cache.
 int padded_dim(int32_t head_size) { return head_size <= 64 ? 64 : head_size <= 128 ? 128 : head_size <= 256 ? 256 : 512; }
 
@@ -59,15 +81,15 @@ int attention_args(const gcache_attention_args* a, int32_t hk, int32_t dk, int32
     if (a->q_token_stride < 0 || a->q_head_stride < 0 || a->out_token_stride < 0 || a->out_head_stride < 0 ||
         a->lse_token_stride < 0)
         return GCACHE_ERR_SHAPE;
-    // rows of the output must not share elements
-    if ((a->num_q_heads > 1 && a->out_head_stride < dv) || (a->total_q > 1 && a->out_token_stride < dv) ||
-        (a->lse && a->total_q > 1 && a->lse_token_stride < a->num_q_heads))
-        return GCACHE_ERR_SHAPE;
     if (!std::isfinite(a->softmax_scale)) return GCACHE_ERR_SHAPE;
     if (!aligned(a->q, 16) || !aligned(a->out, 16) || a->q_token_stride % 8 || a->q_head_stride % 8 ||
         a->out_token_stride % 8 || a->out_head_stride % 8 || !aligned(a->lse, 4) || !aligned(a->query_starts, 4) ||
         !aligned(a->seq_lens, 4) || !aligned(a->block_table, 4) || !aligned(a->workspace, 16))
         return GCACHE_ERR_ALIGN;
+    // rows of an output must not share elements
+    if (!rows_apart(a->total_q, a->num_q_heads, a->out_token_stride, a->out_head_stride, dv) ||
+        (a->lse && a->total_q > 1 && a->lse_token_stride < a->num_q_heads))
+        return GCACHE_ERR_SHAPE;
     (void)dk;
     p->q = static_cast<const uint16_t*>(a->q);
     p->out = static_cast<uint16_t*>(a->out);
@@ -226,11 +248,9 @@ int gcache_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, 
         if (st[i] % 8) return GCACHE_ERR_ALIGN;
     }
     // rows of an output must not share elements
-    for (int i = 0; i < 2; i++) {
-        const int32_t n = i ? num_kv_heads : num_q_heads;
-        if (n && ((n > 1 && st[5 + 2 * i] < head_size) || (num_tokens > 1 && st[4 + 2 * i] < head_size)))
+    for (int i = 0; i < 2; i++)
+        if (!rows_apart(num_tokens, i ? num_kv_heads : num_q_heads, st[4 + 2 * i], st[5 + 2 * i], head_size))
             return GCACHE_ERR_SHAPE;
-    }
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_weight, 16) ||
         !aligned(k_weight, 16) || !aligned(positions, 8) || !aligned(cos_sin, cos_sin_bf16 ? 2 : 4))
         return GCACHE_ERR_ALIGN;

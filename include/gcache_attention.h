@@ -31,8 +31,9 @@ extern "C" {
  *
  *  q, k          bf16 [num_tokens, heads, head_size], token and head strides
  *                in elements (multiples of 8), 16-byte aligned
- *  q_out, k_out  likewise; may be q and k themselves (same strides), else
- *                they must not overlap the inputs
+ *  q_out, k_out  likewise, no two rows sharing an element; may be q and k
+ *                themselves (same strides), else they must not overlap the
+ *                inputs
  *  q_weight, k_weight  bf16 [head_size], 16-byte aligned
  *  positions     int64 [num_tokens]
  *  cos_sin       fp32 (cos_sin_bf16 == 0) or bf16 [max_position, >= rot], row
@@ -81,7 +82,7 @@ typedef struct {
     float* lse;                  /* [total_q, >= num_q_heads] natural log of the row's sum of
                                     exp(logit), or NULL */
     int64_t q_token_stride, q_head_stride;       /* elements, multiples of 8 */
-    int64_t out_token_stride, out_head_stride;   /* elements, multiples of 8 */
+    int64_t out_token_stride, out_head_stride;   /* likewise; no two rows may share an element */
     int64_t lse_token_stride;                    /* elements */
     const int32_t* query_starts; /* [batch_size + 1] */
     const int32_t* seq_lens;     /* [batch_size] */

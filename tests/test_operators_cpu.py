@@ -256,3 +256,31 @@ def test_reference_page_rules():
     assert refs.tolist() == [1, 1, 0, 1, 1] and lens.tolist() == [0, 6, 8]
     assert ref.compact(table, lens, refs, 4, [cache]).tolist() == [0, 1, -1, 3, 2]
     assert table.tolist() == [[-1, -1], [2, 0], [1, 3]] and cache[2, 0] == 4
+
+
+# strides of 3 tokens and 4 heads of 64 values: rows that meet, and rows that do not
+SHARED = [(64, 64), (128, 64), (64, 128), (192, 64), (72, 64), (64, 184), (128, 256), (192, 128)]
+APART = [(256, 64), (64, 192), (512, 128), (80, 240), (320, 72), (1024, 64), (128, 320), (192, 256), (192, 320)]
+
+
+@pytest.mark.parametrize("strides,ok", [(s, False) for s in SHARED] + [(s, True) for s in APART])
+def test_rows_of_an_output_share_no_element(lib, strides, ok):
+    """(token stride, head stride) pairs, each at least a row: refused when two
+    rows of the output meet, whichever of the two strides is the larger."""
+    import gather_concat_cache_amd as g
+    T, H, hs = 3, 4, 64
+    ts, st = strides
+    used = np.zeros(T * ts + H * st + hs, int)
+    for t in range(T):
+        for h in range(H):
+            used[t * ts + h * st:][:hs] += 1
+    assert (used.max() == 1) == ok, "the lists above"
+    L = g.nvfp4_kv_split_layout(16, 2, hs)
+    a = _args(total_q=T, num_q_heads=H, q_head_stride=hs, out_token_stride=ts, out_head_stride=st)
+    if ok and torch.cuda.is_available():
+        return                                               # accepted: would be launched
+    want = (-4, -5) if ok else (-2,)                         # refused for its shape, or for want of a GPU
+    assert lib.gcache_attention_nvfp4_kv(C.byref(a), A16, C.byref(L), A16, A16, 2, hs, 0, 0, None) in want
+    for heads, out in (((H, 0), (ts, st, 0, 0)), ((0, H), (0, 0, ts, st))):      # q's output, k's
+        assert lib.gcache_qk_norm_rope(A16, A16, A16, A16, A16, A16, None, None, 0, 0, 0, T, *heads, hs, 0, 0, 1e-6, 256, 64,
+                                       256, 64, *out, None) in want
