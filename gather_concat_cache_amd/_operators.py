@@ -56,6 +56,7 @@ _SIGS = {
     "gcache_compact_pages": (C.c_int, [_STATE, _CACHES, _P, _P, _I64, _P]),
 }
 
+_INT32_MAX = 2 ** 31 - 1
 _lib = None
 
 
@@ -223,6 +224,8 @@ def _attention(fn, extra, q, dk, dv, hk, num_blocks, block_size, block_table, qu
     B = seq_lens.numel()
     if query_starts.numel() != B + 1 or block_table.shape[0] < B:
         raise ValueError("query_starts must hold batch + 1 entries and block_table a row per request")
+    if B > _INT32_MAX or hq > _INT32_MAX or block_size > _INT32_MAX:
+        raise ValueError("requests, heads and block size must be within int32")
     if out is None:
         out = torch.empty((T, hq, dv), dtype=_BF16, device=dev)
     else:
@@ -275,7 +278,7 @@ def _tree_mask(mask, T, dev):
     if (cols > 1 and unit != 1) or (T > 1 and row < cols):
         raise ValueError("tree_mask must be [T, columns] with unit last stride and rows that do not overlap")
     # a mask without columns has no memory, and no pointer would mean a chain
-    return mask.data_ptr() or _NO_COLUMNS, max(row, cols), cols
+    return mask.data_ptr() or _NO_COLUMNS, max(row, cols), min(cols, _INT32_MAX)
 
 
 _split_layout = functools.lru_cache(maxsize=64)(nvfp4_kv_split_layout)     # of sizes; not handed out
@@ -323,7 +326,8 @@ def attention_nvfp4_kv(q, kv_cache, k_scale, v_scale, block_table, query_starts,
     hk, hs, nb, bs, layout = _per_head(kv_cache, q, k_scale, v_scale, layout, dev)
     if window is not None and window < 1:
         raise ValueError("window must be at least 1 (None: no window)")
-    w, sinks = (0, 0) if window is None else (window, num_sinks)
+    # no position reaches int32's end, so larger numbers mean the same as it (ctypes would keep their low bits)
+    w, sinks = (0, 0) if window is None else (min(window, _INT32_MAX), max(min(num_sinks, _INT32_MAX), -1))
     extra = (kv_cache.data_ptr(), C.byref(layout), k_scale.data_ptr(), v_scale.data_ptr(), hk, hs, w, sinks)
     return _attention("gcache_attention_nvfp4_kv", extra, q, hs, hs, hk, nb, bs, block_table, query_starts, seq_lens,
                       max_seq_len, softmax_scale, w, sinks, out, lse, return_lse, workspace, dev)
@@ -405,6 +409,8 @@ def _page_state(block_size, block_table, seq_lens, ref_counts, dev=None):
     _vector(ref_counts, _I32T, "ref_counts", dev)
     if seq_lens.numel() != block_table.shape[0]:
         raise ValueError("seq_lens must hold one length per row of block_table")
+    if not 1 <= block_size <= _INT32_MAX or block_table.shape[0] > _INT32_MAX:
+        raise ValueError("block_size must be positive, it and the rows of block_table within int32")
     return PageState(block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), ref_counts.data_ptr(),
                      ref_counts.numel(), block_table.shape[0], block_size), dev
 

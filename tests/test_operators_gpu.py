@@ -905,3 +905,30 @@ def test_strides_past_32_bits(g, hs, bs, qlens, far):
             o, l, ot, lt = ref.attend(q64[r0:r0 + n, h * group:(h + 1) * group].reshape(-1, hs), k, v, see, scale)
             close(out[r0:r0 + n, h * group:(h + 1) * group].reshape(-1, hs), o, ot, f"request {b} head {h} out")
             close(lse[r0:r0 + n, h * group:(h + 1) * group].reshape(-1), l, lt, f"request {b} head {h} lse")
+
+
+def test_windows_and_sinks_past_32_bits(g):
+    """A window or a number of sinks of 2^31 and more covers every position:
+    the answers are those without it.  Sizes of pages that no int32 holds
+    are refused."""
+    rng = np.random.default_rng(31)
+    batch = Batch(rng, [1, 40], [200, 90], 16)
+    _, cache, L = kv_cache(g, rng, batch, 1, 64, "split")
+    q, _ = queries(rng, batch.T, 2, 64)
+    bt, starts, lens = batch.metadata()
+    one = torch.ones(1, device="cuda")
+    call = lambda **kw: g.attention_nvfp4_kv(q, cache, one, one, bt, starts, lens, 200, 0.125, **kw)      # noqa: E731
+    wide = 1 << 30                                           # beyond any position, within int32
+    for kw, same in ((dict(window=(1 << 32) + 8), {}), (dict(window=1 << 31), {}), (dict(window=(1 << 63) - 1, num_sinks=3), {}),
+                     (dict(window=7, num_sinks=1 << 32), dict(window=7, num_sinks=wide)),
+                     (dict(window=1, num_sinks=(1 << 40) + 1), dict(window=1, num_sinks=wide))):
+        assert torch.equal(call(**kw), call(**same)), kw
+    for kw in (dict(window=0), dict(window=-(1 << 32) + 5), dict(window=4, num_sinks=-(1 << 32))):
+        with pytest.raises((ValueError, RuntimeError)):
+            call(**kw)
+    refs = torch.zeros(batch.nb, dtype=torch.int32, device="cuda")
+    for bs in ((1 << 32) + 16, 1 << 31, 0, -16):
+        with pytest.raises((ValueError, RuntimeError)):
+            g.free_requests(bs, bt, lens, refs, lens[:1])
+        with pytest.raises((ValueError, RuntimeError)):
+            g.extend_requests(bs, bt, lens, refs, lens[:1], lens[:1])
