@@ -932,3 +932,26 @@ def test_windows_and_sinks_past_32_bits(g):
             g.free_requests(bs, bt, lens, refs, lens[:1])
         with pytest.raises((ValueError, RuntimeError)):
             g.extend_requests(bs, bt, lens, refs, lens[:1], lens[:1])
+
+
+@pytest.mark.parametrize("hs,rot,inter", [(128, 128, False), (64, 32, True), (256, 96, False), (16, 16, True), (80, 0, False),
+                                          (512, 64, False)])
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-6])
+def test_qk_norm_rope_magnitudes(g, hs, rot, inter, eps):
+    """Heads of every magnitude bf16 has, whose mean square leaves binary32 at
+    either end, beside ordinary ones in the same token; eps may be 0."""
+    rng = np.random.default_rng(hs)
+    T, hq, hk = 6, 7, 2
+    x = rng.standard_normal((T, hq + hk, hs))
+    power = rng.choice([-130, -124, -110, -80, -63, -62, -50, -30, 0, 30, 59, 61, 64, 100, 124], (T, hq + hk, 1))
+    qk, qk64 = ref.bf16(x * 2.0 ** power)
+    qk = qk.cuda()
+    w = [ref.bf16(1 + 0.3 * rng.standard_normal(hs)) for _ in range(2)]
+    pos = rng.integers(0, 30, T)
+    ang = np.arange(30)[:, None] * 3.0 ** -np.arange(rot // 2)
+    table = torch.from_numpy(np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32))
+    cs = table.cuda() if rot else None
+    q, k = g.qk_norm_rope(qk[:, :hq], qk[:, hq:], w[0][0].cuda(), w[1][0].cuda(), dev(pos), cs, eps=eps, interleaved=inter)
+    for out, at, wt, n in ((q, slice(0, hq), w[0][1], "q"), (k, slice(hq, None), w[1][1], "k")):
+        want, tol = ref.norm_rope(qk64[:, at], wt, pos, table.double().numpy(), rot, float(np.float32(eps)), inter)
+        close(out, want, tol, n)
