@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxRequests = int64_t(1) << 22;
+constexpr int64_t kMaxRows = INT32_MAX - 127;   // attention: query tokens x heads, rounded up to tiles of 128 in 32 bits
 std::atomic<int> g_arch_state[kMaxDevices];   // 0 unknown, 1 gfx950, -1 other
 
 int check_device() {
@@ -73,7 +74,7 @@ int attention_args(const gcache_attention_args* a, int32_t hk, int32_t dk, int32
     int64_t rows;
     if (a->num_q_heads <= 0 || hk <= 0 || a->num_q_heads % hk || a->block_size <= 0 ||
         a->block_table_stride <= 0 || a->num_blocks < 0 || a->max_seq_len < 0 || a->workspace_bytes < 0 ||
-        !mul_ok(a->total_q, a->num_q_heads, &rows) || rows > INT32_MAX || a->total_q > INT32_MAX - 1)
+        !mul_ok(a->total_q, a->num_q_heads, &rows) || rows > kMaxRows)
         return GCACHE_ERR_SHAPE;
     int64_t tmp;
     if (!mul_ok(a->block_table_stride, a->block_size, &tmp) || !mul_ok(a->block_table_stride, a->batch_size, &tmp))
@@ -288,7 +289,7 @@ int64_t gcache_attention_workspace_bytes(int64_t total_q, int32_t batch_size, in
                                          int32_t num_kv_heads, int32_t head_size, int64_t max_seq_len, int32_t window,
                                          int32_t num_sinks) {
     if (total_q <= 0 || batch_size <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
-        head_size <= 0 || max_seq_len < 0 || window < 0 || num_sinks < 0 || total_q > INT32_MAX / num_q_heads)
+        head_size <= 0 || max_seq_len < 0 || window < 0 || num_sinks < 0 || total_q > kMaxRows / num_q_heads)
         return 0;
     const int dp = padded_dim(head_size);
     const int32_t dv = head_size > 256 ? kNope : head_size;

@@ -112,7 +112,8 @@ int64_t gcache_attention_workspace_bytes(int64_t total_q, int32_t batch_size, in
  * gcache_reshape_and_cache_nvfp4.
  * Requirements: head_size a multiple of 16, at most 256 (larger:
  * GCACHE_ERR_UNSUPPORTED); num_q_heads a multiple of num_kv_heads;
- * total_q * num_q_heads < 2^31; q, out 16-byte aligned.
+ * total_q * num_q_heads <= 2^31 - 128 (in every attention call); q, out 16-byte
+ * aligned.
  */
 int gcache_attention_nvfp4_kv(const gcache_attention_args* args, const void* kv_cache,
                               const gcache_nvfp4_kv_layout* layout, const float* k_scale,

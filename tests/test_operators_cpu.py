@@ -284,3 +284,17 @@ def test_rows_of_an_output_share_no_element(lib, strides, ok):
     for heads, out in (((H, 0), (ts, st, 0, 0)), ((0, H), (0, 0, ts, st))):      # q's output, k's
         assert lib.gcache_qk_norm_rope(A16, A16, A16, A16, A16, A16, None, None, 0, 0, 0, T, *heads, hs, 0, 0, 1e-6, 256, 64,
                                        256, 64, *out, None) in want
+
+
+@pytest.mark.parametrize("rows", [(1 << 31) - 1, (1 << 31) - 127, (1 << 31) - 128])
+def test_rows_end_before_int32(lib, rows):
+    """The kernels round rows up to tiles of 128 in 32 bits: more than 2^31 -
+    128 rows (tokens x heads) are refused before anything is launched."""
+    import gather_concat_cache_amd as g
+    L = g.nvfp4_kv_split_layout(16, 1, 16)
+    a = _args(total_q=1, num_q_heads=rows, q_head_stride=16, out_head_stride=16, lse_token_stride=rows)
+    if rows > (1 << 31) - 128:
+        assert lib.gcache_attention_nvfp4_kv(C.byref(a), A16, C.byref(L), A16, A16, 1, 16, 0, 0, None) == -2
+        assert lib.gcache_attention_workspace_bytes(1, 1, rows, 1, 16, 1 << 20, 0, 0) == 0
+    elif not torch.cuda.is_available():
+        assert lib.gcache_attention_nvfp4_kv(C.byref(a), A16, C.byref(L), A16, A16, 1, 16, 0, 0, None) in (-4, -5)
