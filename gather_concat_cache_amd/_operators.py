@@ -79,6 +79,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 def _elsewhere(dev, stream):
     """True when a call's stream or device is not the current one: the call is
     then repeated inside _on()."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
     return stream is not None or dev.index != torch.cuda.current_device()
 
 

@@ -298,3 +298,14 @@ def test_rows_end_before_int32(lib, rows):
         assert lib.gcache_attention_workspace_bytes(1, 1, rows, 1, 16, 1 << 20, 0, 0) == 0
     elif not torch.cuda.is_available():
         assert lib.gcache_attention_nvfp4_kv(C.byref(a), A16, C.byref(L), A16, A16, 1, 16, 0, 0, None) in (-4, -5)
+
+
+def test_stream_of_another_device_is_refused():
+    """The kernels run on the device of their tensors: a stream of another one
+    is an error, not a launch on some other stream."""
+    import types
+    from gather_concat_cache_amd import _operators
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    with pytest.raises(ValueError):
+        _operators._elsewhere(torch.device("cuda", 0), other)
+    assert _operators._elsewhere(torch.device("cuda", 1), other)
