@@ -955,3 +955,86 @@ def test_qk_norm_rope_magnitudes(g, hs, rot, inter, eps):
     for out, at, wt, n in ((q, slice(0, hq), w[0][1], "q"), (k, slice(hq, None), w[1][1], "k")):
         want, tol = ref.norm_rope(qk64[:, at], wt, pos, table.double().numpy(), rot, float(np.float32(eps)), inter)
         close(out, want, tol, n)
+
+
+def kv_bytes(flat, L, blk, off, hk, hs):
+    """Views of every data and scale byte of one position, all heads, K and V."""
+    for side in (0, 1):
+        for h in range(hk):
+            base = blk * L.block_stride + side * L.side_stride
+            d = base + L.data_offset + off * L.data_token_stride + h * L.data_head_stride
+            s = base + L.scale_offset + off * L.scale_token_stride + h * L.scale_head_stride
+            yield flat[d:d + hs // 2]
+            yield flat[s:s + hs // 16]
+
+
+@pytest.mark.parametrize("hs,bs,qlens", [(128, 16, [1, 3]), (80, 24, [2, 1]), (256, 16, [1, 2]), (64, 16, [45, 2]),
+                                         (128, 16, [130, 40]), (176, 8, [50, 1])])
+def test_nan_bytes_before_a_window(g, hs, bs, qlens):
+    """Positions of the sequence that the window hides from every row, in tiles
+    that other positions share, hold NaN codes in all bytes: the outputs are
+    those with ordinary bytes there."""
+    rng = np.random.default_rng(hs + bs + 1)
+    window, sinks, lens, hk = 21, 5, [233, 150], 2
+    batch = Batch(rng, qlens, lens, bs)
+    flat, cache, L = kv_cache(g, rng, batch, hk, hs, "split")
+    q, _ = queries(rng, batch.T, 4 * hk, hs)
+    bt, starts, sl = batch.metadata()
+    one = torch.ones(1, device="cuda")
+    call = lambda c: g.attention_nvfp4_kv(q, c, one, one, bt, starts, sl, 233, 0.1, window=window, num_sinks=sinks,     # noqa: E731
+                                          layout=L, return_lse=True)
+    want = call(cache)
+    hidden = 0
+    for b, (n, length) in enumerate(zip(qlens, lens)):
+        for p in np.nonzero(~ref.causal(n, length, window, sinks).any(0))[0]:
+            hidden += 1
+            for x in kv_bytes(flat, L, int(batch.table[b, p // bs]), int(p) % bs, hk, hs):
+                x[:] = 0xFF
+    assert hidden > 150
+    got = call(torch.as_strided(dev(flat), cache.shape, cache.stride()))
+    assert torch.isfinite(got[0]).all() and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("hs,bs", [(128, 16), (80, 24), (256, 16)])
+@pytest.mark.parametrize("n", [5, 40])
+def test_nan_bytes_of_hidden_drafts(g, hs, bs, n):
+    """Drafted tokens that no row's mask names, per-head cache."""
+    rng = np.random.default_rng(hs + n)
+    batch = Batch(rng, [n], [70 + n], bs)
+    flat, cache, L = kv_cache(g, rng, batch, 1, hs, "split")
+    q, _ = queries(rng, n, 4, hs)
+    bt, starts, sl = batch.metadata()
+    one = torch.ones(1, device="cuda")
+    mask = rng.random((n, n)) < 0.6
+    mask[:, 1::3] = False
+    call = lambda c: g.tree_attention_nvfp4_kv(q, c, one, one, bt, starts, sl, dev(mask), 110, 0.1, layout=L,      # noqa: E731
+                                               return_lse=True)
+    want = call(cache)
+    for p in range(71, 70 + n, 3):
+        for x in kv_bytes(flat, L, int(batch.table[0, p // bs]), p % bs, 1, hs):
+            x[:] = 0xFF
+    got = call(torch.as_strided(dev(flat), cache.shape, cache.stride()))
+    assert torch.isfinite(got[0]).all() and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("bs", [64, 40])
+@pytest.mark.parametrize("n,heads", [(4, 4), (9, 2), (20, 8)])
+def test_nan_bytes_of_hidden_latent_drafts(g, bs, n, heads):
+    """The same over the latent cache, RoPE bytes too, in the kernel for few rows and the one for many."""
+    rng = np.random.default_rng(bs + n)
+    batch = Batch(rng, [n], [75 + n], bs)
+    flat = np.full((batch.nb, bs, 352), 0xFF, np.uint8)
+    for p in range(75 + n):
+        e = flat[batch.table[0, p // bs], p % bs]
+        e[:256], e[320:352] = fp4_bytes(rng, 256), scale_bytes(rng, 32)
+        e[256:320] = rng.integers(0, 0x48, 64, dtype=np.uint8)
+    q, _ = queries(rng, n, heads, 576)
+    bt, starts, sl = batch.metadata()
+    mask = rng.random((n, n)) < 0.6
+    mask[:, 1::3] = False
+    call = lambda: g.tree_attention_nvfp4_ds_mla(q, dev(flat), bt, starts, sl, dev(mask), 100, 0.07, return_lse=True)       # noqa: E731
+    want = call()
+    for p in range(76, 75 + n, 3):
+        flat[batch.table[0, p // bs], p % bs] = 0xFF
+    got = call()
+    assert torch.isfinite(got[0]).all() and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
