@@ -69,7 +69,7 @@ struct QkNormRopeParams {
     int32_t cs_bf16;
     float eps;
     int64_t num_tokens;
-    int32_t waves_per_token;     // set by the launcher, as is
+    int32_t waves_per_token, sets;   // set by the launcher, as is
     float inv_hs;
 };
 hipError_t launch_qk_norm_rope(const QkNormRopeParams& p, hipStream_t s);

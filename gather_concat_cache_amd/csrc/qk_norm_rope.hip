@@ -17,7 +17,14 @@
 
 namespace gcache {
 
-constexpr int kHeadSets = 5;     // heads a lane works on: 40 heads of 128 values fill two waves
+// A set is the heads that one load of a wave holds (4 of 128 values).  A token
+// takes as few waves as hold its sets at kHeadSets each, and the sets are dealt
+// evenly, so that fewer of them than waves stay empty.
+// At most 4, 5, 6 and 8 sets, 16384 tokens (us): 28 + 4 heads of 128 70.0,
+// 70.1, 70.2, 71.5; 32 + 8 93.0, 85.1, 85.0, 92.1; 64 + 8 156.8, 152.7, 145.0,
+// 158.2; 16 + 2 36.6, 32.6, 32.6, 35.5; 16 + 16 of 64 29.1, 29.2, 29.3, 30.4; 4096
+// tokens of 16 + 2 of 512 32.1, 31.6, 30.5, 31.6.  (Always 5, uneven: 28 + 4 72.1.)
+constexpr int kHeadSets = 6;
 
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
@@ -102,8 +109,8 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
     const int64_t token = wave / p.waves_per_token;
     if (token >= p.num_tokens) return;
     const int sub = lane & (LPH - 1), dim = 8 * sub;     // the lane's values dim .. dim + 7
-    const int head0 = (int)(wave - token * p.waves_per_token) * (kHeadSets * HPW) + (lane >> SH);
-    const int total = p.heads[0] + p.heads[1];
+    const int first = (int)(wave - token * p.waves_per_token) * (p.sets * HPW), head0 = first + (lane >> SH);
+    const int end = min(p.heads[0] + p.heads[1], first + p.sets * HPW);  // behind the wave's heads
     const bool in_dim = dim < p.hs;
     const int64_t pos = p.rot > 0 ? p.positions[token] : 0;
 
@@ -112,7 +119,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
     for (int u = 0; u < kHeadSets; u++) {
         const int h = head0 + u * HPW;
         x[u] = make_uint4(0, 0, 0, 0);
-        if (h < total && in_dim) {
+        if (h < end && in_dim) {
             const int kk = h >= p.heads[0];
             x[u] = *reinterpret_cast<const uint4*>(p.x[kk] + token * p.x_ts[kk] +
                                                   (int64_t)(h - (kk ? p.heads[0] : 0)) * p.x_hs[kk] + dim);
@@ -156,6 +163,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
     }
 #pragma unroll
     for (int u = 0; u < kHeadSets; u++) {
+        if (u >= p.sets) break;
         const int h = head0 + u * HPW;
         const int kk = h >= p.heads[0];
         uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
@@ -180,7 +188,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
 #pragma unroll
             for (int i = 0; i < 4; i++)
                 pw[i] = (uint32_t)__shfl((int)xw[i], (lane & ~(LPH - 1)) | (partner & (LPH - 1)));
-        if (h >= total || !in_dim) continue;
+        if (h >= end || !in_dim) continue;
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) y[i] = v[i] * inv * (kk ? w[1][i] : w[0][i]);
@@ -210,8 +218,10 @@ __global__ __launch_bounds__(kBlockThreads) void k_qk_norm_rope(QkNormRopeParams
 template <int SH>
 static hipError_t launch_lanes(const QkNormRopeParams& in, hipStream_t s) {
     QkNormRopeParams p = in;
-    const int per_wave = kHeadSets * (64 >> SH);
-    p.waves_per_token = (p.heads[0] + p.heads[1] + per_wave - 1) / per_wave;
+    // as few waves as hold the token's heads, each with as many sets as the others
+    const int sets = (p.heads[0] + p.heads[1] + (64 >> SH) - 1) / (64 >> SH);
+    p.waves_per_token = (sets + kHeadSets - 1) / kHeadSets;
+    p.sets = (sets + p.waves_per_token - 1) / p.waves_per_token;
     p.inv_hs = 1.0f / (float)p.hs;
     const int64_t wgs = (p.num_tokens * p.waves_per_token + kWavesPerBlock - 1) / kWavesPerBlock;
     auto k = p.interleaved ? (p.cs_bf16 ? k_qk_norm_rope<SH, true, true> : k_qk_norm_rope<SH, true, false>)

@@ -1038,3 +1038,21 @@ def test_nan_bytes_of_hidden_latent_drafts(g, bs, n, heads):
         flat[batch.table[0, p // bs], p % bs] = 0xFF
     got = call()
     assert torch.isfinite(got[0]).all() and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 0), (4, 1), (20, 3), (23, 1), (24, 1), (25, 0), (28, 4), (40, 9), (49, 24), (97, 2)])
+def test_qk_norm_rope_head_counts(g, hq, hk):
+    """Head counts around what one, two and more waves of a token hold, in place:
+    every head is normed once."""
+    rng = np.random.default_rng(hq)
+    T, hs = 5, 128
+    qk, qk64 = ref.bf16(rng.standard_normal((T, hq + hk, hs)))
+    qk = qk.cuda()
+    w, w64 = ref.bf16(1 + 0.3 * rng.standard_normal(hs))
+    ang = np.arange(9)[:, None] * 2.0 ** -np.arange(hs // 2)
+    table = np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+    pos = rng.integers(0, 9, T)
+    q, k = qk[:, :hq], qk[:, hq:] if hk else None
+    g.qk_norm_rope(q, k, w.cuda(), w.cuda() if hk else None, dev(pos), dev(table), eps=1e-6, q_out=q, k_out=k)
+    want, tol = ref.norm_rope(qk64, w64, pos, table.astype(np.float64), hs, float(np.float32(1e-6)), False)
+    close(qk, want, tol, "q and k")
