@@ -145,11 +145,13 @@ __device__ __forceinline__ int scan_lanes(int x) {
     return x;
 }
 
-// Key splits of a request: as many as its length gives in pieces of `chunk`
-// 32-key tiles (a multiple of 4), at least one.
+// 32-key tiles of a request, as far as the plan counts them: at most key_tiles,
+// the bound from max_seq_len and the window.
 __device__ __forceinline__ int request_work(const AttnParams& p, int b) {
     return min((int)(((uint32_t)max(p.seq_lens[b], 0) + kTileKeys - 1) / kTileKeys), p.key_tiles);
 }
+// Key splits of a request: as many pieces of `chunk` 32-key tiles (a multiple
+// of 4) as its counted tiles give, at least one.
 __device__ __forceinline__ int request_splits(int work, int chunk) { return max(1, (work + chunk - 1) / chunk); }
 
 // What work unit `unit` of a kv head is.  The host knows the packed rows and
@@ -433,7 +435,7 @@ __device__ __forceinline__ void load_query(const AttnParams& p, const RowTile& t
 // A row at position pos sees the keys <= hi that are > lo or sinks, and of a
 // tree's drafted tokens those that its mask names.
 template <bool TREE>
-__device__ __forceinline__ int sight_hi(const AttnParams& p, const RowTile& t, int pos) {
+__device__ __forceinline__ int sight_hi(const RowTile& t, int pos) {
     return pos < 0 ? -1 : TREE ? t.kv_len - 1 : min(pos, t.kv_len - 1);
 }
 __device__ __forceinline__ int sight_lo(const AttnParams& p, int pos) {
@@ -452,7 +454,7 @@ __device__ __forceinline__ uint32_t keys_upto(int last, int key0) {
 template <bool TREE, int H>
 __device__ __forceinline__ void hide(const AttnParams& p, const RowTile& t, int pos, int tok, int key0, uint32_t live,
                                      f32x4* x) {
-    uint32_t see = live & keys_upto<H>(sight_hi<TREE>(p, t, pos), key0);
+    uint32_t see = live & keys_upto<H>(sight_hi<TREE>(t, pos), key0);
     if (TREE) {
         // drafted keys: their byte in the row's mask, four loads at a time
         const uint8_t* row = p.mask + (int64_t)tok * p.mask_ts;

@@ -116,8 +116,9 @@ __device__ __forceinline__ void attend_rows(const AttnParams& p, const RowTile& 
     }
     const LaneParts<UNI> lo = lane_parts<DP, UNI>(p, kvh, lane);
     // Steps of 64 keys: the tiles [v0, v1) are runs of sink tiles and window
-    // tiles; a step covers two consecutive tile numbers of one run.  Keys of a
-    // step behind its run (or behind v1) are hidden by `end`.
+    // tiles; a step covers two consecutive tile numbers of one run, or the run's
+    // last one alone: then its upper 32 keys are hidden as if their pages did not
+    // exist (the mask lv), for the next run may hold them, or another split.
     const auto step_key = [&](int v) { return (v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0) * kTileKeys; };
     const auto run_end = [&](int v) { return v < t.sink_tiles ? min(t.sink_tiles, v1) : v1; };
     Share<DP> raw;

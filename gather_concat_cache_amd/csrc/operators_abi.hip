@@ -68,7 +68,7 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t token_stride, int64_t hea
 int padded_dim(int32_t head_size) { return head_size <= 64 ? 64 : head_size <= 128 ? 128 : head_size <= 256 ? 256 : 512; }
 
 // Checks shared by the attention calls, and the parameters they fill.
-int attention_args(const gcache_attention_args* a, int32_t hk, int32_t dk, int32_t dv, AttnParams* p) {
+int attention_args(const gcache_attention_args* a, int32_t hk, int32_t dv, AttnParams* p) {
     if (a->total_q < 0 || a->batch_size < 0) return GCACHE_ERR_SHAPE;
     if (!a->q || !a->out || !a->query_starts || !a->seq_lens || !a->block_table) return GCACHE_ERR_NULL;
     int64_t rows;
@@ -91,7 +91,6 @@ int attention_args(const gcache_attention_args* a, int32_t hk, int32_t dk, int32
     if (!rows_apart(a->total_q, a->num_q_heads, a->out_token_stride, a->out_head_stride, dv) ||
         (a->lse && a->total_q > 1 && a->lse_token_stride < a->num_q_heads))
         return GCACHE_ERR_SHAPE;
-    (void)dk;
     p->q = static_cast<const uint16_t*>(a->q);
     p->out = static_cast<uint16_t*>(a->out);
     p->lse = a->lse;
@@ -146,7 +145,7 @@ int kv_attention(const gcache_attention_args* a, const void* kv_cache, const gca
     if (hs <= 0 || hs % 16 || window < 0 || sinks < 0) return GCACHE_ERR_SHAPE;
     if (hs > 256) return GCACHE_ERR_UNSUPPORTED;
     AttnParams p;
-    int rc = attention_args(a, hk, hs, hs, &p);
+    int rc = attention_args(a, hk, hs, &p);
     if (rc) return rc;
     const int64_t v[8] = {L->data_offset, L->data_token_stride, L->data_head_stride, L->scale_offset,
                           L->scale_token_stride, L->scale_head_stride, L->side_stride, L->block_stride};
@@ -326,7 +325,7 @@ int gcache_tree_attention_nvfp4_ds_mla(const gcache_attention_args* a, const voi
     if (!kv_cache && a->num_blocks > 0) return GCACHE_ERR_NULL;
     if (tree_mask && (mask_columns < 0 || tree_mask_stride < mask_columns)) return GCACHE_ERR_SHAPE;
     AttnParams p;
-    int rc = attention_args(a, 1, kRow, kNope, &p);
+    int rc = attention_args(a, 1, kNope, &p);
     if (rc) return rc;
     int64_t need;
     if (entry_stride < kNvEntry || !mul_ok(a->block_size, entry_stride, &need) || block_stride < need ||
