@@ -1056,3 +1056,36 @@ def test_qk_norm_rope_head_counts(g, hq, hk):
     g.qk_norm_rope(q, k, w.cuda(), w.cuda() if hk else None, dev(pos), dev(table), eps=1e-6, q_out=q, k_out=k)
     want, tol = ref.norm_rope(qk64, w64, pos, table.astype(np.float64), hs, float(np.float32(1e-6)), False)
     close(qk, want, tol, "q and k")
+
+
+@pytest.mark.parametrize("requests,length", [(3, 40), (2, 1700), (1025, 20)])
+@pytest.mark.parametrize("hs", [64, 576])
+def test_rows_before_the_first_request(g, requests, length, hs):
+    """query_starts that begin behind row 0: the rows before are left as they
+    were, for short, split and large batches."""
+    rng = np.random.default_rng(requests)
+    before, n, heads = 37, 2, 2
+    batch = Batch(rng, [n] * requests, [length] * requests, 16)
+    bt, starts, lens = batch.metadata()
+    q, q64 = queries(rng, before + batch.T, heads, hs)
+    scale, dv = 0.0625, min(hs, 512)
+    kw = dict(out=torch.full((before + batch.T, heads, dv), 7.0, dtype=torch.bfloat16, device="cuda"),
+              lse=torch.full((before + batch.T, heads), 7.0, device="cuda"))
+    if hs == 576:
+        flat = rng.integers(0, 0x38, (batch.nb, 16, 352), dtype=np.uint8)
+        g.tree_attention_nvfp4_ds_mla(q, dev(flat), bt, starts + before, lens, None, length, scale, **kw)
+    else:
+        flat, one = rng.integers(0, 0x38, (batch.nb, 2, 16, 1, hs // 2 + hs // 16), dtype=np.uint8), torch.ones(1, device="cuda")
+        g.attention_nvfp4_kv(q, dev(flat), one, one, bt, starts + before, lens, length, scale, **kw)
+    assert (kw["out"][:before] == 7).all() and (kw["lse"][:before] == 7).all()
+    see = np.repeat(ref.causal(n, length), heads, 0)
+    for b in {0, requests // 2, requests - 1}:
+        row = batch.table[b]
+        if hs == 576:
+            k, v, _ = ref.mla_positions(flat.reshape(-1), row, length, 16, batch.nb, 16 * 352, 352)
+        else:
+            k, v, _ = ref.kv_positions(flat.reshape(-1), g.nvfp4_kv_split_layout(16, 1, hs), row, length, 16, batch.nb, 0, hs)
+        at = slice(before + n * b, before + n * (b + 1))
+        o, l, ot, lt = ref.attend(q64[at].reshape(-1, hs), k, v, see, scale)
+        close(kw["out"][at].reshape(-1, dv), o, ot, f"request {b} out")
+        close(kw["lse"][at].reshape(-1), l, lt, f"request {b} lse")
