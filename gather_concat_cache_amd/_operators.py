@@ -436,8 +436,10 @@ def _status(status, n, dev):
 
 def copy_pages(caches, src, dst, stream=None):
     """Copy pages src[i] -> dst[i] (int32 vectors) in every cache: a tensor
-    [num_blocks, ...] or a sequence of such tensors of one geometry.
-    Destinations are distinct and none is a source."""
+    [num_blocks, ...] or a sequence of such tensors of one geometry.  A page
+    goes from its first element to its last, padding between them included
+    (for forks and compaction too); bytes between pages stay.  Destinations
+    are distinct and none is a source."""
     pc, _keep, nb, dev = _page_caches(caches)
     if _elsewhere(dev, stream):
         with _on(dev, stream):

@@ -21,7 +21,7 @@ namespace gcache {
 // maxima and writes the weights again (two more barriers, rare).
 // Bound by instruction issue around the two products, about 230 registers a lane
 // (Q 72, O 64, raw bytes and operands) allowing one workgroup a CU: 32 x 32
-// tokens of 16 heads over 8192 keys 457 us, 640 TFLOP/s.  (Running the values of
+// tokens of 16 heads over 8192 keys 433 us, 675 TFLOP/s.  (Running the values of
 // a step between the scores of the next took 5 per cent longer.)
 // ---------------------------------------------------------------------------
 constexpr int kLatentWaves = 8, kLatentRows = 64;
@@ -238,8 +238,9 @@ __global__ __launch_bounds__(kLatentWaves * kWave, 2) void k_attention_latent(At
 // adds dims 128 w .. 128 w + 127 of all 64 keys.  A wave so holds 32
 // accumulator registers instead of 128, and two workgroups fit a CU: one's
 // loads and barriers pass under the other's conversions.  128 x 1 token of 16
-// heads over 8192 keys: 117 us, 3.2 TB/s; bound by HBM and the conversions,
-// 1088 values for 352 bytes.  (Waves with 32 keys each for themselves, as in
+// heads over 8192 keys: 116 us, 3.2 TB/s of the 7 that a plain stream of reads
+// reaches; beside the loads, in pieces of 16 bytes down to one, the conversions
+// of 1088 values for 352 bytes.  (Waves with 32 keys each for themselves, as in
 // the per-head form, took 11 per cent longer.)  The query is converted once,
 // a quarter of its fragments by each wave: 2 us less for a single short call.
 // ---------------------------------------------------------------------------

@@ -1,11 +1,12 @@
 // attention_few.h -- attention of few query rows (one token to a few drafted
 // ones): the four waves of a workgroup share 16 * R query rows, take every
 // fourth 32-key tile of the workgroup's key range straight into registers and
-// join through LDS.  Bound by HBM for long contexts: each wave has a tile's
-// bytes in flight while it works on another (64 x 1 token over 8192 keys, 8
-// kv heads of 128: 169 us, 3.6 TB/s of the 4.85 that a large copy reaches); for
-// short ones by the chain of dependent loads and the launches (1038 keys in 9
-// splits: 8 us and 5 for the join).
+// join through LDS.  Long contexts are bound by memory: each wave has a tile's
+// bytes in flight while it works on another, but reads them in pieces of 64
+// bytes a key and one byte a scale (64 x 1 token over 8192 keys, 8 kv heads of
+// 128: 172 us, 3.5 TB/s; a plain stream of reads reaches 7).  Short ones are
+// bound by the chain of dependent loads and the launches (8 tokens over 1029
+// keys, split: 11 us, and 4 for the join).
 #pragma once
 
 #include <type_traits>
@@ -49,7 +50,8 @@ struct LaneParts {
 // so that a group's address is wave-uniform; the others take any head size up
 // to DP (dims behind head_size read the row's first bytes with a zero scale)
 // and look up every key's page.  The general form on a UNI call: 64 x 1 token
-// over 8192 keys 240 us against 169, prefill 4 x 2048 975 against 512.
+// over 8192 keys 219 us against 172, 16 x 8 74 against 48, prefill 4 x 2048
+// 1050 against 510.
 template <int DP, bool UNI>
 __device__ __forceinline__ LaneParts<UNI> lane_parts(const AttnParams& p, int kvh, int lane) {
     const int c = lane & 15, g = lane >> 4;

