@@ -3,7 +3,7 @@ for AMD Instinct MI355X (gfx950), with the attention that reads the pages in
 place, the norm and rotation before the write, and the ownership of pages.
 
 The computation lives in libgcache.so (hand-written HIP kernels behind the C
-ABI of include/gcache.h, gcache_attention.h and gcache_pages.h); this package only marshals torch tensors (device
+ABI of the headers in include/); this package only marshals torch tensors (device
 memory and streams) into those calls.  Each function is exported under the
 C name and under the C name without the ``gcache_`` prefix.
 """
@@ -16,6 +16,7 @@ from ._native import (FP8_DS_MLA, LIB_PATH, NVFP4_DS_MLA, GcacheError, NvFp4KvLa
                       reshape_and_cache_nvfp4, time_next_launch)
 from ._operators import (attention_nvfp4_kv, compact_pages, copy_pages, extend_requests, fork_requests, free_requests,
                          qk_norm_rope, tree_attention_nvfp4_ds_mla, tree_attention_nvfp4_kv)
+from ._serving import attention_fp8_kv, prompt_attention, rope_append_fp8_kv
 
 __all__ = [
     "NVFP4_DS_MLA", "FP8_DS_MLA", "LIB_PATH", "GcacheError", "NvFp4KvLayout", "load",
@@ -25,6 +26,7 @@ __all__ = [
     "reshape_and_cache_nvfp4", "gather_upconvert_nvfp4_kv",
     "context_chunks", "gather_context_chunked", "convert_req_index_to_global_index", "time_next_launch",
     "qk_norm_rope", "attention_nvfp4_kv", "tree_attention_nvfp4_kv", "tree_attention_nvfp4_ds_mla",
+    "rope_append_fp8_kv", "attention_fp8_kv", "prompt_attention",
     "copy_pages", "fork_requests", "extend_requests", "free_requests", "compact_pages",
 ]
 
@@ -50,6 +52,9 @@ gcache_fork_requests = fork_requests
 gcache_extend_requests = extend_requests
 gcache_free_requests = free_requests
 gcache_compact_pages = compact_pages
+gcache_rope_append_fp8_kv = rope_append_fp8_kv
+gcache_attention_fp8_kv = attention_fp8_kv
+gcache_prompt_attention = prompt_attention
 __all__ += [n for n in list(globals()) if n.startswith("gcache_")]
 
 load()   # fail at import time when libgcache.so has not been built

@@ -210,7 +210,8 @@ def _norm_side(x, w, y, name, T, hs, dev):
 # attention
 # ---------------------------------------------------------------------------
 def _attention(fn, extra, q, dk, dv, hk, num_blocks, block_size, block_table, query_starts, seq_lens, max_seq_len,
-               softmax_scale, window, sinks, out, lse, return_lse, workspace, dev):
+               softmax_scale, window, sinks, out, lse, return_lse, workspace, dev,
+               scratch="gcache_attention_workspace_bytes"):
     """Checks the shared tensors, marshals gcache_attention_args and calls
     `fn`(args, *extra, stream)."""
     _want(q, _BF16, "q", dev)
@@ -255,7 +256,7 @@ def _attention(fn, extra, q, dk, dv, hk, num_blocks, block_size, block_table, qu
         lib = _load()
         nbytes = 0
         if workspace is None:
-            nbytes = lib.gcache_attention_workspace_bytes(T, B, hq, hk, dk, max_seq_len, window, sinks)
+            nbytes = getattr(lib, scratch)(T, B, hq, hk, dk, max_seq_len, window, sinks)
         workspace, nbytes = _scratch(workspace, nbytes, dev)
         a = AttentionArgs(q.data_ptr(), out.data_ptr(), lse_ptr, qs[0], qs[1], os[0], os[1], lse_ts,
                           query_starts.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), block_table.shape[1], T,

@@ -21,14 +21,16 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgcache.so")
 SOURCES = ["ds_mla_kernels.hip", "nvfp4_kv_kernels.hip", "sparse_index.hip", "gcache_abi.hip"]
-# the operators around the cache (include/gcache_attention.h, include/gcache_pages.h)
-OPERATOR_SOURCES = ["attention_kv.hip", "attention_ds_mla.hip", "attention_plan.hip", "qk_norm_rope.hip", "page_kernels.hip", "operators_abi.hip"]
+# the operators around the caches (the other headers of include/)
+OPERATOR_SOURCES = ["attention_kv.hip", "attention_ds_mla.hip", "attention_fp8_kv.hip", "prompt_attention.hip", "attention_plan.hip",
+                    "qk_norm_rope.hip", "rope_append.hip", "page_kernels.hip", "operators_abi.hip"]
 # measurement helper beside the library (include/gcache_bench.h), loaded by bench.py only
 BENCH_LIB = os.path.join(PKG, "libgcache_bench.so")
 BENCH_SOURCES = ["bench_ceiling.hip"]
 HEADERS = ["gcache_device.h", "gcache_internal.h"]
-OPERATOR_HEADERS = ["gcache_operators.h", "attention_device.h", "attention_few.h"]
-PUBLIC_HEADERS = ["gcache.h", "gcache_attention.h", "gcache_pages.h"]
+OPERATOR_HEADERS = ["gcache_operators.h", "attention_device.h", "attention_join.h", "attention_few.h", "attention_tiles.h",
+                    "fp8_scale.h"]
+PUBLIC_HEADERS = ["gcache.h", "gcache_attention.h", "gcache_fp8_kv.h", "gcache_prompt.h", "gcache_pages.h"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

@@ -55,7 +55,7 @@ constexpr int kTileKeys = 32;
 // below 2^(kShift + kLag) = 2^14.
 constexpr float kShift = 6.0f, kLag = 8.0f;
 constexpr float kNegInf = -__builtin_inff();
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 // Zero every byte of x that holds the e4m3 NaN code (0x7F or 0xFF).
 __device__ __forceinline__ uint32_t drop_nan_e4m3x4(uint32_t x) {
@@ -112,13 +112,33 @@ __device__ __forceinline__ int query_start(const AttnParams& p, int b) {
     return min(max(v, 0), p.total_q);
 }
 
+// What the two sources of keys differ in: the keys of a request, the most that
+// can be addressed, and the position of a request's first query.
+__device__ __forceinline__ int key_count(const AttnParams& p, int b) { return max(p.seq_lens[b], 0); }
+__device__ __forceinline__ int64_t addressable_keys(const AttnParams& p) {
+    return p.blocks > 0 ? min(p.bt_stride * p.div.size, (int64_t)INT32_MAX - 2 * kTileKeys) : 0;
+}
+__device__ __forceinline__ int first_position(const AttnParams&, int keys, int qlen) {
+    return keys - qlen;          // may be negative: those rows see nothing
+}
+// Packed prompts: request b's keys are rows ks[b] .. ks[b + 1] - 1.  Without the
+// causal order every query stands behind the last key.
+__device__ __forceinline__ int key_start(const PromptParams& p, int b) { return min(max(p.ks[b], 0), p.total_k); }
+__device__ __forceinline__ int key_count(const PromptParams& p, int b) {
+    return max(key_start(p, b + 1) - key_start(p, b), 0);
+}
+__device__ __forceinline__ int64_t addressable_keys(const PromptParams&) { return INT32_MAX - 2 * kTileKeys; }
+__device__ __forceinline__ int first_position(const PromptParams& p, int keys, int qlen) {
+    return p.causal ? keys - qlen : keys;
+}
+
 // Visible 32-key tiles of rows [row0, row0 + rows) of request b.
-__device__ __forceinline__ void tile_range(const AttnParams& p, RowTile& t) {
+template <typename P>
+__device__ __forceinline__ void tile_range(const P& p, RowTile& t) {
     // key numbers stay clear of int32's end, so key0 + 32 cannot wrap
-    const int64_t table_keys =
-        p.blocks > 0 ? min(p.bt_stride * p.div.size, (int64_t)INT32_MAX - 2 * kTileKeys) : 0;
-    const int seq = max(p.seq_lens[t.b], 0);
-    t.ctx = seq - t.qlen;        // may be negative: those rows see nothing
+    const int64_t table_keys = addressable_keys(p);
+    const int seq = key_count(p, t.b);
+    t.ctx = first_position(p, seq, t.qlen);
     t.kv_len = (int)min((int64_t)seq, table_keys);
     const int p0 = t.ctx + t.row0 / p.group;
     const int p1 = t.ctx + (t.row0 + t.rows - 1) / p.group;
@@ -147,8 +167,9 @@ __device__ __forceinline__ int scan_lanes(int x) {
 
 // 32-key tiles of a request, as far as the plan counts them: at most key_tiles,
 // the bound from max_seq_len and the window.
-__device__ __forceinline__ int request_work(const AttnParams& p, int b) {
-    return min((int)(((uint32_t)max(p.seq_lens[b], 0) + kTileKeys - 1) / kTileKeys), p.key_tiles);
+template <typename P>
+__device__ __forceinline__ int request_work(const P& p, int b) {
+    return min((int)(((uint32_t)key_count(p, b) + kTileKeys - 1) / kTileKeys), p.key_tiles);
 }
 // Key splits of a request: as many pieces of `chunk` 32-key tiles (a multiple
 // of 4) as its counted tiles give, at least one.
@@ -179,7 +200,8 @@ __device__ __forceinline__ int request_splits(int work, int chunk) { return max(
 __host__ __device__ __forceinline__ bool counts_requests(int batch, int kv_heads) {
     return batch <= 256 || (batch <= 512 && batch * kv_heads <= 512);
 }
-__device__ __forceinline__ bool find_tile(const AttnParams& p, int64_t unit, int RT, RowTile& t) {
+template <typename P>
+__device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowTile& t) {
     const int lane = lane_id();
     const auto tiles_of = [&](int rows) { return (max(rows, 0) + RT - 1) / RT; };
     int index, before;

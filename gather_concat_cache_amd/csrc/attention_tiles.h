@@ -1,0 +1,708 @@
+// attention_tiles.h -- attention of many query rows over keys and values that
+// reach the matrix instructions through LDS as they lie in memory: bf16 rows
+// of packed prompts, or e4m3 rows of a paged cache.
+//
+// Four waves share a stream of 64-key steps; a wave has 32 query rows (query
+// token x head of the group) of a 128-row tile.
+//   S^T = K Q^T    32x32x16: matrix rows are keys, columns query rows;
+//   O^T = V^T P^T  32x32x16: matrix rows are value dims.
+// A result lane (column l % 32, half h = l / 32) holds the keys 8 a + 4 h + i
+// (a, i < 4) of a 32-key tile: registers 8 s .. 8 s + 7 are the k-operand of
+// the second product's 16-key step s when V's operand takes its 8 k-slots as
+// keys 16 s + 4 h + i and 16 s + 8 + 4 h + i.  So weights stay in their lane,
+// row statistics are per column, and V's transposition is done by the LDS
+// transpose reads, whose lanes name any 4 (bf16) or 8 (e4m3) rows.
+//
+// Loads go from memory straight to LDS (16 bytes a lane, a wave's 1 KiB in
+// one piece), double buffered: step i + 1 is in flight while step i is
+// multiplied.  A lane's place in LDS is fixed, so rows are swizzled by which
+// 16-byte chunk of a row a lane asks for: chunk ^ f(row) with f chosen so
+// that the lanes that LDS serves in one clock (8 of a 16-byte read, 16 of a
+// transpose read) fall into distinct banks.
+#pragma once
+
+#include <type_traits>
+
+#include "attention_join.h"
+#include "fp8_scale.h"
+
+namespace gcache {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kStep = 64, kTileWaves = 4, kTileRows = 128;   // keys of a step, waves, rows of a tile
+
+// One load from memory to LDS: 16 bytes a lane, lane l's to `lds` + 16 l.  The
+// instruction has no register result; its end is counted by vmcnt, and the
+// kernels wait for it themselves (tile_ready), because the compiler would make
+// every read of any LDS buffer wait for the newest load.  m0 needs a wait state
+// before an LDS load uses it.
+__device__ __forceinline__ void load_lds(uint32_t lds, const void* base, uint32_t offset) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 : : "s"(lds), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void load_lds(uint32_t lds, const void* lane_address) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 : : "s"(lds), "v"(lane_address) : "memory");
+}
+// Every wave's loads have landed and every wave's reads are done.
+__device__ __forceinline__ void tile_ready() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" : : : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// Which chunk of its row stands at chunk c (of NC) of LDS row r: c ^ swizzle.
+// Keys are read 16 bytes a lane, 32 rows side by side.
+template <int NC>
+__device__ __forceinline__ int key_swizzle(int r) {
+    return NC == 4 ? (r >> 1) & 3 : r & 7;
+}
+// bf16 values: a transpose read takes rows 4 n .. 4 n + 3, two chunks each.
+// e4m3 values: rows 4 n + i and 4 n + 8 + i, one chunk each.
+template <int NC, bool FP8>
+__device__ __forceinline__ int value_swizzle(int r) {
+    if (!FP8) return (r & 3) << 1;
+    return NC == 4 ? (r >> 1 & 1) | (r >> 2 & 2) : (r & 3) | (r >> 1 & 4);
+}
+
+// What differs between the two sources.
+struct PackedBf16 {
+    typedef bf16x8 frag;
+    static constexpr bool kFp8 = false;
+    static constexpr int kBytes = 2;
+    static constexpr float kShiftUp = 0.0f;              // bf16 weights have binary32's range
+    static __device__ __forceinline__ f32x16 mma(const frag& a, const frag& b, const f32x16& c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+struct PagedFp8 {
+    typedef f16x8 frag;
+    static constexpr bool kFp8 = true;
+    static constexpr int kBytes = 1;
+    static constexpr float kShiftUp = kShift;
+    static __device__ __forceinline__ f32x16 mma(const frag& a, const frag& b, const f32x16& c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+// First of the 8 dims that lane half h holds in step st of the first product.
+template <typename T>
+__device__ __forceinline__ int step_dim(int st, int h) {
+    return T::kFp8 ? 32 * (st >> 1) + 16 * h + 8 * (st & 1) : 16 * st + 8 * h;
+}
+
+__device__ __forceinline__ f16x8 fp8_operand(uint32_t x, uint32_t y) { return rope_operand(x, y); }
+
+// Over the two lanes of a column.
+__device__ __forceinline__ float pair_max(float v) {
+    const u32x2 b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b.x), __uint_as_float(b.y));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+    const u32x2 b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b.x) + __uint_as_float(b.y);
+}
+
+// Bit 4 a + i: the lane's key key0 + 8 a + i (a < 8, i < 4; key0 counts the
+// lane half) is <= last.
+__device__ __forceinline__ uint32_t step_keys_upto(int last, int key0) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int a = 0; a < 8; a++) bits |= ((1u << min(max(last - key0 + 1 - 8 * a, 0), 4)) - 1) << (4 * a);
+    return bits;
+}
+
+__device__ __forceinline__ float max16(const f32x16& a) {
+    const float x = max3(max3(a[0], a[1], a[2]), a[3], a[4]), y = max3(max3(a[5], a[6], a[7]), a[8], a[9]);
+    return fmaxf(max3(x, max3(a[10], a[11], a[12]), a[13]), max3(y, a[14], a[15]));
+}
+
+// hide() of one row for a 64-key step: bit 4 a + i of live, and the logits, as
+// step_keys_upto counts.  Returns which keys the row sees.
+template <bool TREE>
+__device__ __forceinline__ uint32_t hide_step(const AttnParams& p, const RowTile& t, int pos, int tok, int key0, uint32_t live,
+                                          f32x16* x) {
+    uint32_t see = live & step_keys_upto(sight_hi<TREE>(t, pos), key0);
+    if (TREE) {
+        const uint8_t* row = p.mask + (int64_t)tok * p.mask_ts;
+        uint32_t named = 0;
+#pragma unroll 1
+        for (int a = 0; a < 8; a++) {
+            const int d0 = key0 + 8 * a - t.ctx;
+            uint32_t byte[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                byte[i] = (see >> (4 * a + i) & 1) && d0 + i >= 0 && d0 + i < p.mask_cols ? row[d0 + i] : 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++) named |= (uint32_t)(byte[i] != 0) << (4 * a + i);
+        }
+        see &= step_keys_upto(t.ctx - 1, key0) | named;
+    } else if (p.window > 0) {
+        see &= ~step_keys_upto(sight_lo(p, pos), key0) | step_keys_upto(p.sinks - 1, key0);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j++) x[j >> 4][j & 15] = see >> j & 1 ? x[j >> 4][j & 15] : kNegInf;
+    return see;
+}
+
+// Where a step's rows come from.  Packed prompts: row `key` of a side is
+// key * stride bytes behind base[side].  Paged cache: see page_of().
+template <typename T>
+struct Rows {
+    const uint8_t* base[2];      // K, V of the request and head
+    int64_t stride[2];           // bytes from token to token
+};
+
+// A 16-key group's page and what its weights are scaled with.
+struct PageScale {
+    float k, log2_v, inv_v;      // K's scale; V's as log2 and reciprocal
+    uint32_t live;               // the page exists
+};
+
+template <bool FP8, int N> struct ScaleLds { PageScale at[2][N]; };
+template <int N> struct ScaleLds<false, N> {};
+// The kernel's part of LDS: two buffers of a step's K and V rows, and the
+// scales of its groups (of its keys where pages are not whole groups).
+template <typename T, int DK, int DV, bool UNI>
+struct StepLds : ScaleLds<T::kFp8, UNI ? kStep / 16 : kStep> {
+    static constexpr int KB = DK * T::kBytes, VB = DV * T::kBytes;       // bytes of a row
+    alignas(128) uint8_t k[2][kStep * KB];
+    alignas(128) uint8_t v[2][kStep * VB];
+};
+
+// One side's 64 rows of a packed prompt into LDS: wave w issues every fourth
+// KiB.  EX: heads of exactly N dims.  Otherwise chunks behind the head's last
+// dim come from zeros (K: they meet zeros of the query, so they must be
+// finite), and rows behind the last key are the last key's.
+__device__ const u32x4 g_zero_chunk = {0, 0, 0, 0};
+template <int NC, bool VALUES, bool EX>
+__device__ __forceinline__ void load_rows(const uint8_t* base, int64_t stride, int dims, int left, uint32_t lds, int lane, int w) {
+    constexpr int N = NC / kTileWaves;                   // KiB a wave: 64 rows of 16 NC bytes
+    static_assert(kStep * NC == N * kTileWaves * kWave, "whole KiB");
+    const bool all = left >= kStep;
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        const int at = (n * kTileWaves + w) * kWave + lane, row = at / NC, place = at % NC;
+        const int chunk = place ^ (VALUES ? value_swizzle<NC, false>(row) : key_swizzle<NC>(row));
+        const uint32_t to = lds + (n * kTileWaves + w) * 1024;
+        const uint32_t off = (uint32_t)(all ? row : min(row, left - 1)) * (uint32_t)stride + 16 * chunk;
+        if (EX) load_lds(to, base, off);
+        else load_lds(to, 8 * chunk < dims ? base + off : reinterpret_cast<const uint8_t*>(&g_zero_chunk));
+    }
+}
+
+// Scalar loads of what the whole wave needs.  They count on another counter
+// than the loads to LDS: a vector load's wait would drain those too.
+template <typename V>
+__device__ __forceinline__ V load_scalar(const V* p) {
+    return *reinterpret_cast<const __attribute__((address_space(4))) V*>(reinterpret_cast<uint64_t>(p));
+}
+
+// A page as a wave (UNI: 16 keys of one page, scalars) or a lane finds it.
+struct PageAt {
+    int blk, off;                // as in the table; off -1: behind the table's row
+};
+template <bool UNI>
+__device__ __forceinline__ PageAt find_page(const AttnParams& p, const int32_t* bt_row, int pos) {
+    int bi;
+    PageAt g;
+    split_position(p, pos, bi, g.off);
+    const bool in = bi < p.bt_stride;
+    const int32_t* at = bt_row + (in ? bi : 0);
+    g.blk = UNI ? load_scalar(at) : *at;
+    if (!in) g.off = -1;
+    return g;
+}
+__device__ __forceinline__ bool page_exists(const AttnParams& p, const PageAt& g) {
+    return g.off >= 0 && (uint32_t)g.blk < (uint32_t)p.blocks;
+}
+// Rows of pages that do not exist are page 0's, and hidden.
+__device__ __forceinline__ const uint8_t* page_row(const AttnParams& p, const PageAt& g) {
+    const bool ok = page_exists(p, g);
+    return p.cache + (int64_t)(ok ? g.blk : 0) * p.L.block_stride + (int64_t)(ok ? g.off : 0) * p.L.data_token_stride;
+}
+// The layout's scale strides count floats: offset from K's to V's, token from
+// page to page, head.
+struct RawScale {
+    float k, v;
+};
+template <bool UNI>
+__device__ __forceinline__ RawScale raw_scale(const AttnParams& p, const PageAt& g, int kvh) {
+    const float* at = p.gscale[0] + (int64_t)(page_exists(p, g) ? g.blk : 0) * p.L.scale_token_stride + kvh * p.L.scale_head_stride;
+    return UNI ? RawScale{load_scalar(at), load_scalar(at + p.L.scale_offset)} : RawScale{at[0], at[p.L.scale_offset]};
+}
+__device__ __forceinline__ PageScale scale_of(const RawScale& r, bool exists) {
+    const float v = page_scale(r.v);
+    return PageScale{page_scale(r.k), __builtin_log2f(v), 1.0f / v, exists ? 1u : 0u};
+}
+
+// The pages of a step of the paged cache.  Wave w loads the rows of keys 16 w ..
+// 16 w + 15 of both sides, and writes their scales to LDS for all.
+// UNI: the 16 keys lie in one page, whose id and scales are scalars; else every
+// lane looks up the pages of the rows that it loads, and of key lane % 16.
+template <int DP, bool UNI>
+struct PageWalk {
+    static constexpr int NC = DP / 16, N = 16 * NC / kWave;      // loads of a side: 16 rows of NC chunks
+    static constexpr int LR = kWave / NC;                // rows of a load
+    static constexpr int IDS = UNI ? 1 : N + 1;
+    const int32_t* bt_row;
+    int kvh, wave;
+    PageAt next[IDS], at[IDS];
+    RawScale scale;
+
+    __device__ __forceinline__ void init(const AttnParams& p, const RowTile& t, int head, int w) {
+        bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
+        kvh = head;
+        wave = w;
+    }
+    // Ids of the step at key0; take() looks at them a step later.
+    __device__ __forceinline__ void find(const AttnParams& p, int key0, int lane) {
+        const int first = key0 + 16 * wave;
+#pragma unroll
+        for (int n = 0; n < IDS; n++)
+            next[n] = find_page<UNI>(p, bt_row, first + (UNI ? 0 : n < N ? n * LR + lane / NC : lane & 15));
+    }
+    __device__ __forceinline__ void take(const AttnParams& p) {
+#pragma unroll
+        for (int n = 0; n < IDS; n++) at[n] = next[n];
+        scale = raw_scale<UNI>(p, at[IDS - 1], kvh);
+    }
+    __device__ __forceinline__ void issue(const AttnParams& p, uint32_t k, uint32_t v, int lane) const {
+        const int64_t head = kvh * p.L.data_head_stride, side = p.L.side_stride;
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const int row = n * LR + lane / NC, place = lane % NC;
+            const int kc = place ^ key_swizzle<NC>(row), vc = place ^ value_swizzle<NC, true>(row);
+            const uint32_t to = 16 * wave * DP + n * 1024;
+            if constexpr (UNI) {
+                const uint8_t* page = page_row(p, at[0]) + head;
+                const uint32_t off = (uint32_t)row * p.data_token;
+                load_lds(k + to, page, off + 16 * kc);
+                load_lds(v + to, page + side, off + 16 * vc);
+            } else {
+                const uint8_t* row_at = page_row(p, at[n]) + head;       // chunks behind the head's last dim are zeros
+                const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero_chunk);
+                load_lds(k + to, 16 * kc < p.hs ? row_at + 16 * kc : zero);
+                load_lds(v + to, 16 * vc < p.hs ? row_at + side + 16 * vc : zero);
+            }
+        }
+    }
+    __device__ __forceinline__ void publish(const AttnParams& p, PageScale* to, int lane) const {
+        const PageScale s = scale_of(scale, page_exists(p, at[IDS - 1]));
+        if (UNI ? lane == 0 : lane < 16) to[UNI ? wave : 16 * wave + lane] = s;
+    }
+};
+struct NoWalk {};
+
+// N fragments with DEPTH reads in flight: the barrier keeps reads and matrix
+// instructions in this order.
+template <int N, int DEPTH, typename F, typename Load, typename Use>
+__device__ __forceinline__ void stream(Load load, Use use) {
+    F b[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH; i++) b[i] = load(i);
+    __builtin_amdgcn_sched_barrier(0x676);
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        use(i, b[i % DEPTH]);
+        if (i + DEPTH < N) b[i % DEPTH] = load(i + DEPTH);
+        __builtin_amdgcn_sched_barrier(0x676);
+    }
+}
+
+template <typename V>
+__device__ __forceinline__ V read_lds(uint32_t at) {
+    return *reinterpret_cast<const __attribute__((address_space(3))) V*>(at);
+}
+__device__ __forceinline__ i16x4 read_transposed16(uint32_t at) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) i16x4*>(at));
+}
+__device__ __forceinline__ i32x2 read_transposed8(uint32_t at) {
+    return __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<__attribute__((address_space(3))) i32x2*>(at));
+}
+
+// Raw words of a fragment, and the operand they make.
+template <typename T> struct RawFrag;
+template <> struct RawFrag<PackedBf16> { u32x4 w; };
+template <> struct RawFrag<PagedFp8> { u32x2 w; };
+__device__ __forceinline__ bf16x8 operand(const RawFrag<PackedBf16>& r) { return __builtin_bit_cast(bf16x8, r.w); }
+__device__ __forceinline__ f16x8 operand(const RawFrag<PagedFp8>& r) { return fp8_operand(r.w.x, r.w.y); }
+
+// Values that some rows of a step do not see: what is not finite becomes 0
+// before the product, where a weight of 0 would make it a NaN.  Returns whether
+// there was any.  (An e4m3 NaN code, which no write makes, counts as 0 there.)
+__device__ __forceinline__ uint32_t drop_nonfinite(RawFrag<PackedBf16>& r) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t x = r.w[i];
+        const uint32_t lo = (x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+        any |= lo | hi;
+        r.w[i] = x & ~(lo | hi);
+    }
+    return any;
+}
+__device__ __forceinline__ uint32_t drop_nonfinite(RawFrag<PagedFp8>& r) {
+    r.w.x = drop_nan_e4m3x4(r.w.x);
+    r.w.y = drop_nan_e4m3x4(r.w.y);
+    return 0;
+}
+// What is not finite as bf16's largest value, the rest as 0.
+__device__ __forceinline__ void keep_nonfinite(RawFrag<PackedBf16>& r) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t x = r.w[i];
+        r.w[i] = ((x & 0x7F80u) == 0x7F80u ? 0x7F7Fu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0x7F7F0000u : 0u);
+    }
+}
+
+// row_end for weights shifted by T's shift (row_lse takes kShift off).
+template <typename T, typename P>
+__device__ __forceinline__ RowEnd row_end_shifted(const P& p, int64_t token, int head, float m, float l) {
+    return row_end(p, token, head, m - T::kShiftUp + kShift, l, 1.0f);
+}
+
+// Query rows as the second operand of S^T = K Q^T.  For the e4m3 cache they
+// are scaled by a power of two into binary16; mul undoes it in the logits.
+template <int DK>
+__device__ __forceinline__ void load_rows_q(const PromptParams& p, const uint16_t* src, bool in, int h, bf16x8* q, float& fac) {
+#pragma unroll
+    for (int st = 0; st < DK / 16; st++) {
+        const int dim = step_dim<PackedBf16>(st, h);
+        u32x4 raw = {0, 0, 0, 0};
+        if (in && dim < p.dk) raw = *reinterpret_cast<const u32x4*>(src + dim);
+        q[st] = __builtin_bit_cast(bf16x8, raw);
+    }
+    fac = p.scale_log2;
+}
+template <int DK>
+__device__ __forceinline__ void load_rows_q(const AttnParams& p, const uint16_t* src, bool in, int h, f16x8* q, float& fac) {
+    u32x4 raw[DK / 16];
+    float amax = 0.0f;
+#pragma unroll
+    for (int st = 0; st < DK / 16; st++) {
+        const int dim = step_dim<PagedFp8>(st, h);
+        raw[st] = u32x4{0, 0, 0, 0};
+        if (in && dim < p.hs) raw[st] = *reinterpret_cast<const u32x4*>(src + dim);
+    }
+#pragma unroll
+    for (int st = 0; st < DK / 16; st++) amax = row_amax(raw[st], amax);
+    const float mul = query_scale(p, pair_max(amax), 1.0f, fac);
+#pragma unroll
+    for (int st = 0; st < DK / 16; st++) q[st] = query_operand(raw[st], mul);
+}
+
+// One tile of up to 128 R rows over the 32-key tiles [v0, v1).
+// EX: packed prompts with head sizes of exactly DK and DV; a cache whose head
+// size is DK and whose pages are whole 16-key groups within 32 bits.
+template <typename T, int DK, int DV, int R, bool EX, bool TREE, typename P>
+__device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
+    typedef StepLds<T, DK, DV, EX> L;
+    typedef typename T::frag frag;
+    constexpr int KS = DK / 16, DT = DV / 32, KC = L::KB / 16, VC = L::VB / 16;
+    constexpr bool FP8 = T::kFp8;
+    const int lane = lane_id(), w = wave_id(), c = lane & 31, h = lane >> 5;
+
+    // ---- steps: one or two consecutive 32-key tiles of one run (sinks, then the window)
+    const auto step_key = [&](int v) { return (v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0) * kTileKeys; };
+    const auto after = [&](int v) { return min(v + 2, v < t.sink_tiles ? min(t.sink_tiles, v1) : v1); };
+
+    // ---- loads of a step
+    const uint32_t lds_k = lds_address(lds.k[0]), lds_v = lds_address(lds.v[0]);
+    Rows<T> rows;
+    std::conditional_t<FP8, PageWalk<DK, EX>, NoWalk> walk;
+    if constexpr (FP8) walk.init(p, t, kvh, w);
+    else {
+        const int64_t first = key_start(p, t.b);
+        rows.stride[0] = 2 * p.k_ts;
+        rows.stride[1] = 2 * p.v_ts;
+        rows.base[0] = reinterpret_cast<const uint8_t*>(p.k + first * p.k_ts + kvh * p.k_hs);
+        rows.base[1] = reinterpret_cast<const uint8_t*>(p.v + first * p.v_ts + kvh * p.v_hs);
+    }
+    const auto issue = [&](int v, int buf) {
+        const int key0 = step_key(v);
+        const uint32_t k = lds_k + buf * (int)sizeof(lds.k[0]), vv = lds_v + buf * (int)sizeof(lds.v[0]);
+        if constexpr (FP8) walk.issue(p, k, vv, lane);
+        else {
+            const int left = t.kv_len - key0;
+            load_rows<KC, false, EX>(rows.base[0] + key0 * rows.stride[0], rows.stride[0], p.dk, left, k, lane, w);
+            load_rows<VC, true, EX>(rows.base[1] + key0 * rows.stride[1], rows.stride[1], p.hs, left, vv, lane, w);
+        }
+    };
+
+    int v = v0, vn = v1;
+    if (v < v1) {
+        vn = after(v);
+        if constexpr (FP8) {
+            walk.find(p, step_key(v), lane);
+            walk.take(p);
+            if (vn < v1) walk.find(p, step_key(vn), lane);
+        }
+        issue(v, 0);
+        if constexpr (FP8) walk.publish(p, lds.at[0], lane);
+    }
+
+    // ---- query rows
+    frag q[R][KS];
+    float fac[R];
+    int pos[R], tok[R], row_of[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const int off = 32 * (R * w + r) + c;
+        const bool in = off < t.rows;
+        const int row = in ? t.row0 + off : t.row0, tl = row / p.group, head = kvh * p.group + row - tl * p.group;
+        row_of[r] = in ? row : -1;
+        tok[r] = t.q0 + tl;
+        pos[r] = in ? t.ctx + tl : -1;
+        load_rows_q<DK>(p, p.q + (int64_t)tok[r] * p.q_ts + (int64_t)head * p.q_hs, in, h, q[r], fac[r]);
+    }
+    const bool busy = 32 * R * w < t.rows;               // the other waves of a partly filled tile only load
+    const int pos_lo = t.ctx + min(t.row0 + 32 * R * w, t.row0 + t.rows - 1) / p.group;
+    const int pos_hi = t.ctx + min(t.row0 + 32 * R * (w + 1) - 1, t.row0 + t.rows - 1) / p.group;
+
+    // ---- where a lane reads: K rows c and 32 + c; V rows of its 16-lane group.  Swizzles move chunks within 128 bytes,
+    // so a fragment's place is an exclusive or below 128 and an addition above
+    const uint32_t k_lane = c * L::KB + ((h ^ key_swizzle<KC>(c)) << 4);
+    const int i = lane & 15, dim_half = lane >> 4 & 1;
+    const int v_row = FP8 ? 4 * h + (i >> 1 & 3) + 8 * (i >> 3) : 4 * h + (i >> 2);
+    const int v_chunk = FP8 ? dim_half : 2 * dim_half + (i >> 1 & 1);
+    const uint32_t v_lane = v_row * L::VB + ((v_chunk ^ value_swizzle<VC, FP8>(v_row)) << 4) + 8 * (i & 1);
+
+    f32x16 o[R][DT];
+    // weights are exp2(x + sub), sub = shift - m (0 before the first visible key); a step whose largest exponent passes
+    // lim moves m
+    float m[R], l[R], sub[R], lim[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        m[r] = lim[r] = kNegInf;
+        l[r] = sub[r] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+            for (int j = 0; j < 16; j++) o[r][d][j] = 0.0f;
+    }
+
+    for (int buf = 0; v < v1; buf ^= 1) {                // workgroup-uniform
+        const int key0 = step_key(v), tiles = after(v) - v;
+        tile_ready();
+        if (vn < v1) {
+            if constexpr (FP8) walk.take(p);
+            issue(vn, buf ^ 1);
+            if constexpr (FP8) {
+                walk.publish(p, lds.at[buf ^ 1], lane);
+                const int vp = after(vn);
+                if (vp < v1) walk.find(p, step_key(vp), lane);
+            }
+        }
+        if (busy) {                                      // wave-uniform
+            const uint32_t k_at = k_lane + lds_k + buf * (int)sizeof(lds.k[0]);
+            const uint32_t v_at = v_lane + lds_v + buf * (int)sizeof(lds.v[0]);
+            // ---- S^T = K Q^T
+            f32x16 s[R][2];
+#pragma unroll
+            for (int r = 0; r < R; r++)
+#pragma unroll
+                for (int kt = 0; kt < 2; kt++)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) s[r][kt][j] = 0.0f;
+            // a 16-byte read is one step's operand in bf16, two steps' in e4m3
+            constexpr int PER = FP8 ? 2 : 1;
+            stream<2 * KS / PER, 4, u32x4>(
+                [&](int n) {
+                    const int j = n % (KS / PER);
+                    return read_lds<u32x4>((k_at ^ (j & 3) << 5) + (j >> 2) * 128 + n / (KS / PER) * 32 * L::KB);
+                },
+                [&](int n, const u32x4& x) {
+                    const int kt = n / (KS / PER), st = n % (KS / PER) * PER;
+                    if constexpr (FP8) {
+                        const f16x8 a = fp8_operand(x.x, x.y), b = fp8_operand(x.z, x.w);
+#pragma unroll
+                        for (int r = 0; r < R; r++) {
+                            s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
+                            s[r][kt] = T::mma(b, q[r][st + 1], s[r][kt]);
+                        }
+                    } else {
+                        const bf16x8 a = __builtin_bit_cast(bf16x8, x);
+#pragma unroll
+                        for (int r = 0; r < R; r++) s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
+                    }
+                });
+            // ---- logits; the cache's carry the scales of their pages
+            uint32_t live = tiles == 1 ? 0xFFFFu : ~0u;  // 16 keys of the lane a tile
+            PageScale ps[FP8 && EX ? 4 : 1];
+            if constexpr (FP8 && EX) {
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    ps[g] = lds.at[buf][g];
+                    if (!ps[g].live) live &= ~(0xFFu << (8 * g));
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                if constexpr (FP8 && EX) {
+#pragma unroll
+                    for (int g = 0; g < 4; g++) {
+                        const float f = fac[r] * ps[g].k, a = sub[r] + ps[g].log2_v;
+#pragma unroll
+                        for (int j = 8 * (g & 1); j < 8 * (g & 1) + 8; j++)
+                            s[r][g >> 1][j] = __builtin_fmaf(s[r][g >> 1][j], f, a);
+                    }
+                } else if constexpr (FP8) {
+                    uint32_t there = 0;
+#pragma unroll
+                    for (int j = 0; j < 32; j++) {
+                        const PageScale x = lds.at[buf][8 * (j >> 2) + 4 * h + (j & 3)];
+                        there |= (x.live ? 1u : 0u) << j;
+                        s[r][j >> 4][j & 15] = __builtin_fmaf(s[r][j >> 4][j & 15], fac[r] * x.k, sub[r] + x.log2_v);
+                    }
+                    live &= there;
+                } else {
+#pragma unroll
+                    for (int kt = 0; kt < 2; kt++)
+#pragma unroll
+                        for (int j = 0; j < 16; j++) s[r][kt][j] = __builtin_fmaf(s[r][kt][j], fac[r], sub[r]);
+                }
+            }
+            const bool all = __all(live == ~0u && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kStep));
+            uint32_t see[R];
+            if (!all) {
+#pragma unroll
+                for (int r = 0; r < R; r++) see[r] = hide_step<TREE>(p, t, pos[r], tok[r], key0 + 4 * h, live, s[r]);
+            }
+            // ---- running maximum; the accumulators follow it with a lag
+            float top[R];
+            bool late = false;
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                top[r] = pair_max(fmaxf(max16(s[r][0]), max16(s[r][1])));
+                late = late || top[r] > lim[r];
+            }
+            if (__builtin_expect(__any(late), 0)) {      // wave-uniform, rare after the first steps
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    const float mn = fmaxf(m[r], top[r] - sub[r]);
+                    const bool any = mn != kNegInf;
+                    const float al = any ? __builtin_amdgcn_exp2f(m[r] - mn) : 1.0f;
+                    const float to = any ? T::kShiftUp - mn : 0.0f, by = to - sub[r];
+                    m[r] = mn;
+                    sub[r] = to;
+                    lim[r] = any ? T::kShiftUp + kLag : kNegInf;
+                    l[r] *= al;
+#pragma unroll
+                    for (int kt = 0; kt < 2; kt++)
+#pragma unroll
+                        for (int j = 0; j < 16; j++) s[r][kt][j] += by;
+#pragma unroll
+                    for (int d = 0; d < DT; d++)
+#pragma unroll
+                        for (int j = 0; j < 16; j++) o[r][d][j] *= al;
+                }
+            }
+            // ---- weights
+            frag pw[R][4];
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const float e = __builtin_amdgcn_exp2f(s[r][g >> 1][8 * (g & 1) + j]);
+                        if constexpr (FP8 && !EX) sum += e * lds.at[buf][16 * g + 8 * (j >> 2) + 4 * h + (j & 3)].inv_v;
+                        else sum += e;
+                        if constexpr (FP8) pw[r][g][j] = (_Float16)e;
+                        else pw[r][g][j] = (__bf16)e;
+                    }
+                    if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sum, ps[g].inv_v, l[r]);
+                    else l[r] += sum;
+                }
+            }
+            // ---- O^T += V^T P^T
+            const auto load_v = [&](int n) {
+                const int d = n % DT;
+                const uint32_t at = (v_at ^ (FP8 ? (d & 3) << 5 : (d & 1) << 6)) + (FP8 ? d >> 2 : d >> 1) * 128 + n / DT * 16 * L::VB;
+                RawFrag<T> x;
+                if constexpr (FP8) x.w = __builtin_bit_cast(u32x2, read_transposed8(at));
+                else {
+                    const u32x2 a = __builtin_bit_cast(u32x2, read_transposed16(at));
+                    const u32x2 b = __builtin_bit_cast(u32x2, read_transposed16(at + 8 * L::VB));
+                    x.w = u32x4{a.x, a.y, b.x, b.y};
+                }
+                return x;
+            };
+            const auto add = [&](int n, const frag& a) {
+#pragma unroll
+                for (int r = 0; r < R; r++) o[r][n % DT] = T::mma(a, pw[r][n / DT], o[r][n % DT]);
+            };
+            if (all) {
+                stream<4 * DT, 4, RawFrag<T>>(load_v, [&](int n, const RawFrag<T>& x) { add(n, operand(x)); });
+            } else {
+                // values that a row does not see may hold anything
+                uint32_t odd = 0;
+                stream<4 * DT, 4, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
+                    odd |= drop_nonfinite(x);
+                    add(n, operand(x));
+                });
+                if constexpr (!FP8) {
+                    // rare: rows that do see a value that is not finite get an infinity in its dim (the sum is
+                    // not finite there), the product of two large values
+                    if (__any(odd != 0)) {
+#pragma unroll
+                        for (int r = 0; r < R; r++)
+#pragma unroll
+                            for (int j = 0; j < 32; j++) pw[r][j >> 3][j & 7] = (__bf16)(see[r] >> j & 1 ? 0x1p100f : 0.0f);
+                        stream<4 * DT, 2, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
+                            keep_nonfinite(x);
+                            add(n, operand(x));
+                        });
+                    }
+                }
+            }
+        }
+        v = vn;
+        vn = vn < v1 ? after(vn) : v1;
+    }
+
+    // ---- each lane holds runs of four dims of its rows
+    const bool partial = p.splits > 1 && t.total > t.chunk;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+        const float ll = pair_sum(l[r]);
+        if (row_of[r] < 0) continue;
+        const int tl = row_of[r] / p.group, head = kvh * p.group + row_of[r] - tl * p.group;
+        const int64_t token = t.q0 + tl, id = token * p.hq + head;
+        if (partial) {
+            if (h == 0) {
+                float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
+                ml[0] = m[r] - T::kShiftUp + kShift;     // the join takes kShift off
+                ml[1] = ll;
+            }
+            float* dst = p.ws_o + ((int64_t)t.split * p.total_q * p.hq + id) * p.hs + 4 * h;
+#pragma unroll
+            for (int d = 0; d < DT; d++)
+#pragma unroll
+                for (int a = 0; a < 4; a++)
+                    if (EX || 32 * d + 8 * a + 4 * h < p.hs)
+                        *reinterpret_cast<f32x4*>(dst + 32 * d + 8 * a) =
+                            f32x4{o[r][d][4 * a], o[r][d][4 * a + 1], o[r][d][4 * a + 2], o[r][d][4 * a + 3]};
+        } else {
+            const RowEnd end = row_end_shifted<T>(p, token, head, m[r], ll);
+            if (h == 0 && p.lse) p.lse[token * p.lse_ts + head] = end.lse;
+            uint16_t* dst = p.out + token * p.o_ts + (int64_t)head * p.o_hs + 4 * h;
+#pragma unroll
+            for (int d = 0; d < DT; d++)
+#pragma unroll
+                for (int a = 0; a < 4; a++)
+                    if (EX || 32 * d + 8 * a + 4 * h < p.hs)
+                        write_dims(p, end, dst + 32 * d + 8 * a, o[r][d][4 * a], o[r][d][4 * a + 1], o[r][d][4 * a + 2],
+                                   o[r][d][4 * a + 3]);
+        }
+    }
+}
+
+}  // namespace gcache

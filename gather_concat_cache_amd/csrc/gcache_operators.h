@@ -44,6 +44,18 @@ struct AttnParams {
     int32_t row_tile;            // rows of a row tile (set by the launcher, for the join)
 };
 
+// Attention of packed prompts: the same, with keys and values in packed rows.
+// hs is the value size; block_table, cache, L and gscale are unused.
+struct PromptParams : AttnParams {
+    const uint16_t* k;           // bf16 [total_k, hk, dk]
+    const uint16_t* v;           // bf16 [total_k, hk, hs]
+    int64_t k_ts, k_hs, v_ts, v_hs;      // element strides
+    const int32_t* ks;           // key_starts [batch + 1]
+    int32_t total_k, dk;
+    int32_t causal;
+    int32_t accumulate;          // join with what out and lse hold
+};
+
 // Rows per workgroup (16 to 128), work units and key splits of a call; filled
 // by plan_attention from sizes that the host knows.
 struct AttnPlan {
@@ -53,6 +65,14 @@ struct AttnPlan {
 };
 AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t dp, int32_t dv,
                         int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail);
+AttnPlan plan_attention_rows(int row_tiles, int64_t slots, int64_t total_q, int32_t batch, int32_t hq, int32_t hk,
+                             int32_t dv, int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail);
+AttnPlan plan_attention_fp8(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t hs, int64_t max_seq_len,
+                            int32_t window, int32_t sinks, int64_t ws_floats_avail);
+AttnPlan plan_attention_prompt(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t dk, int32_t dv,
+                               int64_t max_key_len, int32_t window, int32_t sinks, int64_t ws_floats_avail);
+hipError_t launch_attention_fp8(const AttnParams& p, int row_tiles, hipStream_t s);
+hipError_t launch_attention_prompt(const PromptParams& p, hipStream_t s);
 hipError_t launch_attention_kv(const AttnParams& p, int row_tiles, hipStream_t s);
 hipError_t launch_attention_ds_mla(const AttnParams& p, int row_tiles, hipStream_t s);
 
@@ -73,6 +93,29 @@ struct QkNormRopeParams {
     float inv_hs;
 };
 hipError_t launch_qk_norm_rope(const QkNormRopeParams& p, hipStream_t s);
+
+struct AppendParams {
+    const uint16_t *q, *k, *v;   // bf16 [T, heads, hs]
+    uint16_t *qo, *ko;           // ko may be nullptr
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, qo_ts, qo_hs, ko_ts, ko_hs;
+    uint8_t* cache;
+    int64_t token_stride, head_stride, side_stride, block_stride;    // bytes
+    float* scales;
+    int64_t s_head, s_side, s_block;
+    const int32_t *qs, *lens, *block_table;
+    int64_t bt_stride, num_blocks;
+    const int64_t* positions;    // [T] or nullptr
+    const void* cos_sin;
+    int64_t max_pos, cs_stride;
+    int32_t cs_bf16, interleaved, rot, hs, hq, hk, batch;
+    int32_t num_tokens;
+    BlockDiv div;
+    // set by the launcher
+    int32_t chunk_heads, head_chunks, wave_rows;     // heads of a workgroup; rows of a wave
+    int32_t by_token, q_waves;
+    int64_t page_groups;
+};
+hipError_t launch_rope_append(const AppendParams& p, hipStream_t s);
 
 constexpr int kMaxCaches = 64;   // cache pointers carried by one launch
 struct CacheList {

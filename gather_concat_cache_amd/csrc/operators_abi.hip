@@ -1,13 +1,16 @@
-// operators_abi.hip -- the extern "C" entry points of gcache_attention.h and
-// gcache_pages.h: host checks, then one short sequence of launches on the
+// operators_abi.hip -- the extern "C" entry points of gcache_attention.h,
+// gcache_fp8_kv.h, gcache_prompt.h and gcache_pages.h: host checks, then one short sequence of launches on the
 // caller's stream.  Nothing here allocates, frees or synchronizes.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
 #include <utility>
 
 #include "../../include/gcache_attention.h"
+#include "../../include/gcache_fp8_kv.h"
 #include "../../include/gcache_pages.h"
+#include "../../include/gcache_prompt.h"
 #include "gcache_operators.h"
 
 using namespace gcache;
@@ -121,19 +124,62 @@ int attention_args(const gcache_attention_args* a, int32_t hk, int32_t dv, AttnP
     return GCACHE_OK;
 }
 
-AttnPlan set_plan(const gcache_attention_args* a, int dp, AttnParams* p) {
-    const int64_t have = a->workspace ? a->workspace_bytes / (int64_t)sizeof(float) : 0;
-    const AttnPlan plan = plan_attention(p->total_q, p->batch, p->hq, p->hk, dp, p->hs, a->max_seq_len, p->window,
-                                         p->sinks, have);
+// The plan's sizes and the workspace's parts.
+void use_plan(const AttnPlan& plan, void* workspace, AttnParams* p) {
     p->tiles = plan.tiles;
     p->units = plan.units;
     p->splits = plan.splits;
     p->key_tiles = plan.key_tiles;
-    p->ws_o = static_cast<float*>(a->workspace);
+    p->ws_o = static_cast<float*>(workspace);
     const int64_t rows = (int64_t)plan.splits * p->total_q * p->hq;
     p->ws_ml = p->ws_o ? p->ws_o + rows * p->hs : nullptr;
     p->ws_chunk = p->ws_o ? reinterpret_cast<int32_t*>(p->ws_ml + 2 * rows) : nullptr;
+}
+
+int64_t workspace_floats(const void* workspace, int64_t bytes) { return workspace ? bytes / (int64_t)sizeof(float) : 0; }
+
+AttnPlan set_plan(const gcache_attention_args* a, int dp, AttnParams* p) {
+    const AttnPlan plan = plan_attention(p->total_q, p->batch, p->hq, p->hk, dp, p->hs, a->max_seq_len, p->window,
+                                         p->sinks, workspace_floats(a->workspace, a->workspace_bytes));
+    use_plan(plan, a->workspace, p);
     return plan;
+}
+
+// Rows of n elements, repeated `count` times `stride` apart in each of several
+// dimensions, share no element: in the order of their strides, each dimension's
+// steps are as long as what lies inside it.
+struct Dim {
+    int64_t count, stride;
+};
+bool nested(Dim* d, int dims, int64_t n) {
+    std::sort(d, d + dims, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    for (int i = 0; i < dims; i++) {
+        if (d[i].count <= 1) continue;
+        if (d[i].stride < n) return false;
+        int64_t span;
+        if (!mul_ok(d[i].count - 1, d[i].stride, &span) || __builtin_add_overflow(span, n, &n)) return false;
+    }
+    return true;
+}
+
+int check_fp8_layout(const gcache_fp8_kv_layout* L, const void* cache, const float* scales, int64_t num_blocks, bool written,
+                     int32_t hk, int32_t hs, int32_t block_size) {
+    const int64_t s[7] = {L->token_stride, L->head_stride, L->side_stride, L->block_stride,
+                          L->scale_head_stride, L->scale_side_stride, L->scale_block_stride};
+    int64_t tmp;
+    for (int64_t x : s)
+        if (x < 0 || !mul_ok(x, 2, &tmp)) return GCACHE_ERR_SHAPE;
+    if (!mul_ok(num_blocks, L->block_stride, &tmp) || !mul_ok(num_blocks, L->scale_block_stride, &tmp) ||
+        !mul_ok(hk, L->head_stride, &tmp) || !mul_ok(hk, L->scale_head_stride, &tmp) ||
+        !mul_ok(block_size, L->token_stride, &tmp))
+        return GCACHE_ERR_SHAPE;
+    if (!aligned(cache, 16) || !aligned(scales, 4)) return GCACHE_ERR_ALIGN;
+    for (int i = 0; i < 4; i++)
+        if (s[i] % 16) return GCACHE_ERR_ALIGN;
+    Dim data[4] = {{block_size, s[0]}, {hk, s[1]}, {2, s[2]}, {num_blocks, s[3]}};
+    Dim scale[3] = {{hk, s[4]}, {2, s[5]}, {num_blocks, s[6]}};
+    if (written && (!nested(data, 4, hs) || !nested(scale, 3, 1))) return GCACHE_ERR_SHAPE;
+    return GCACHE_OK;
 }
 
 int kv_attention(const gcache_attention_args* a, const void* kv_cache, const gcache_nvfp4_kv_layout* L,
@@ -340,6 +386,205 @@ int gcache_tree_attention_nvfp4_ds_mla(const gcache_attention_args* a, const voi
     p.mask_cols = tree_mask ? mask_columns : 0;
     const AttnPlan plan = set_plan(a, kNope, &p);
     return launched(launch_attention_ds_mla(p, plan.row_tiles, stream));
+}
+
+int gcache_rope_append_fp8_kv(const gcache_append_args* a, void* kv_cache, float* kv_scales,
+                              const gcache_fp8_kv_layout* L, hipStream_t stream) {
+    if (!a) return GCACHE_ERR_NULL;
+    if (a->num_tokens < 0 || a->batch_size < 0) return GCACHE_ERR_SHAPE;
+    if (a->num_tokens == 0 || a->batch_size == 0) return GCACHE_OK;
+    if (!L || !a->k || !a->v || (a->num_q_heads > 0 && (!a->q || !a->q_out)) || !a->query_starts || !a->seq_lens ||
+        !a->block_table || (a->num_blocks > 0 && (!kv_cache || !kv_scales)) || (a->rot > 0 && !a->cos_sin))
+        return GCACHE_ERR_NULL;
+    int64_t tmp;
+    const int64_t heads = (int64_t)a->num_q_heads + a->num_kv_heads;
+    if (a->num_q_heads < 0 || a->num_kv_heads <= 0 || a->head_size < 16 || a->head_size % 16 || a->rot < 0 || a->rot % 16 ||
+        a->rot > a->head_size || a->block_size <= 0 || a->block_size > 65536 || a->block_table_stride <= 0 ||
+        a->num_blocks < 0 || !mul_ok(a->num_tokens, heads, &tmp) || tmp > kMaxRows ||
+        !mul_ok(a->block_table_stride, a->batch_size, &tmp) || !mul_ok(a->block_table_stride, a->block_size, &tmp) ||
+        (a->rot > 0 && (a->max_position < 0 || a->cos_sin_stride < a->rot)))
+        return GCACHE_ERR_SHAPE;
+    if (a->head_size > 256) return GCACHE_ERR_UNSUPPORTED;
+    const bool sides[5] = {a->num_q_heads > 0, true, true, a->num_q_heads > 0, a->k_out != nullptr};   // q, k, v, q_out, k_out
+    const int64_t st[10] = {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride, a->v_token_stride,
+                            a->v_head_stride, a->q_out_token_stride, a->q_out_head_stride, a->k_out_token_stride,
+                            a->k_out_head_stride};
+    const void* at[5] = {a->q, a->k, a->v, a->q_out, a->k_out};
+    for (int i = 0; i < 10; i++) {
+        if (!sides[i / 2]) continue;
+        if (st[i] < 0) return GCACHE_ERR_SHAPE;
+        if (st[i] % 8 || !aligned(at[i / 2], 16)) return GCACHE_ERR_ALIGN;
+    }
+    for (int i = 3; i < 5; i++)                          // rows of an output must not share elements
+        if (sides[i] && !rows_apart(a->num_tokens, i == 3 ? a->num_q_heads : a->num_kv_heads, st[2 * i], st[2 * i + 1], a->head_size))
+            return GCACHE_ERR_SHAPE;
+    if (!aligned(a->query_starts, 4) || !aligned(a->seq_lens, 4) || !aligned(a->block_table, 4) ||
+        !aligned(a->positions, 8) || !aligned(a->cos_sin, a->cos_sin_bf16 ? 2 : 4))
+        return GCACHE_ERR_ALIGN;
+    int rc = check_fp8_layout(L, kv_cache, kv_scales, a->num_blocks, true, a->num_kv_heads, a->head_size, a->block_size);
+    if (rc) return rc;
+    if ((rc = check_device())) return rc;
+    AppendParams p;
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.k = static_cast<const uint16_t*>(a->k);
+    p.v = static_cast<const uint16_t*>(a->v);
+    p.qo = static_cast<uint16_t*>(a->q_out);
+    p.ko = static_cast<uint16_t*>(a->k_out);
+    p.q_ts = st[0];
+    p.q_hs = st[1];
+    p.k_ts = st[2];
+    p.k_hs = st[3];
+    p.v_ts = st[4];
+    p.v_hs = st[5];
+    p.qo_ts = st[6];
+    p.qo_hs = st[7];
+    p.ko_ts = st[8];
+    p.ko_hs = st[9];
+    p.cache = static_cast<uint8_t*>(kv_cache);
+    p.token_stride = L->token_stride;
+    p.head_stride = L->head_stride;
+    p.side_stride = L->side_stride;
+    p.block_stride = L->block_stride;
+    p.scales = kv_scales;
+    p.s_head = L->scale_head_stride;
+    p.s_side = L->scale_side_stride;
+    p.s_block = L->scale_block_stride;
+    p.qs = a->query_starts;
+    p.lens = a->seq_lens;
+    p.block_table = a->block_table;
+    p.bt_stride = a->block_table_stride;
+    p.num_blocks = a->num_blocks;
+    p.positions = a->positions;
+    p.cos_sin = a->cos_sin;
+    p.max_pos = a->max_position;
+    p.cs_stride = a->cos_sin_stride;
+    p.cs_bf16 = a->cos_sin_bf16 != 0;
+    p.interleaved = a->interleaved != 0;
+    p.rot = a->rot;
+    p.hs = a->head_size;
+    p.hq = a->num_q_heads;
+    p.hk = a->num_kv_heads;
+    p.batch = a->batch_size;
+    p.num_tokens = (int32_t)a->num_tokens;
+    p.div = make_div(a->block_size);
+    return launched(launch_rope_append(p, stream));
+}
+
+int gcache_attention_fp8_kv(const gcache_attention_args* a, const void* kv_cache, const float* kv_scales,
+                            const gcache_fp8_kv_layout* L, int32_t hk, int32_t hs, int32_t window, int32_t num_sinks,
+                            const uint8_t* tree_mask, int64_t tree_mask_stride, int32_t mask_columns, hipStream_t stream) {
+    if (!a) return GCACHE_ERR_NULL;
+    if ((a->total_q == 0 && a->batch_size >= 0) || (a->batch_size == 0 && a->total_q >= 0)) return GCACHE_OK;
+    if (!L || (a->num_blocks > 0 && (!kv_cache || !kv_scales))) return GCACHE_ERR_NULL;
+    if (hs <= 0 || hs % 16 || window < 0 || num_sinks < 0 ||
+        (tree_mask && (window > 0 || mask_columns < 0 || tree_mask_stride < mask_columns)))
+        return GCACHE_ERR_SHAPE;
+    if (hs > 256) return GCACHE_ERR_UNSUPPORTED;
+    AttnParams p;
+    int rc = attention_args(a, hk, hs, &p);
+    if (rc) return rc;
+    if ((rc = check_fp8_layout(L, kv_cache, kv_scales, a->num_blocks, false, hk, hs, a->block_size))) return rc;
+    if ((rc = check_device())) return rc;
+    p.cache = static_cast<const uint8_t*>(kv_cache);
+    // the scales' strides in floats: see raw_scale()
+    p.L = KvLayout{0, L->token_stride, L->head_stride, L->scale_side_stride, L->scale_block_stride, L->scale_head_stride,
+                   L->side_stride, L->block_stride};
+    p.gscale[0] = kv_scales;
+    p.window = window;
+    p.sinks = num_sinks;
+    p.mask = tree_mask;
+    p.mask_ts = tree_mask_stride;
+    p.mask_cols = tree_mask ? mask_columns : 0;
+    const AttnPlan plan = plan_attention_fp8(p.total_q, p.batch, p.hq, hk, hs, a->max_seq_len, window, num_sinks,
+                                             workspace_floats(a->workspace, a->workspace_bytes));
+    use_plan(plan, a->workspace, &p);
+    return launched(launch_attention_fp8(p, plan.row_tiles, stream));
+}
+
+int64_t gcache_attention_fp8_kv_workspace_bytes(int64_t total_q, int32_t batch_size, int32_t num_q_heads,
+                                                int32_t num_kv_heads, int32_t head_size, int64_t max_seq_len,
+                                                int32_t window, int32_t num_sinks) {
+    if (total_q <= 0 || batch_size <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
+        head_size <= 0 || max_seq_len < 0 || window < 0 || num_sinks < 0 || total_q > kMaxRows / num_q_heads)
+        return 0;
+    return plan_attention_fp8(total_q, batch_size, num_q_heads, num_kv_heads, head_size, max_seq_len, window, num_sinks,
+                              INT64_MAX).ws_floats * (int64_t)sizeof(float);
+}
+
+int gcache_prompt_attention(const gcache_prompt_args* a, hipStream_t stream) {
+    if (!a) return GCACHE_ERR_NULL;
+    if (a->total_q < 0 || a->batch_size < 0 || a->total_k < 0) return GCACHE_ERR_SHAPE;
+    if (a->total_q == 0 || a->batch_size == 0) return GCACHE_OK;
+    if (!a->q || !a->out || !a->query_starts || !a->key_starts || (a->total_k > 0 && (!a->k || !a->v)) ||
+        (a->accumulate && !a->lse))
+        return GCACHE_ERR_NULL;
+    int64_t rows;
+    if (a->num_q_heads <= 0 || a->num_kv_heads <= 0 || a->num_q_heads % a->num_kv_heads || a->key_size < 8 ||
+        a->key_size % 8 || a->value_size < 8 || a->value_size % 8 || a->max_key_len < 0 || a->workspace_bytes < 0 ||
+        a->window < 0 || a->num_sinks < 0 || (!a->causal && a->window > 0) || !std::isfinite(a->softmax_scale) ||
+        !mul_ok(a->total_q, a->num_q_heads, &rows) || rows > kMaxRows || a->total_k > INT32_MAX - 255 - a->total_q)
+        return GCACHE_ERR_SHAPE;
+    const int64_t st[8] = {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride, a->v_token_stride,
+                           a->v_head_stride, a->out_token_stride, a->out_head_stride};
+    const void* at[4] = {a->q, a->k, a->v, a->out};
+    for (int i = 0; i < 8; i++) {
+        if (st[i] < 0) return GCACHE_ERR_SHAPE;
+        if (st[i] % 8 || !aligned(at[i / 2], 16)) return GCACHE_ERR_ALIGN;
+    }
+    if (a->lse_token_stride < 0 || !rows_apart(a->total_q, a->num_q_heads, st[6], st[7], a->value_size) ||
+        (a->lse && a->total_q > 1 && a->lse_token_stride < a->num_q_heads))
+        return GCACHE_ERR_SHAPE;
+    if (!aligned(a->lse, 4) || !aligned(a->query_starts, 4) || !aligned(a->key_starts, 4) || !aligned(a->workspace, 16))
+        return GCACHE_ERR_ALIGN;
+    if (a->key_size > 256 || a->value_size > 256 || a->k_token_stride > (1 << 23) || a->v_token_stride > (1 << 23))
+        return GCACHE_ERR_UNSUPPORTED;
+    const int rc = check_device();
+    if (rc) return rc;
+    PromptParams p{};
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.k = static_cast<const uint16_t*>(a->k);
+    p.v = static_cast<const uint16_t*>(a->v);
+    p.out = static_cast<uint16_t*>(a->out);
+    p.lse = a->lse;
+    p.q_ts = st[0];
+    p.q_hs = st[1];
+    p.k_ts = st[2];
+    p.k_hs = st[3];
+    p.v_ts = st[4];
+    p.v_hs = st[5];
+    p.o_ts = st[6];
+    p.o_hs = st[7];
+    p.lse_ts = a->lse_token_stride;
+    p.qs = a->query_starts;
+    p.ks = a->key_starts;
+    p.batch = a->batch_size;
+    p.total_q = (int32_t)a->total_q;
+    p.total_k = (int32_t)a->total_k;
+    p.hq = a->num_q_heads;
+    p.hk = a->num_kv_heads;
+    p.group = a->num_q_heads / a->num_kv_heads;
+    p.dk = a->key_size;
+    p.hs = a->value_size;
+    p.scale_log2 = (float)(a->softmax_scale * 1.4426950408889634);
+    p.window = a->window;
+    p.sinks = a->num_sinks;
+    p.causal = a->causal != 0;
+    p.accumulate = a->accumulate != 0;
+    p.div = make_div(1);
+    const AttnPlan plan = plan_attention_prompt(p.total_q, p.batch, p.hq, p.hk, p.dk, p.hs, a->max_key_len, p.window, p.sinks,
+                                                workspace_floats(a->workspace, a->workspace_bytes));
+    use_plan(plan, a->workspace, &p);
+    return launched(launch_attention_prompt(p, stream));
+}
+
+int64_t gcache_prompt_workspace_bytes(int64_t total_q, int32_t batch_size, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t key_size, int32_t value_size, int64_t max_key_len, int32_t window,
+                                      int32_t num_sinks) {
+    if (total_q <= 0 || batch_size <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads ||
+        key_size <= 0 || value_size <= 0 || max_key_len < 0 || window < 0 || num_sinks < 0 || total_q > kMaxRows / num_q_heads)
+        return 0;
+    return plan_attention_prompt(total_q, batch_size, num_q_heads, num_kv_heads, key_size, value_size, max_key_len, window,
+                                 num_sinks, INT64_MAX).ws_floats * (int64_t)sizeof(float);
 }
 
 int64_t gcache_pages_workspace_bytes(int64_t num_blocks, int32_t num_rows, int64_t num_requests) {
