@@ -123,9 +123,9 @@ __device__ __forceinline__ float max16(const f32x16& a) {
 }
 
 // hide() of one row for a 64-key step: bit 4 a + i of live, and the logits, as
-// step_keys_upto counts.  Returns which keys the row sees.
+// step_keys_upto counts.
 template <bool TREE>
-__device__ __forceinline__ uint32_t hide_step(const AttnParams& p, const RowTile& t, int pos, int tok, int key0, uint32_t live,
+__device__ __forceinline__ void hide_step(const AttnParams& p, const RowTile& t, int pos, int tok, int key0, uint32_t live,
                                           f32x16* x) {
     uint32_t see = live & step_keys_upto(sight_hi<TREE>(t, pos), key0);
     if (TREE) {
@@ -147,16 +147,7 @@ __device__ __forceinline__ uint32_t hide_step(const AttnParams& p, const RowTile
     }
 #pragma unroll
     for (int j = 0; j < 32; j++) x[j >> 4][j & 15] = see >> j & 1 ? x[j >> 4][j & 15] : kNegInf;
-    return see;
 }
-
-// Where a step's rows come from.  Packed prompts: row `key` of a side is
-// key * stride bytes behind base[side].  Paged cache: see page_of().
-template <typename T>
-struct Rows {
-    const uint8_t* base[2];      // K, V of the request and head
-    int64_t stride[2];           // bytes from token to token
-};
 
 // A 16-key group's page and what its weights are scaled with.
 struct PageScale {
@@ -164,10 +155,11 @@ struct PageScale {
     uint32_t live;               // the page exists
 };
 
-template <bool FP8, int N> struct ScaleLds { PageScale at[2][N]; };
+template <bool FP8, int N> struct ScaleLds { PageScale at[4][N]; };
 template <int N> struct ScaleLds<false, N> {};
 // The kernel's part of LDS: two buffers of a step's K and V rows, and the
-// scales of its groups (of its keys where pages are not whole groups).
+// scales of the groups of four steps (of their keys where pages are not whole
+// groups): a step's are written two steps before its weights need them.
 template <typename T, int DK, int DV, bool UNI>
 struct StepLds : ScaleLds<T::kFp8, UNI ? kStep / 16 : kStep> {
     static constexpr int KB = DK * T::kBytes, VB = DV * T::kBytes;       // bytes of a row
@@ -252,7 +244,7 @@ struct PageWalk {
     static constexpr int IDS = UNI ? 1 : N + 1;
     const int32_t* bt_row;
     int kvh, wave;
-    PageAt next[IDS], at[IDS];
+    PageAt next[IDS], at[IDS], was[IDS];
     RawScale scale;
 
     __device__ __forceinline__ void init(const AttnParams& p, const RowTile& t, int head, int w) {
@@ -269,27 +261,25 @@ struct PageWalk {
     }
     __device__ __forceinline__ void take(const AttnParams& p) {
 #pragma unroll
-        for (int n = 0; n < IDS; n++) at[n] = next[n];
+        for (int n = 0; n < IDS; n++) {
+            was[n] = at[n];
+            at[n] = next[n];
+        }
         scale = raw_scale<UNI>(p, at[IDS - 1], kvh);
     }
-    __device__ __forceinline__ void issue(const AttnParams& p, uint32_t k, uint32_t v, int lane) const {
-        const int64_t head = kvh * p.L.data_head_stride, side = p.L.side_stride;
+    // Keys (side 0) of the step taken last, values (side 1) of the one before.
+    __device__ __forceinline__ void issue(const AttnParams& p, uint32_t to, int side, int lane) const {
+        const int64_t far = kvh * p.L.data_head_stride + side * p.L.side_stride;
+        const PageAt* from = side ? was : at;
 #pragma unroll
         for (int n = 0; n < N; n++) {
             const int row = n * LR + lane / NC, place = lane % NC;
-            const int kc = place ^ key_swizzle<NC>(row), vc = place ^ value_swizzle<NC, true>(row);
-            const uint32_t to = 16 * wave * DP + n * 1024;
-            if constexpr (UNI) {
-                const uint8_t* page = page_row(p, at[0]) + head;
-                const uint32_t off = (uint32_t)row * p.data_token;
-                load_lds(k + to, page, off + 16 * kc);
-                load_lds(v + to, page + side, off + 16 * vc);
-            } else {
-                const uint8_t* row_at = page_row(p, at[n]) + head;       // chunks behind the head's last dim are zeros
-                const uint8_t* zero = reinterpret_cast<const uint8_t*>(&g_zero_chunk);
-                load_lds(k + to, 16 * kc < p.hs ? row_at + 16 * kc : zero);
-                load_lds(v + to, 16 * vc < p.hs ? row_at + side + 16 * vc : zero);
-            }
+            const int chunk = place ^ (side ? value_swizzle<NC, true>(row) : key_swizzle<NC>(row));
+            const uint32_t there = to + 16 * wave * DP + n * 1024;
+            if constexpr (UNI) load_lds(there, page_row(p, from[0]) + far, (uint32_t)row * p.data_token + 16 * chunk);
+            else                                         // chunks behind the head's last dim are zeros
+                load_lds(there, 16 * chunk < p.hs ? page_row(p, from[n]) + far + 16 * chunk
+                                                  : reinterpret_cast<const uint8_t*>(&g_zero_chunk));
         }
     }
     __device__ __forceinline__ void publish(const AttnParams& p, PageScale* to, int lane) const {
@@ -348,9 +338,10 @@ __device__ __forceinline__ uint32_t drop_nonfinite(RawFrag<PackedBf16>& r) {
     return any;
 }
 __device__ __forceinline__ uint32_t drop_nonfinite(RawFrag<PagedFp8>& r) {
-    r.w.x = drop_nan_e4m3x4(r.w.x);
-    r.w.y = drop_nan_e4m3x4(r.w.y);
-    return 0;
+    const u32x2 x = r.w;
+    r.w.x = drop_nan_e4m3x4(x.x);
+    r.w.y = drop_nan_e4m3x4(x.y);
+    return (r.w.x ^ x.x) | (r.w.y ^ x.y);
 }
 // What is not finite as bf16's largest value, the rest as 0.
 __device__ __forceinline__ void keep_nonfinite(RawFrag<PackedBf16>& r) {
@@ -397,11 +388,50 @@ __device__ __forceinline__ void load_rows_q(const AttnParams& p, const uint16_t*
     for (int st = 0; st < DK / 16; st++) q[st] = query_operand(raw[st], mul);
 }
 
+// Scores of a step: S^T = K Q^T.  A 16-byte read is one step's operand in bf16,
+// two steps' in e4m3.
+template <typename T, int KS, int KB, int R>
+__device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::frag (*q)[KS], f32x16 (*s)[2]) {
+    constexpr int PER = T::kFp8 ? 2 : 1, J = KS / PER;
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int kt = 0; kt < 2; kt++)
+#pragma unroll
+            for (int j = 0; j < 16; j++) s[r][kt][j] = 0.0f;
+    stream<2 * J, 4, u32x4>(
+        [&](int n) { return read_lds<u32x4>((k_at ^ (n % J & 3) << 5) + (n % J >> 2) * 128 + n / J * 32 * KB); },
+        [&](int n, const u32x4& x) {
+            const int kt = n / J, st = n % J * PER;
+            if constexpr (T::kFp8) {
+                const f16x8 a = fp8_operand(x.x, x.y), b = fp8_operand(x.z, x.w);
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
+                    s[r][kt] = T::mma(b, q[r][st + 1], s[r][kt]);
+                }
+            } else {
+                const bf16x8 a = __builtin_bit_cast(bf16x8, x);
+#pragma unroll
+                for (int r = 0; r < R; r++) s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
+            }
+        });
+}
+
 // One tile of up to 128 R rows over the 32-key tiles [v0, v1).
 // EX: packed prompts with head sizes of exactly DK and DV; a cache whose head
 // size is DK and whose pages are whole 16-key groups within 32 bits.
-template <typename T, int DK, int DV, int R, bool EX, bool TREE, typename P>
-__device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
+// CAREFUL: values of hidden keys may be infinities or NaN, which a weight of 0
+// would let through: looked for in every step with a mask.  Without it such a
+// value makes a NaN, and the tile is computed again with it.  Returns whether
+// there is a NaN in the workgroup's tile, when not CAREFUL; nothing is written
+// then.
+//
+// The scores of step i + 1 are multiplied while step i's weights are computed,
+// and its values while the next logits are scaled: a wave's matrix instructions
+// and its vector ones are independent, and run side by side.
+template <typename T, int DK, int DV, int R, bool EX, bool TREE, bool CAREFUL, typename P>
+__device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
     typedef StepLds<T, DK, DV, EX> L;
     typedef typename T::frag frag;
     constexpr int KS = DK / 16, DT = DV / 32, KC = L::KB / 16, VC = L::VB / 16;
@@ -410,41 +440,54 @@ __device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kv
 
     // ---- steps: one or two consecutive 32-key tiles of one run (sinks, then the window)
     const auto step_key = [&](int v) { return (v < t.sink_tiles ? v : v - t.sink_tiles + t.win_tile0) * kTileKeys; };
-    const auto after = [&](int v) { return min(v + 2, v < t.sink_tiles ? min(t.sink_tiles, v1) : v1); };
+    const auto after = [&](int v) { return v < v1 ? min(v + 2, v < t.sink_tiles ? min(t.sink_tiles, v1) : v1) : v1; };
 
     // ---- loads of a step
     const uint32_t lds_k = lds_address(lds.k[0]), lds_v = lds_address(lds.v[0]);
-    Rows<T> rows;
+    const uint8_t* base[2] = {nullptr, nullptr};
+    int64_t stride[2] = {0, 0};
     std::conditional_t<FP8, PageWalk<DK, EX>, NoWalk> walk;
     if constexpr (FP8) walk.init(p, t, kvh, w);
     else {
         const int64_t first = key_start(p, t.b);
-        rows.stride[0] = 2 * p.k_ts;
-        rows.stride[1] = 2 * p.v_ts;
-        rows.base[0] = reinterpret_cast<const uint8_t*>(p.k + first * p.k_ts + kvh * p.k_hs);
-        rows.base[1] = reinterpret_cast<const uint8_t*>(p.v + first * p.v_ts + kvh * p.v_hs);
+        stride[0] = 2 * p.k_ts;
+        stride[1] = 2 * p.v_ts;
+        base[0] = reinterpret_cast<const uint8_t*>(p.k + first * p.k_ts + kvh * p.k_hs);
+        base[1] = reinterpret_cast<const uint8_t*>(p.v + first * p.v_ts + kvh * p.v_hs);
     }
-    const auto issue = [&](int v, int buf) {
-        const int key0 = step_key(v);
-        const uint32_t k = lds_k + buf * (int)sizeof(lds.k[0]), vv = lds_v + buf * (int)sizeof(lds.v[0]);
-        if constexpr (FP8) walk.issue(p, k, vv, lane);
+    // keys of step number n at v, values of step number n at v
+    const auto issue_keys = [&](int v, int n) {
+        const uint32_t to = lds_k + (n & 1) * (int)sizeof(lds.k[0]);
+        if constexpr (FP8) {
+            walk.issue(p, to, 0, lane);
+            walk.publish(p, lds.at[n & 3], lane);
+        } else {
+            const int key0 = step_key(v);
+            load_rows<KC, false, EX>(base[0] + key0 * stride[0], stride[0], p.dk, t.kv_len - key0, to, lane, w);
+        }
+    };
+    const auto issue_values = [&](int v, int n) {
+        const uint32_t to = lds_v + (n & 1) * (int)sizeof(lds.v[0]);
+        if constexpr (FP8) walk.issue(p, to, 1, lane);
         else {
-            const int left = t.kv_len - key0;
-            load_rows<KC, false, EX>(rows.base[0] + key0 * rows.stride[0], rows.stride[0], p.dk, left, k, lane, w);
-            load_rows<VC, true, EX>(rows.base[1] + key0 * rows.stride[1], rows.stride[1], p.hs, left, vv, lane, w);
+            const int key0 = step_key(v);
+            load_rows<VC, true, EX>(base[1] + key0 * stride[1], stride[1], p.hs, t.kv_len - key0, to, lane, w);
         }
     };
 
-    int v = v0, vn = v1;
+    int v = v0, vn = after(v), vp = after(vn);           // this step, the next, the one after
     if (v < v1) {
-        vn = after(v);
         if constexpr (FP8) {
             walk.find(p, step_key(v), lane);
             walk.take(p);
-            if (vn < v1) walk.find(p, step_key(vn), lane);
+            walk.find(p, step_key(vn < v1 ? vn : v), lane);
         }
-        issue(v, 0);
-        if constexpr (FP8) walk.publish(p, lds.at[0], lane);
+        issue_keys(v, 0);
+        if constexpr (FP8) {
+            walk.take(p);
+            walk.find(p, step_key(vp < v1 ? vp : v), lane);
+        }
+        issue_values(v, 0);
     }
 
     // ---- query rows
@@ -467,15 +510,15 @@ __device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kv
 
     // ---- where a lane reads: K rows c and 32 + c; V rows of its 16-lane group.  Swizzles move chunks within 128 bytes,
     // so a fragment's place is an exclusive or below 128 and an addition above
-    const uint32_t k_lane = c * L::KB + ((h ^ key_swizzle<KC>(c)) << 4);
+    const uint32_t k_lane = lds_k + c * L::KB + ((h ^ key_swizzle<KC>(c)) << 4);
     const int i = lane & 15, dim_half = lane >> 4 & 1;
     const int v_row = FP8 ? 4 * h + (i >> 1 & 3) + 8 * (i >> 3) : 4 * h + (i >> 2);
     const int v_chunk = FP8 ? dim_half : 2 * dim_half + (i >> 1 & 1);
-    const uint32_t v_lane = v_row * L::VB + ((v_chunk ^ value_swizzle<VC, FP8>(v_row)) << 4) + 8 * (i & 1);
+    const uint32_t v_lane = lds_v + v_row * L::VB + ((v_chunk ^ value_swizzle<VC, FP8>(v_row)) << 4) + 8 * (i & 1);
 
     f32x16 o[R][DT];
-    // weights are exp2(x + sub), sub = shift - m (0 before the first visible key); a step whose largest exponent passes
-    // lim moves m
+    // weights are exp2(x), x the logits + sub, sub = shift - m (0 before the first visible key); a step whose largest
+    // exponent passes lim moves m
     float m[R], l[R], sub[R], lim[R];
 #pragma unroll
     for (int r = 0; r < R; r++) {
@@ -486,186 +529,207 @@ __device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kv
 #pragma unroll
             for (int j = 0; j < 16; j++) o[r][d][j] = 0.0f;
     }
+    f32x16 s[R][2];                                      // of the step whose weights come next
+    bool seen_all = true;                                // no key of it is hidden
 
-    for (int buf = 0; v < v1; buf ^= 1) {                // workgroup-uniform
-        const int key0 = step_key(v), tiles = after(v) - v;
-        tile_ready();
-        if (vn < v1) {
-            if constexpr (FP8) walk.take(p);
-            issue(vn, buf ^ 1);
-            if constexpr (FP8) {
-                walk.publish(p, lds.at[buf ^ 1], lane);
-                const int vp = after(vn);
-                if (vp < v1) walk.find(p, step_key(vp), lane);
-            }
-        }
-        if (busy) {                                      // wave-uniform
-            const uint32_t k_at = k_lane + lds_k + buf * (int)sizeof(lds.k[0]);
-            const uint32_t v_at = v_lane + lds_v + buf * (int)sizeof(lds.v[0]);
-            // ---- S^T = K Q^T
-            f32x16 s[R][2];
+    // ---- logits of a step from its scores: scaled, shifted, the hidden ones -infinity; the running maximum, which the
+    // accumulators follow with a lag
+    const auto scale_scores = [&](int n, f32x16 (*x)[2]) {
 #pragma unroll
-            for (int r = 0; r < R; r++)
-#pragma unroll
-                for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-                    for (int j = 0; j < 16; j++) s[r][kt][j] = 0.0f;
-            // a 16-byte read is one step's operand in bf16, two steps' in e4m3
-            constexpr int PER = FP8 ? 2 : 1;
-            stream<2 * KS / PER, 4, u32x4>(
-                [&](int n) {
-                    const int j = n % (KS / PER);
-                    return read_lds<u32x4>((k_at ^ (j & 3) << 5) + (j >> 2) * 128 + n / (KS / PER) * 32 * L::KB);
-                },
-                [&](int n, const u32x4& x) {
-                    const int kt = n / (KS / PER), st = n % (KS / PER) * PER;
-                    if constexpr (FP8) {
-                        const f16x8 a = fp8_operand(x.x, x.y), b = fp8_operand(x.z, x.w);
-#pragma unroll
-                        for (int r = 0; r < R; r++) {
-                            s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
-                            s[r][kt] = T::mma(b, q[r][st + 1], s[r][kt]);
-                        }
-                    } else {
-                        const bf16x8 a = __builtin_bit_cast(bf16x8, x);
-#pragma unroll
-                        for (int r = 0; r < R; r++) s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
-                    }
-                });
-            // ---- logits; the cache's carry the scales of their pages
-            uint32_t live = tiles == 1 ? 0xFFFFu : ~0u;  // 16 keys of the lane a tile
-            PageScale ps[FP8 && EX ? 4 : 1];
+        for (int r = 0; r < R; r++) {
             if constexpr (FP8 && EX) {
 #pragma unroll
                 for (int g = 0; g < 4; g++) {
-                    ps[g] = lds.at[buf][g];
-                    if (!ps[g].live) live &= ~(0xFFu << (8 * g));
+                    const PageScale ps = lds.at[n & 3][g];
+                    const float f = fac[r] * ps.k, a = sub[r] + ps.log2_v;
+#pragma unroll
+                    for (int j = 8 * (g & 1); j < 8 * (g & 1) + 8; j++) x[r][g >> 1][j] = __builtin_fmaf(x[r][g >> 1][j], f, a);
                 }
-            }
+            } else if constexpr (FP8) {
 #pragma unroll
-            for (int r = 0; r < R; r++) {
-                if constexpr (FP8 && EX) {
-#pragma unroll
-                    for (int g = 0; g < 4; g++) {
-                        const float f = fac[r] * ps[g].k, a = sub[r] + ps[g].log2_v;
-#pragma unroll
-                        for (int j = 8 * (g & 1); j < 8 * (g & 1) + 8; j++)
-                            s[r][g >> 1][j] = __builtin_fmaf(s[r][g >> 1][j], f, a);
-                    }
-                } else if constexpr (FP8) {
-                    uint32_t there = 0;
-#pragma unroll
-                    for (int j = 0; j < 32; j++) {
-                        const PageScale x = lds.at[buf][8 * (j >> 2) + 4 * h + (j & 3)];
-                        there |= (x.live ? 1u : 0u) << j;
-                        s[r][j >> 4][j & 15] = __builtin_fmaf(s[r][j >> 4][j & 15], fac[r] * x.k, sub[r] + x.log2_v);
-                    }
-                    live &= there;
-                } else {
-#pragma unroll
-                    for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-                        for (int j = 0; j < 16; j++) s[r][kt][j] = __builtin_fmaf(s[r][kt][j], fac[r], sub[r]);
+                for (int j = 0; j < 32; j++) {
+                    const PageScale& ps = lds.at[n & 3][8 * (j >> 2) + 4 * h + (j & 3)];
+                    x[r][j >> 4][j & 15] = __builtin_fmaf(x[r][j >> 4][j & 15], fac[r] * ps.k, sub[r] + ps.log2_v);
                 }
-            }
-            const bool all = __all(live == ~0u && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kStep));
-            uint32_t see[R];
-            if (!all) {
-#pragma unroll
-                for (int r = 0; r < R; r++) see[r] = hide_step<TREE>(p, t, pos[r], tok[r], key0 + 4 * h, live, s[r]);
-            }
-            // ---- running maximum; the accumulators follow it with a lag
-            float top[R];
-            bool late = false;
-#pragma unroll
-            for (int r = 0; r < R; r++) {
-                top[r] = pair_max(fmaxf(max16(s[r][0]), max16(s[r][1])));
-                late = late || top[r] > lim[r];
-            }
-            if (__builtin_expect(__any(late), 0)) {      // wave-uniform, rare after the first steps
-#pragma unroll
-                for (int r = 0; r < R; r++) {
-                    const float mn = fmaxf(m[r], top[r] - sub[r]);
-                    const bool any = mn != kNegInf;
-                    const float al = any ? __builtin_amdgcn_exp2f(m[r] - mn) : 1.0f;
-                    const float to = any ? T::kShiftUp - mn : 0.0f, by = to - sub[r];
-                    m[r] = mn;
-                    sub[r] = to;
-                    lim[r] = any ? T::kShiftUp + kLag : kNegInf;
-                    l[r] *= al;
-#pragma unroll
-                    for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-                        for (int j = 0; j < 16; j++) s[r][kt][j] += by;
-#pragma unroll
-                    for (int d = 0; d < DT; d++)
-#pragma unroll
-                        for (int j = 0; j < 16; j++) o[r][d][j] *= al;
-                }
-            }
-            // ---- weights
-            frag pw[R][4];
-#pragma unroll
-            for (int r = 0; r < R; r++) {
-#pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const float e = __builtin_amdgcn_exp2f(s[r][g >> 1][8 * (g & 1) + j]);
-                        if constexpr (FP8 && !EX) sum += e * lds.at[buf][16 * g + 8 * (j >> 2) + 4 * h + (j & 3)].inv_v;
-                        else sum += e;
-                        if constexpr (FP8) pw[r][g][j] = (_Float16)e;
-                        else pw[r][g][j] = (__bf16)e;
-                    }
-                    if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sum, ps[g].inv_v, l[r]);
-                    else l[r] += sum;
-                }
-            }
-            // ---- O^T += V^T P^T
-            const auto load_v = [&](int n) {
-                const int d = n % DT;
-                const uint32_t at = (v_at ^ (FP8 ? (d & 3) << 5 : (d & 1) << 6)) + (FP8 ? d >> 2 : d >> 1) * 128 + n / DT * 16 * L::VB;
-                RawFrag<T> x;
-                if constexpr (FP8) x.w = __builtin_bit_cast(u32x2, read_transposed8(at));
-                else {
-                    const u32x2 a = __builtin_bit_cast(u32x2, read_transposed16(at));
-                    const u32x2 b = __builtin_bit_cast(u32x2, read_transposed16(at + 8 * L::VB));
-                    x.w = u32x4{a.x, a.y, b.x, b.y};
-                }
-                return x;
-            };
-            const auto add = [&](int n, const frag& a) {
-#pragma unroll
-                for (int r = 0; r < R; r++) o[r][n % DT] = T::mma(a, pw[r][n / DT], o[r][n % DT]);
-            };
-            if (all) {
-                stream<4 * DT, 4, RawFrag<T>>(load_v, [&](int n, const RawFrag<T>& x) { add(n, operand(x)); });
             } else {
-                // values that a row does not see may hold anything
-                uint32_t odd = 0;
-                stream<4 * DT, 4, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
-                    odd |= drop_nonfinite(x);
-                    add(n, operand(x));
-                });
-                if constexpr (!FP8) {
-                    // rare: rows that do see a value that is not finite get an infinity in its dim (the sum is
-                    // not finite there), the product of two large values
-                    if (__any(odd != 0)) {
 #pragma unroll
-                        for (int r = 0; r < R; r++)
+                for (int kt = 0; kt < 2; kt++)
 #pragma unroll
-                            for (int j = 0; j < 32; j++) pw[r][j >> 3][j & 7] = (__bf16)(see[r] >> j & 1 ? 0x1p100f : 0.0f);
-                        stream<4 * DT, 2, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
-                            keep_nonfinite(x);
-                            add(n, operand(x));
-                        });
-                    }
+                    for (int j = 0; j < 16; j++) x[r][kt][j] = __builtin_fmaf(x[r][kt][j], fac[r], sub[r]);
+            }
+        }
+    };
+    const auto find_top = [&](f32x16 (*x)[2], float* top) {
+#pragma unroll
+        for (int r = 0; r < R; r++) top[r] = pair_max(fmaxf(max16(x[r][0]), max16(x[r][1])));
+    };
+    const auto settle = [&](int v, int n, f32x16 (*x)[2], float* top) {
+        uint32_t live = after(v) - v == 1 ? 0xFFFFu : ~0u;   // 16 keys of the lane a 32-key tile
+        if constexpr (FP8) {
+            constexpr int PER = EX ? 8 : 1;
+#pragma unroll
+            for (int j = 0; j < 32 / PER; j++)
+                if (!lds.at[n & 3][EX ? j : 8 * (j >> 2) + 4 * h + (j & 3)].live) live &= ~((PER == 8 ? 0xFFu : 1u) << (PER * j));
+        }
+        seen_all = __all(live == ~0u && all_seen<TREE>(p, t, pos_lo, pos_hi, step_key(v), kStep));
+        if (!seen_all) {
+#pragma unroll
+            for (int r = 0; r < R; r++) hide_step<TREE>(p, t, pos[r], tok[r], step_key(v) + 4 * h, live, x[r]);
+            find_top(x, top);
+        }
+        bool late = false;
+#pragma unroll
+        for (int r = 0; r < R; r++) late = late || top[r] > lim[r];
+        if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first steps
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                const float mn = fmaxf(m[r], top[r] - sub[r]);
+                const bool any = mn != kNegInf;
+                const float al = any ? __builtin_amdgcn_exp2f(m[r] - mn) : 1.0f;
+                const float to = any ? T::kShiftUp - mn : 0.0f, by = to - sub[r];
+                m[r] = mn;
+                sub[r] = to;
+                lim[r] = any ? T::kShiftUp + kLag : kNegInf;
+                l[r] *= al;
+#pragma unroll
+                for (int kt = 0; kt < 2; kt++)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) x[r][kt][j] += by;
+#pragma unroll
+                for (int d = 0; d < DT; d++)
+#pragma unroll
+                    for (int j = 0; j < 16; j++) o[r][d][j] *= al;
+            }
+        }
+    };
+    frag pw[R][4];
+    const auto weigh = [&](int n) {
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float e = __builtin_amdgcn_exp2f(s[r][g >> 1][8 * (g & 1) + j]);
+                    if constexpr (FP8 && !EX) sum += e * lds.at[n & 3][16 * g + 8 * (j >> 2) + 4 * h + (j & 3)].inv_v;
+                    else sum += e;
+                    if constexpr (FP8) pw[r][g][j] = (_Float16)e;
+                    else pw[r][g][j] = (__bf16)e;
+                }
+                if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sum, lds.at[n & 3][g].inv_v, l[r]);
+                else l[r] += sum;
+            }
+        }
+    };
+    const auto add_values = [&](int n) {
+        const uint32_t v_at = v_lane + (n & 1) * (int)sizeof(lds.v[0]);
+        const auto load_v = [&](int n) {
+            const int d = n % DT;
+            const uint32_t at = (v_at ^ (FP8 ? (d & 3) << 5 : (d & 1) << 6)) + (FP8 ? d >> 2 : d >> 1) * 128 + n / DT * 16 * L::VB;
+            RawFrag<T> x;
+            if constexpr (FP8) x.w = __builtin_bit_cast(u32x2, read_transposed8(at));
+            else {
+                const u32x2 a = __builtin_bit_cast(u32x2, read_transposed16(at));
+                const u32x2 b = __builtin_bit_cast(u32x2, read_transposed16(at + 8 * L::VB));
+                x.w = u32x4{a.x, a.y, b.x, b.y};
+            }
+            return x;
+        };
+        const auto add = [&](int n, const frag& a) {
+#pragma unroll
+            for (int r = 0; r < R; r++) o[r][n % DT] = T::mma(a, pw[r][n / DT], o[r][n % DT]);
+        };
+        if constexpr (!CAREFUL) {
+            stream<4 * DT, 4, RawFrag<T>>(load_v, [&](int n, const RawFrag<T>& x) { add(n, operand(x)); });
+        } else {
+            uint32_t odd = 0;
+            stream<4 * DT, 2, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
+                odd |= drop_nonfinite(x);
+                add(n, operand(x));
+            });
+            // rows that do see a value that is not finite get an infinity in its dim (the sum is not finite there), the
+            // product of two large values
+            if constexpr (!FP8) {
+                if (__any(odd != 0)) {
+#pragma unroll
+                    for (int r = 0; r < R; r++)
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            pw[r][j >> 3][j & 7] = (__bf16)(s[r][j >> 4][j & 15] != kNegInf ? 0x1p100f : 0.0f);
+                    stream<4 * DT, 2, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
+                        keep_nonfinite(x);
+                        add(n, operand(x));
+                    });
                 }
             }
         }
+    };
+
+    int n = 0;                                           // number of the step at v
+    if (v < v1) {
+        tile_ready();
+        if (vn < v1) issue_keys(vn, 1);
+        if (busy) {
+            multiply_keys<T, KS, L::KB, R>(k_lane, q, s);
+            float top[R];
+            scale_scores(0, s);
+            find_top(s, top);
+            settle(v, 0, s, top);
+        }
+    }
+    while (vn < v1) {                                    // workgroup-uniform
+        // ---- keys of the next step and values of this one are there; the places of this step's keys and of the last
+        // step's values are free
+        tile_ready();
+        if constexpr (FP8) {
+            walk.take(p);                                // the pages of step vp; those of vn are the ones before
+            const int vq = after(vp);
+            walk.find(p, step_key(vq < v1 ? vq : v), lane);
+        }
+        if (vp < v1) issue_keys(vp, n + 2);
+        issue_values(vn, n + 1);
+        if (busy) {                                      // wave-uniform
+            f32x16 x[R][2];
+            float top[R];
+            multiply_keys<T, KS, L::KB, R>(k_lane + ((n + 1) & 1) * (int)sizeof(lds.k[0]), q, x);
+            weigh(n);
+            add_values(n);
+            scale_scores(n + 1, x);
+            find_top(x, top);
+            settle(vn, n + 1, x, top);
+#pragma unroll
+            for (int r = 0; r < R; r++)
+#pragma unroll
+                for (int kt = 0; kt < 2; kt++) s[r][kt] = x[r][kt];
+        }
         v = vn;
-        vn = vn < v1 ? after(vn) : v1;
+        vn = vp;
+        vp = after(vp);
+        n++;
+    }
+    if (v < v1) {
+        tile_ready();
+        if (busy) {
+            weigh(n);
+            add_values(n);
+        }
+    }
+
+    if constexpr (!CAREFUL) {
+        bool odd = false;
+#pragma unroll
+        for (int r = 0; r < R; r++)
+#pragma unroll
+            for (int d = 0; d < DT; d++)
+#pragma unroll
+                for (int j = 0; j < 16; j++) odd = odd || o[r][d][j] != o[r][d][j];
+        uint32_t* flag = reinterpret_cast<uint32_t*>(lds.k[0]);  // the steps are done with it
+        tile_ready();
+        if (lane == 0) flag[w] = 0;
+        if (busy && odd) flag[w] = 1;
+        __syncthreads();
+        if (flag[0] | flag[1] | flag[2] | flag[3]) return true;
     }
 
     // ---- each lane holds runs of four dims of its rows
@@ -702,6 +766,15 @@ __device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kv
                         write_dims(p, end, dst + 32 * d + 8 * a, o[r][d][4 * a], o[r][d][4 * a + 1], o[r][d][4 * a + 2],
                                    o[r][d][4 * a + 3]);
         }
+    }
+    return false;
+}
+
+template <typename T, int DK, int DV, int R, bool EX, bool TREE, typename P>
+__device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
+    if (attend_once<T, DK, DV, R, EX, TREE, false>(p, t, kvh, v0, v1, lds)) {
+        __syncthreads();
+        attend_once<T, DK, DV, R, EX, TREE, true>(p, t, kvh, v0, v1, lds);
     }
 }
 
