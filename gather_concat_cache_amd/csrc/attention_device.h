@@ -200,7 +200,10 @@ __device__ __forceinline__ int request_splits(int work, int chunk) { return max(
 __host__ __device__ __forceinline__ bool counts_requests(int batch, int kv_heads) {
     return batch <= 256 || (batch <= 512 && batch * kv_heads <= 512);
 }
-template <typename P>
+// SORTED: for up to 64 requests that are not split, the tiles of all requests in
+// the order of their distance from position 0, the furthest first, so that the
+// longest of every request start before the short ones of any.
+template <bool SORTED = false, typename P>
 __device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowTile& t) {
     const int lane = lane_id();
     const auto tiles_of = [&](int rows) { return (max(rows, 0) + RT - 1) / RT; };
@@ -249,7 +252,31 @@ __device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowT
         int at = (__builtin_ffsll(__ballot(upto > index)) - 1) & (kWave - 1);
         before = __builtin_amdgcn_readlane(upto - n, at);
         int work = work1;
-        if (per == 1) {
+        if (SORTED && per == 1 && !split) {
+            // level of a request's tile j: from + j; count(x) tiles have level x or more
+            const int keys = key_count(p, min(b0, p.batch - 1)), qlen = max(q_last - q_first, 0);
+            const int from = (int)((int64_t)max(first_position(p, keys, qlen), 0) * p.group / RT);
+            const auto count = [&](int x) {
+                return __builtin_amdgcn_readlane(scan_lanes(n > 0 ? min(max(from + n - x, 0), n) : 0), kWave - 1);
+            };
+            int most = n > 0 ? from + n : 0;
+#pragma unroll
+            for (int d = 1; d < kWave; d <<= 1) most = max(most, __shfl_xor(most, d));
+            int lo = 0, hi = __builtin_amdgcn_readfirstlane(most);       // the unit's level is in [lo, hi)
+            while (hi - lo > 1) {
+                const int mid = (int)(((int64_t)lo + hi) >> 1);
+                if (count(mid) > unit) lo = mid;
+                else hi = mid;
+            }
+            uint64_t at_level = __ballot(n > 0 && from <= lo && lo < from + n);
+            for (int rank = (int)unit - count(lo + 1); rank > 0; rank--) at_level &= at_level - 1;
+            at = (__builtin_ffsll(at_level) - 1) & (kWave - 1);
+            before = 0;
+            index = lo - __builtin_amdgcn_readlane(from, at);
+            t.b = at;
+            t.q0 = __builtin_amdgcn_readlane(q_first, at);
+            t.qlen = __builtin_amdgcn_readlane(q_last, at) - t.q0;
+        } else if (per == 1) {
             t.b = at;
             t.q0 = __builtin_amdgcn_readlane(q_first, at);
             t.qlen = __builtin_amdgcn_readlane(q_last, at) - t.q0;

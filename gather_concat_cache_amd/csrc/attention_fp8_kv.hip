@@ -22,7 +22,7 @@ __global__ __launch_bounds__(kTileWaves * kWave, DP <= 128 ? 2 : 1) void k_fp8_r
     const int64_t wg = wg0 + blockIdx.x, per = 8 * (int64_t)p.hk;
     const int rem = (int)(wg % per), kvh = rem / 8;
     RowTile t;
-    if (!find_tile(p, wg / per * 8 + rem % 8, kTileRows, t)) return;
+    if (!find_tile<true>(p, wg / per * 8 + rem % 8, kTileRows, t)) return;
     int v0, v1;
     if (!key_range(t, v0, v1)) return;
     attend_tile<PagedFp8, DP, DP, 1, UNI, TREE>(p, t, kvh, v0, v1, lds);
@@ -49,10 +49,12 @@ static hipError_t launch_rows(const AttnParams& p, bool uni, hipStream_t s) {
 // ---------------------------------------------------------------------------
 constexpr int kFew = 4;                                  // waves
 
-// V rows: the transpose read of lane group g takes rows 4 g + i and 16 + 4 g + i.
+// V rows: the transpose read of two lane groups takes a chunk of the rows 8 n + i
+// and 16 + 8 n + i, i < 8.
 template <int NC>
 __device__ __forceinline__ int few_value_swizzle(int r) {
-    return NC == 4 ? (r >> 1 & 1) | (r >> 3 & 2) : (r & 3) | (r >> 2 & 4);
+    constexpr int W = kWindow<NC>;
+    return W == 16 ? (r & 7) | (r >> 1 & 8) : W == 8 ? (r >> 1 & 3) | (r >> 2 & 4) : (r >> 2 & 1) | (r >> 3 & 2);
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -68,7 +70,7 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
     constexpr int SIDE = kTileKeys * DP;                 // bytes
     constexpr int OROW = DP + 4;
     static_assert(kFew * 16 * OROW * 4 <= kFew * 4 * SIDE, "the join fits the ring");
-    __shared__ __attribute__((aligned(128))) uint8_t s_ring[kFew][4][SIDE];      // K, V of two tiles
+    __shared__ __attribute__((aligned(256))) uint8_t s_ring[kFew][4][SIDE];      // K, V of two tiles
     __shared__ float s_m[kFew][16], s_l[kFew][16];
 
     // heads of a unit 8 apart: the same XCD
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
         for (int kt = 0; kt < 2; kt++)
 #pragma unroll
             for (int j = 0; j < KS / 2; j++)
-                raw[kt][j] = read_lds<u32x4>((k_at ^ (j & 1) << 6) + (j >> 1) * 128 + kt * 16 * DP);
+                raw[kt][j] = read_lds<u32x4>(chunk_at<NC>(k_at, 4 * j) + kt * 16 * DP);
 #pragma unroll
         for (int kt = 0; kt < 2; kt++) {
 #pragma unroll
@@ -299,7 +301,7 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
             u32x2 vr[DT];
 #pragma unroll
             for (int d = 0; d < DT; d++)
-                vr[d] = __builtin_bit_cast(u32x2, read_transposed8((v_at ^ (d & (NC < 8 ? 3 : 7)) << 4) + (d >> 3) * 128));
+                vr[d] = __builtin_bit_cast(u32x2, read_transposed8(chunk_at<NC>(v_at, d)));
 #pragma unroll
             for (int d = 0; d < DT; d++) {
                 const f16x8 a = fp8_operand(fix(vr[d].x), fix(vr[d].y));

@@ -56,18 +56,32 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 
-// Which chunk of its row stands at chunk c (of NC) of LDS row r: c ^ swizzle.
-// Keys are read 16 bytes a lane, 32 rows side by side.
+// Which chunk of its row stands at chunk c (of NC) of LDS row r: c ^ swizzle,
+// within a window of the largest power of two that divides NC, at most 16
+// chunks.  LDS has 64 banks: the 16 lanes of a 16-byte read, or the 32 of an
+// 8-byte transpose read, that it serves in one clock have to cover 256 bytes.
+template <int NC>
+constexpr int kWindow = NC % 16 == 0 ? 16 : NC % 8 == 0 ? 8 : 4;
+// Keys: 16 neighbouring rows read the same chunk.
 template <int NC>
 __device__ __forceinline__ int key_swizzle(int r) {
-    return NC == 4 ? (r >> 1) & 3 : r & 7;
+    return kWindow<NC> == 16 ? r & 15 : kWindow<NC> == 8 ? r >> 1 & 7 : r >> 2 & 3;
 }
-// bf16 values: a transpose read takes rows 4 n .. 4 n + 3, two chunks each.
-// e4m3 values: rows 4 n + i and 4 n + 8 + i, one chunk each.
+// Values in bf16: rows 4 n .. 4 n + 3, four neighbouring chunks each; in e4m3:
+// rows 4 n + i and 4 n + 8 + i, two neighbouring chunks each.
 template <int NC, bool FP8>
 __device__ __forceinline__ int value_swizzle(int r) {
-    if (!FP8) return (r & 3) << 1;
-    return NC == 4 ? (r >> 1 & 1) | (r >> 2 & 2) : (r & 3) | (r >> 1 & 4);
+    constexpr int W = kWindow<NC>;
+    if (!FP8) return W == 16 ? (r & 3) << 2 : (r & 3) << 1;
+    return W == 16 ? (r & 3) << 1 | (r & 8) : W == 8 ? (r & 2) | (r >> 1 & 4) : r >> 2 & 2;
+}
+// Chunk number a + b of a row, where `at` is the place of its chunk a < the
+// smallest power of two in b's numbers: an exclusive or inside a window, an
+// addition from window to window.
+template <int NC>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t at, int b) {
+    constexpr int W = kWindow<NC>;
+    return (at ^ (uint32_t)(b % W) << 4) + b / W * W * 16;
 }
 
 // What differs between the two sources.
@@ -163,8 +177,8 @@ template <int N> struct ScaleLds<false, N> {};
 template <typename T, int DK, int DV, bool UNI>
 struct StepLds : ScaleLds<T::kFp8, UNI ? kStep / 16 : kStep> {
     static constexpr int KB = DK * T::kBytes, VB = DV * T::kBytes;       // bytes of a row
-    alignas(128) uint8_t k[2][kStep * KB];
-    alignas(128) uint8_t v[2][kStep * VB];
+    alignas(256) uint8_t k[2][kStep * KB];
+    alignas(256) uint8_t v[2][kStep * VB];
 };
 
 // One side's 64 rows of a packed prompt into LDS: wave w issues every fourth
@@ -400,7 +414,7 @@ __device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::f
 #pragma unroll
             for (int j = 0; j < 16; j++) s[r][kt][j] = 0.0f;
     stream<2 * J, 4, u32x4>(
-        [&](int n) { return read_lds<u32x4>((k_at ^ (n % J & 3) << 5) + (n % J >> 2) * 128 + n / J * 32 * KB); },
+        [&](int n) { return read_lds<u32x4>(chunk_at<KB / 16>(k_at, 2 * (n % J)) + n / J * 32 * KB); },
         [&](int n, const u32x4& x) {
             const int kt = n / J, st = n % J * PER;
             if constexpr (T::kFp8) {
@@ -508,8 +522,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     const int pos_lo = t.ctx + min(t.row0 + 32 * R * w, t.row0 + t.rows - 1) / p.group;
     const int pos_hi = t.ctx + min(t.row0 + 32 * R * (w + 1) - 1, t.row0 + t.rows - 1) / p.group;
 
-    // ---- where a lane reads: K rows c and 32 + c; V rows of its 16-lane group.  Swizzles move chunks within 128 bytes,
-    // so a fragment's place is an exclusive or below 128 and an addition above
+    // ---- where a lane reads: K rows c and 32 + c; V rows of its 16-lane group
     const uint32_t k_lane = lds_k + c * L::KB + ((h ^ key_swizzle<KC>(c)) << 4);
     const int i = lane & 15, dim_half = lane >> 4 & 1;
     const int v_row = FP8 ? 4 * h + (i >> 1 & 3) + 8 * (i >> 3) : 4 * h + (i >> 2);
@@ -620,13 +633,16 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                 if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sum, lds.at[n & 3][g].inv_v, l[r]);
                 else l[r] += sum;
             }
+            // summed here, or else 32 weights stay in registers: 192 dims then spill (724 against 1029 TFLOP/s), but
+            // 128 have the room (973 against 925)
+            if constexpr (DK > 128 && DV <= 128) asm volatile("" : "+v"(l[r]));
         }
     };
     const auto add_values = [&](int n) {
         const uint32_t v_at = v_lane + (n & 1) * (int)sizeof(lds.v[0]);
         const auto load_v = [&](int n) {
             const int d = n % DT;
-            const uint32_t at = (v_at ^ (FP8 ? (d & 3) << 5 : (d & 1) << 6)) + (FP8 ? d >> 2 : d >> 1) * 128 + n / DT * 16 * L::VB;
+            const uint32_t at = chunk_at<VC>(v_at, (FP8 ? 2 : 4) * d) + n / DT * 16 * L::VB;
             RawFrag<T> x;
             if constexpr (FP8) x.w = __builtin_bit_cast(u32x2, read_transposed8(at));
             else {

@@ -23,7 +23,7 @@ __global__ __launch_bounds__(kTileWaves * kWave, DK <= 192 ? 2 : 1) void k_promp
     }
     if (kvh >= p.hk) return;
     RowTile t;
-    if (!find_tile(p, unit, kTileRows, t)) return;
+    if (!find_tile<true>(p, unit, kTileRows, t)) return;
     int v0, v1;
     if (!key_range(t, v0, v1)) return;
     attend_tile<PackedBf16, DK, DV, 1, EX, false>(p, t, kvh, v0, v1, lds);
