@@ -32,6 +32,8 @@ __device__ __forceinline__ RowEnd row_end(const PromptParams& p, int64_t token, 
     }
     return e;
 }
+__device__ __forceinline__ bool accumulates(const AttnParams&) { return false; }
+__device__ __forceinline__ bool accumulates(const PromptParams& p) { return p.accumulate; }
 // Four dims of a row.
 __device__ __forceinline__ void write_dims(const AttnParams&, const RowEnd& e, uint16_t* dst, float a, float b, float c, float d) {
     *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16x2(a * e.scale, b * e.scale), pack_bf16x2(c * e.scale, d * e.scale)};

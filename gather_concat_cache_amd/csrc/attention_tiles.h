@@ -323,6 +323,14 @@ template <typename V>
 __device__ __forceinline__ V read_lds(uint32_t at) {
     return *reinterpret_cast<const __attribute__((address_space(3))) V*>(at);
 }
+__device__ __forceinline__ void write_lds(uint32_t at, u32x2 x) {
+    *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(at) = x;
+}
+// Between a wave's own writes and reads of LDS: they are done in order, the
+// compiler only has to keep them so.
+__device__ __forceinline__ void wave_lds_ready() {
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+}
 __device__ __forceinline__ i16x4 read_transposed16(uint32_t at) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) i16x4*>(at));
 }
@@ -450,6 +458,13 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     typedef typename T::frag frag;
     constexpr int KS = DK / 16, DT = DV / 32, KC = L::KB / 16, VC = L::VB / 16;
     constexpr bool FP8 = T::kFp8;
+    // Sums of weights where the weights are made: left to the compiler they follow the step, and 32 weights stay in
+    // registers meanwhile.  With 192 dims those spill (724 against 1029 TFLOP/s); e4m3 540 against 557 us for 4 x 2048
+    // tokens over 4096 keys, 64 dims 804 against 782 TFLOP/s, but 128 dims of bf16 946 against 949 and 256 929 against 936.
+    constexpr bool kSumEarly = FP8 || DK % 128 != 0;
+    // A higher wave priority while matrix instructions are issued: 128 dims 963 against 949 TFLOP/s, e4m3 531 against 557
+    // us, 192 as before; but 64 dims 761 against 780 and 256 919 against 936.
+    constexpr bool kRaise = DK == 128 || DK == 192;
     const int lane = lane_id(), w = wave_id(), c = lane & 31, h = lane >> 5;
 
     // ---- steps: one or two consecutive 32-key tiles of one run (sinks, then the window)
@@ -633,9 +648,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                 if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sum, lds.at[n & 3][g].inv_v, l[r]);
                 else l[r] += sum;
             }
-            // summed here, or else 32 weights stay in registers: 192 dims then spill (724 against 1029 TFLOP/s), but
-            // 128 have the room (973 against 925)
-            if constexpr (DK > 128 && DV <= 128) asm volatile("" : "+v"(l[r]));
+            if constexpr (kSumEarly) asm volatile("" : "+v"(l[r]));
         }
     };
     const auto add_values = [&](int n) {
@@ -708,9 +721,11 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         if (busy) {                                      // wave-uniform
             f32x16 x[R][2];
             float top[R];
+            if constexpr (kRaise) __builtin_amdgcn_s_setprio(1);
             multiply_keys<T, KS, L::KB, R>(k_lane + ((n + 1) & 1) * (int)sizeof(lds.k[0]), q, x);
             weigh(n);
             add_values(n);
+            if constexpr (kRaise) __builtin_amdgcn_s_setprio(0);
             scale_scores(n + 1, x);
             find_top(x, top);
             settle(vn, n + 1, x, top);
@@ -740,7 +755,10 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
             for (int d = 0; d < DT; d++)
 #pragma unroll
                 for (int j = 0; j < 16; j++) odd = odd || o[r][d][j] != o[r][d][j];
-        uint32_t* flag = reinterpret_cast<uint32_t*>(lds.k[0]);  // the steps are done with it
+        // (the steps are done with this place, and the rows below do not reach it)
+        uint32_t* flag;
+        if constexpr (FP8) flag = reinterpret_cast<uint32_t*>(lds.at[0]);
+        else flag = reinterpret_cast<uint32_t*>(lds.v[1] + sizeof(lds.v[1]) - 16);
         tile_ready();
         if (lane == 0) flag[w] = 0;
         if (busy && odd) flag[w] = 1;
@@ -748,15 +766,21 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         if (flag[0] | flag[1] | flag[2] | flag[3]) return true;
     }
 
-    // ---- each lane holds runs of four dims of its rows
+    // ---- each lane holds runs of four dims of its rows.  They go through LDS, so that a store writes whole rows (16 bytes
+    // a lane; as they are, 32 rows would get 16 bytes each a store), but for sums that meet what out holds
     const bool partial = p.splits > 1 && t.total > t.chunk;
+    constexpr int OC = DV / 8, OW = OC < 16 ? OC : 16;   // chunks of an output row, and those that a row's swizzle permutes
+    static_assert(kTileWaves * 32 * 16 * OC + (FP8 ? 0 : 16) <= sizeof(lds.k) + sizeof(lds.v), "rows of all waves fit");
+    const uint32_t mine = lds_k + w * 32 * 16 * OC;
+    if (CAREFUL) tile_ready();
 #pragma unroll
     for (int r = 0; r < R; r++) {
         const float ll = pair_sum(l[r]);
-        if (row_of[r] < 0) continue;
-        const int tl = row_of[r] / p.group, head = kvh * p.group + row_of[r] - tl * p.group;
+        const bool in = row_of[r] >= 0;
+        const int row = max(row_of[r], 0), tl = row / p.group, head = kvh * p.group + row - tl * p.group;
         const int64_t token = t.q0 + tl, id = token * p.hq + head;
         if (partial) {
+            if (!in) continue;
             if (h == 0) {
                 float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
                 ml[0] = m[r] - T::kShiftUp + kShift;     // the join takes kShift off
@@ -770,18 +794,43 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                     if (EX || 32 * d + 8 * a + 4 * h < p.hs)
                         *reinterpret_cast<f32x4*>(dst + 32 * d + 8 * a) =
                             f32x4{o[r][d][4 * a], o[r][d][4 * a + 1], o[r][d][4 * a + 2], o[r][d][4 * a + 3]};
-        } else {
-            const RowEnd end = row_end_shifted<T>(p, token, head, m[r], ll);
+            continue;
+        }
+        RowEnd end{0.0f, 0.0f, 0.0f};
+        if (in) {
+            end = row_end_shifted<T>(p, token, head, m[r], ll);
             if (h == 0 && p.lse) p.lse[token * p.lse_ts + head] = end.lse;
-            uint16_t* dst = p.out + token * p.o_ts + (int64_t)head * p.o_hs + 4 * h;
+        }
+        uint16_t* dst = p.out + token * p.o_ts + (int64_t)head * p.o_hs;
+        if (accumulates(p)) {
+            if (!in) continue;
 #pragma unroll
             for (int d = 0; d < DT; d++)
 #pragma unroll
                 for (int a = 0; a < 4; a++)
                     if (EX || 32 * d + 8 * a + 4 * h < p.hs)
-                        write_dims(p, end, dst + 32 * d + 8 * a, o[r][d][4 * a], o[r][d][4 * a + 1], o[r][d][4 * a + 2],
+                        write_dims(p, end, dst + 32 * d + 8 * a + 4 * h, o[r][d][4 * a], o[r][d][4 * a + 1], o[r][d][4 * a + 2],
                                    o[r][d][4 * a + 3]);
+            continue;
         }
+        if (!busy) continue;                             // wave-uniform
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+            for (int a = 0; a < 4; a++)
+                write_lds(mine + c * 16 * OC + (((4 * d + a) ^ (c & (OW - 1))) << 4) + 8 * h,
+                          u32x2{pack_bf16x2(o[r][d][4 * a] * end.scale, o[r][d][4 * a + 1] * end.scale),
+                                pack_bf16x2(o[r][d][4 * a + 2] * end.scale, o[r][d][4 * a + 3] * end.scale)});
+        const uint64_t to = in ? reinterpret_cast<uint64_t>(dst) : 0;
+        wave_lds_ready();
+#pragma unroll
+        for (int k = 0; k < 32 * OC / kWave; k++) {
+            const int from = (k * kWave + lane) / OC, chunk = (k * kWave + lane) % OC;
+            const u32x4 x = read_lds<u32x4>(mine + from * 16 * OC + ((chunk ^ (from & (OW - 1))) << 4));
+            const uint64_t at = (uint64_t)(uint32_t)__shfl((int)(to >> 32), from) << 32 | (uint32_t)__shfl((int)to, from);
+            if (at != 0 && (EX || 8 * chunk < p.hs)) *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(at) + 8 * chunk) = x;
+        }
+        wave_lds_ready();
     }
     return false;
 }
