@@ -105,6 +105,7 @@ struct RowTile {
     int qlen, ctx, kv_len;       // ctx = position of the request's first query
     int sink_tiles, win_tile0, total;   // 32-key tiles: [0, sink_tiles) then from win_tile0
     int split, splits, chunk;    // the unit's key split, splits of the request, key tiles of one
+    int keys, k0;                // the request's keys, and its first key row (packed prompts)
 };
 
 __device__ __forceinline__ int query_start(const AttnParams& p, int b) {
@@ -118,6 +119,7 @@ __device__ __forceinline__ int key_count(const AttnParams& p, int b) { return ma
 __device__ __forceinline__ int64_t addressable_keys(const AttnParams& p) {
     return p.blocks > 0 ? min(p.bt_stride * p.div.size, (int64_t)INT32_MAX - 2 * kTileKeys) : 0;
 }
+__device__ __forceinline__ int key_start(const AttnParams&, int) { return 0; }
 __device__ __forceinline__ int first_position(const AttnParams&, int keys, int qlen) {
     return keys - qlen;          // may be negative: those rows see nothing
 }
@@ -132,12 +134,12 @@ __device__ __forceinline__ int first_position(const PromptParams& p, int keys, i
     return p.causal ? keys - qlen : keys;
 }
 
-// Visible 32-key tiles of rows [row0, row0 + rows) of request b.
+// Visible 32-key tiles of rows [row0, row0 + rows) of request b, whose keys are t.keys.
 template <typename P>
 __device__ __forceinline__ void tile_range(const P& p, RowTile& t) {
     // key numbers stay clear of int32's end, so key0 + 32 cannot wrap
     const int64_t table_keys = addressable_keys(p);
-    const int seq = key_count(p, t.b);
+    const int seq = t.keys;
     t.ctx = first_position(p, seq, t.qlen);
     t.kv_len = (int)min((int64_t)seq, table_keys);
     const int p0 = t.ctx + t.row0 / p.group;
@@ -163,6 +165,16 @@ __device__ __forceinline__ int scan_lanes(int x) {
     x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // last lane of rows 0 and 2 to rows 1 and 3
     x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // last lane of the lower half to the upper
     return x;
+}
+
+__device__ __forceinline__ int max_lanes(int x) {          // of values >= 0
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));
+    return __builtin_amdgcn_readlane(x, kWave - 1);
 }
 
 // 32-key tiles of a request, as far as the plan counts them: at most key_tiles,
@@ -210,6 +222,7 @@ __device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowT
     int index, before;
     t.splits = 1;
     t.chunk = INT32_MAX;
+    t.keys = -1;
     if (counts_requests(p.batch, p.hk)) {
         const bool split = p.splits > 1;
         const int per = (p.batch + kWave - 1) / kWave;
@@ -217,6 +230,9 @@ __device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowT
         const int q_first = query_start(p, min(b0, p.batch)), q_last = query_start(p, min(b0 + 1, p.batch));
         const int tiles1 = tiles_of((q_last - q_first) * p.group);                  // where a lane has one request
         const int work1 = split ? request_work(p, min(b0, p.batch - 1)) : 0;
+        // (loaded beside the queries' starts)
+        const int keys1 = SORTED ? key_count(p, min(b0, p.batch - 1)) : 0;
+        const int start1 = SORTED ? key_start(p, min(b0, p.batch - 1)) : 0;
         const auto sum = [&](auto of) {                  // of(row tiles, work) over the lane's requests
             if (per == 1) return of(tiles1, work1);
             decltype(of(0, 0)) n = 0;
@@ -254,15 +270,12 @@ __device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowT
         int work = work1;
         if (SORTED && per == 1 && !split) {
             // level of a request's tile j: from + j; count(x) tiles have level x or more
-            const int keys = key_count(p, min(b0, p.batch - 1)), qlen = max(q_last - q_first, 0);
-            const int from = (int)((int64_t)max(first_position(p, keys, qlen), 0) * p.group / RT);
+            const int qlen = max(q_last - q_first, 0);
+            const int from = (int)((int64_t)max(first_position(p, keys1, qlen), 0) * p.group / RT);
             const auto count = [&](int x) {
                 return __builtin_amdgcn_readlane(scan_lanes(n > 0 ? min(max(from + n - x, 0), n) : 0), kWave - 1);
             };
-            int most = n > 0 ? from + n : 0;
-#pragma unroll
-            for (int d = 1; d < kWave; d <<= 1) most = max(most, __shfl_xor(most, d));
-            int lo = 0, hi = __builtin_amdgcn_readfirstlane(most);       // the unit's level is in [lo, hi)
+            int lo = 0, hi = max_lanes(n > 0 ? from + n : 0);            // the unit's level is in [lo, hi)
             while (hi - lo > 1) {
                 const int mid = (int)(((int64_t)lo + hi) >> 1);
                 if (count(mid) > unit) lo = mid;
@@ -276,6 +289,8 @@ __device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowT
             t.b = at;
             t.q0 = __builtin_amdgcn_readlane(q_first, at);
             t.qlen = __builtin_amdgcn_readlane(q_last, at) - t.q0;
+            t.keys = __builtin_amdgcn_readlane(keys1, at);
+            t.k0 = __builtin_amdgcn_readlane(start1, at);
         } else if (per == 1) {
             t.b = at;
             t.q0 = __builtin_amdgcn_readlane(q_first, at);
@@ -316,6 +331,10 @@ __device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowT
     if (t.qlen <= 0 || row0 < 0 || row0 >= rows) return false;
     t.row0 = (int)row0;
     t.rows = (int)min((int64_t)RT, rows - row0);
+    if (t.keys < 0) {
+        t.keys = key_count(p, t.b);
+        t.k0 = key_start(p, t.b);
+    }
     tile_range(p, t);
     return true;
 }

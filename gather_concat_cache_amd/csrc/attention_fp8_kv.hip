@@ -19,10 +19,10 @@ template <int DP, bool UNI, bool TREE>
 __global__ __launch_bounds__(kTileWaves * kWave, DP <= 128 ? 2 : 1) void k_fp8_rows(AttnParams p, int64_t wg0) {
     __shared__ StepLds<PagedFp8, DP, DP, UNI> lds;
     // heads of a unit 8 apart: the same XCD
-    const int64_t wg = wg0 + blockIdx.x, per = 8 * (int64_t)p.hk;
-    const int rem = (int)(wg % per), kvh = rem / 8;
+    const uint32_t wg = (uint32_t)wg0 + blockIdx.x, per = 8 * (uint32_t)p.hk, set = wg / per, rem = wg - set * per;
+    const int kvh = (int)(rem / 8);
     RowTile t;
-    if (!find_tile<true>(p, wg / per * 8 + rem % 8, kTileRows, t)) return;
+    if (!find_tile<true>(p, set * 8 + rem % 8, kTileRows, t)) return;
     int v0, v1;
     if (!key_range(t, v0, v1)) return;
     attend_tile<PagedFp8, DP, DP, 1, UNI, TREE>(p, t, kvh, v0, v1, lds);
@@ -74,10 +74,10 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
     __shared__ float s_m[kFew][16], s_l[kFew][16];
 
     // heads of a unit 8 apart: the same XCD
-    const int64_t wg = wg0 + blockIdx.x, per = 8 * (int64_t)p.hk;
-    const int rem = (int)(wg % per), kvh = rem / 8;
+    const uint32_t wg = (uint32_t)wg0 + blockIdx.x, per = 8 * (uint32_t)p.hk, set = wg / per, rem = wg - set * per;
+    const int kvh = (int)(rem / 8);
     RowTile t;
-    if (!find_tile(p, wg / per * 8 + rem % 8, 16 * R, t)) return;
+    if (!find_tile(p, set * 8 + rem % 8, 16 * R, t)) return;
     int v0, v1;
     if (!key_range(t, v0, v1)) return;
 

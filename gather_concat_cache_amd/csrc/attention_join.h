@@ -87,6 +87,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_attention_join(P p, int64_t w
     const int row = tl * p.group + head % p.group;
     t.row0 = row / RT * RT;
     t.rows = (int)min((int64_t)RT, (int64_t)t.qlen * p.group - t.row0);
+    t.keys = key_count(p, t.b);
     tile_range(p, t);
     const int chunk = *p.ws_chunk;
     if (t.total <= chunk) return;                        // written by its only workgroup

@@ -478,7 +478,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     std::conditional_t<FP8, PageWalk<DK, EX>, NoWalk> walk;
     if constexpr (FP8) walk.init(p, t, kvh, w);
     else {
-        const int64_t first = key_start(p, t.b);
+        const int64_t first = __builtin_amdgcn_readfirstlane(t.k0);
         stride[0] = 2 * p.k_ts;
         stride[1] = 2 * p.v_ts;
         base[0] = reinterpret_cast<const uint8_t*>(p.k + first * p.k_ts + kvh * p.k_hs);
@@ -748,20 +748,21 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     }
 
     if constexpr (!CAREFUL) {
-        bool odd = false;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // a NaN anywhere makes one here
 #pragma unroll
         for (int r = 0; r < R; r++)
 #pragma unroll
             for (int d = 0; d < DT; d++)
 #pragma unroll
-                for (int j = 0; j < 16; j++) odd = odd || o[r][d][j] != o[r][d][j];
-        // (the steps are done with this place, and the rows below do not reach it)
+                for (int j = 0; j < 16; j++) sum[j & 3] += o[r][d][j];
+        const float any = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // a place that the last step does not use, nor the output rows below
         uint32_t* flag;
-        if constexpr (FP8) flag = reinterpret_cast<uint32_t*>(lds.at[0]);
-        else flag = reinterpret_cast<uint32_t*>(lds.v[1] + sizeof(lds.v[1]) - 16);
-        tile_ready();
+        if constexpr (FP8) flag = reinterpret_cast<uint32_t*>(lds.at[(n + 1) & 3]);
+        else flag = reinterpret_cast<uint32_t*>(lds.v[(n + 1) & 1]);
         if (lane == 0) flag[w] = 0;
-        if (busy && odd) flag[w] = 1;
+        wave_lds_ready();
+        if (busy && any != any) flag[w] = 1;
         __syncthreads();
         if (flag[0] | flag[1] | flag[2] | flag[3]) return true;
     }
@@ -770,7 +771,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     // a lane; as they are, 32 rows would get 16 bytes each a store), but for sums that meet what out holds
     const bool partial = p.splits > 1 && t.total > t.chunk;
     constexpr int OC = DV / 8, OW = OC < 16 ? OC : 16;   // chunks of an output row, and those that a row's swizzle permutes
-    static_assert(kTileWaves * 32 * 16 * OC + (FP8 ? 0 : 16) <= sizeof(lds.k) + sizeof(lds.v), "rows of all waves fit");
+    static_assert(kTileWaves * 32 * 16 * OC <= sizeof(lds.k) + (FP8 ? sizeof(lds.v) : 0), "rows of all waves fit");
     const uint32_t mine = lds_k + w * 32 * 16 * OC;
     if (CAREFUL) tile_ready();
 #pragma unroll

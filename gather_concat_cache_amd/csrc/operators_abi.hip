@@ -498,6 +498,7 @@ int gcache_attention_fp8_kv(const gcache_attention_args* a, const void* kv_cache
     const AttnPlan plan = plan_attention_fp8(p.total_q, p.batch, p.hq, hk, hs, a->max_seq_len, window, num_sinks,
                                              workspace_floats(a->workspace, a->workspace_bytes));
     use_plan(plan, a->workspace, &p);
+    if (((int64_t)p.units + 7) * hk > INT32_MAX) return GCACHE_ERR_SHAPE;    // workgroups are numbered in 32 bits
     return launched(launch_attention_fp8(p, plan.row_tiles, stream));
 }
 
@@ -574,6 +575,7 @@ int gcache_prompt_attention(const gcache_prompt_args* a, hipStream_t stream) {
     const AttnPlan plan = plan_attention_prompt(p.total_q, p.batch, p.hq, p.hk, p.dk, p.hs, a->max_key_len, p.window, p.sinks,
                                                 workspace_floats(a->workspace, a->workspace_bytes));
     use_plan(plan, a->workspace, &p);
+    if (((int64_t)p.units + 7) * p.hk > INT32_MAX) return GCACHE_ERR_SHAPE;  // workgroups are numbered in 32 bits
     return launched(launch_attention_prompt(p, stream));
 }
 

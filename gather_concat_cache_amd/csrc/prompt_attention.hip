@@ -10,23 +10,22 @@ __global__ __launch_bounds__(kTileWaves * kWave, DK <= 192 ? 2 : 1) void k_promp
     // Workgroups of a kv head get numbers that are equal modulo 8 (or its
     // divisor): one XCD, whose L2 then serves a request's keys to all of its
     // row tiles.
-    const int64_t wg = wg0 + blockIdx.x, units = p.units;
-    int kvh;
-    int64_t unit;
-    if (p.hk % 8 == 0) {
-        const int64_t per = 8 * units, part = wg / per, in = wg - part * per;
-        kvh = (int)(part * 8 + in % 8);
+    const uint32_t wg = (uint32_t)wg0 + blockIdx.x, units = (uint32_t)p.units, hk = (uint32_t)p.hk;
+    uint32_t kvh, unit;
+    if (hk % 8 == 0) {
+        const uint32_t part = wg / (8 * units), in = wg - part * 8 * units;
+        kvh = part * 8 + in % 8;
         unit = in / 8;
     } else {
-        kvh = (int)(wg % p.hk);
-        unit = wg / p.hk;
+        unit = wg / hk;
+        kvh = wg - unit * hk;
     }
-    if (kvh >= p.hk) return;
+    if (kvh >= hk) return;
     RowTile t;
     if (!find_tile<true>(p, unit, kTileRows, t)) return;
     int v0, v1;
     if (!key_range(t, v0, v1)) return;
-    attend_tile<PackedBf16, DK, DV, 1, EX, false>(p, t, kvh, v0, v1, lds);
+    attend_tile<PackedBf16, DK, DV, 1, EX, false>(p, t, (int)kvh, v0, v1, lds);
 }
 
 template <int DK, int DV>
