@@ -163,6 +163,8 @@ hipError_t launch_parts(void (*kernel)(P, int64_t), int waves, int row_tile, con
     p.data_token = (uint32_t)p.L.data_token_stride;
     p.scale_token = (uint32_t)p.L.scale_token_stride;
     p.row_tile = row_tile;
+    p.group_shift = p.group > 1 ? 32 - __builtin_clz((unsigned)p.group - 1) : 0;
+    p.group_mul = (uint32_t)(((uint64_t(1) << (32 + p.group_shift)) + p.group - 1) / p.group - (uint64_t(1) << 32));
     const int64_t units = p.units;
     const bool join = p.splits > 1;
     const hipError_t e = launch_span(kernel, (units + 7) / 8 * 8 * p.hk, waves * kWave, s, true, !join, p);

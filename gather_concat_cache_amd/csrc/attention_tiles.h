@@ -41,8 +41,12 @@ constexpr int kStep = 64, kTileWaves = 4, kTileRows = 128;   // keys of a step, 
 // every read of any LDS buffer wait for the newest load.  m0 needs a wait state
 // before an LDS load uses it.
 __device__ __forceinline__ void load_lds(uint32_t lds, const void* base, uint32_t offset) {
+    // (the base is the same in all lanes, which the compiler does not always see)
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    const uint64_t s = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)b);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 : : "s"(lds), "v"(offset), "s"(base) : "memory");
+                 : : "s"(lds), "v"(offset), "s"(s) : "memory");
 }
 __device__ __forceinline__ void load_lds(uint32_t lds, const void* lane_address) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
@@ -141,6 +145,12 @@ __device__ __forceinline__ float max16(const f32x16& a) {
 template <bool TREE>
 __device__ __forceinline__ void hide_step(const AttnParams& p, const RowTile& t, int pos, int tok, int key0, uint32_t live,
                                           f32x16* x) {
+    if (!TREE && p.window <= 0 && __all(live == ~0u)) {  // causal alone
+        const int last = sight_hi<TREE>(t, pos) - key0;
+#pragma unroll
+        for (int j = 0; j < 32; j++) x[j >> 4][j & 15] = 8 * (j >> 2) + (j & 3) <= last ? x[j >> 4][j & 15] : kNegInf;
+        return;
+    }
     uint32_t see = live & step_keys_upto(sight_hi<TREE>(t, pos), key0);
     if (TREE) {
         const uint8_t* row = p.mask + (int64_t)tok * p.mask_ts;
@@ -303,20 +313,31 @@ struct PageWalk {
 };
 struct NoWalk {};
 
-// N fragments with DEPTH reads in flight: the barrier keeps reads and matrix
-// instructions in this order.
-template <int N, int DEPTH, typename F, typename Load, typename Use>
-__device__ __forceinline__ void stream(Load load, Use use) {
+// N fragments with DEPTH reads in flight.  Piece i of `side`, vector work that
+// needs none of them, follows the matrix instructions of fragment i and runs
+// beside them; the barriers keep reads, matrix instructions and pieces in this
+// order (left to the compiler the pieces often come first or last: 929 against
+// 994 TFLOP/s from one build to the next).
+template <int N, int DEPTH, typename F, typename Load, typename Use, typename Side>
+__device__ __forceinline__ void stream(Load load, Use use, Side side) {
     F b[DEPTH];
 #pragma unroll
     for (int i = 0; i < DEPTH; i++) b[i] = load(i);
-    __builtin_amdgcn_sched_barrier(0x676);
+    __builtin_amdgcn_sched_barrier(0x274);
 #pragma unroll
     for (int i = 0; i < N; i++) {
         use(i, b[i % DEPTH]);
         if (i + DEPTH < N) b[i % DEPTH] = load(i + DEPTH);
-        __builtin_amdgcn_sched_barrier(0x676);
+        side(i);
+        __builtin_amdgcn_sched_barrier(0x274);
     }
+}
+// The i-th of N parts of COUNT pieces: run(piece) for each.
+template <int N, int COUNT, typename Run>
+__device__ __forceinline__ void part_of(int i, Run run) {
+#pragma unroll
+    for (int k = 0; k < COUNT; k++)
+        if (k * N / COUNT == i) run(k);
 }
 
 template <typename V>
@@ -412,8 +433,8 @@ __device__ __forceinline__ void load_rows_q(const AttnParams& p, const uint16_t*
 
 // Scores of a step: S^T = K Q^T.  A 16-byte read is one step's operand in bf16,
 // two steps' in e4m3.
-template <typename T, int KS, int KB, int R>
-__device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::frag (*q)[KS], f32x16 (*s)[2]) {
+template <typename T, int KS, int KB, int R, typename Side>
+__device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::frag (*q)[KS], f32x16 (*s)[2], Side side) {
     constexpr int PER = T::kFp8 ? 2 : 1, J = KS / PER;
 #pragma unroll
     for (int r = 0; r < R; r++)
@@ -437,7 +458,8 @@ __device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::f
 #pragma unroll
                 for (int r = 0; r < R; r++) s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
             }
-        });
+        },
+        side);
 }
 
 // One tile of up to 128 R rows over the 32-key tiles [v0, v1).
@@ -527,15 +549,15 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     for (int r = 0; r < R; r++) {
         const int off = 32 * (R * w + r) + c;
         const bool in = off < t.rows;
-        const int row = in ? t.row0 + off : t.row0, tl = row / p.group, head = kvh * p.group + row - tl * p.group;
+        const int row = in ? t.row0 + off : t.row0, tl = row_token(p, row), head = kvh * p.group + row - tl * p.group;
         row_of[r] = in ? row : -1;
         tok[r] = t.q0 + tl;
         pos[r] = in ? t.ctx + tl : -1;
         load_rows_q<DK>(p, p.q + (int64_t)tok[r] * p.q_ts + (int64_t)head * p.q_hs, in, h, q[r], fac[r]);
     }
     const bool busy = 32 * R * w < t.rows;               // the other waves of a partly filled tile only load
-    const int pos_lo = t.ctx + min(t.row0 + 32 * R * w, t.row0 + t.rows - 1) / p.group;
-    const int pos_hi = t.ctx + min(t.row0 + 32 * R * (w + 1) - 1, t.row0 + t.rows - 1) / p.group;
+    const int pos_lo = t.ctx + row_token(p, min(t.row0 + 32 * R * w, t.row0 + t.rows - 1));
+    const int pos_hi = t.ctx + row_token(p, min(t.row0 + 32 * R * (w + 1) - 1, t.row0 + t.rows - 1));
 
     // ---- where a lane reads: K rows c and 32 + c; V rows of its 16-lane group
     const uint32_t k_lane = lds_k + c * L::KB + ((h ^ key_swizzle<KC>(c)) << 4);
@@ -562,30 +584,24 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
 
     // ---- logits of a step from its scores: scaled, shifted, the hidden ones -infinity; the running maximum, which the
     // accumulators follow with a lag
-    const auto scale_scores = [&](int n, f32x16 (*x)[2]) {
+    constexpr int kPieces = 16 * R;                      // of a step's logits or weights: two of a row's 32 each
+    const auto scale_piece = [&](int n, f32x16 (*x)[2], float* top, int piece) {
+        const int r = piece / 16, kt = piece % 16 / 8, j = piece % 8 * 2;
+        if constexpr (FP8) {
 #pragma unroll
-        for (int r = 0; r < R; r++) {
-            if constexpr (FP8 && EX) {
-#pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    const PageScale ps = lds.at[n & 3][g];
-                    const float f = fac[r] * ps.k, a = sub[r] + ps.log2_v;
-#pragma unroll
-                    for (int j = 8 * (g & 1); j < 8 * (g & 1) + 8; j++) x[r][g >> 1][j] = __builtin_fmaf(x[r][g >> 1][j], f, a);
-                }
-            } else if constexpr (FP8) {
-#pragma unroll
-                for (int j = 0; j < 32; j++) {
-                    const PageScale& ps = lds.at[n & 3][8 * (j >> 2) + 4 * h + (j & 3)];
-                    x[r][j >> 4][j & 15] = __builtin_fmaf(x[r][j >> 4][j & 15], fac[r] * ps.k, sub[r] + ps.log2_v);
-                }
-            } else {
-#pragma unroll
-                for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-                    for (int j = 0; j < 16; j++) x[r][kt][j] = __builtin_fmaf(x[r][kt][j], fac[r], sub[r]);
+            for (int i = j; i < j + 2; i++) {
+                const PageScale& ps = lds.at[n & 3][EX ? 2 * kt + i / 8 : 32 * kt + 8 * (i >> 2) + 4 * h + (i & 3)];
+                x[r][kt][i] = __builtin_fmaf(x[r][kt][i], fac[r] * ps.k, sub[r] + ps.log2_v);
             }
+        } else {
+            x[r][kt][j] = __builtin_fmaf(x[r][kt][j], fac[r], sub[r]);
+            x[r][kt][j + 1] = __builtin_fmaf(x[r][kt][j + 1], fac[r], sub[r]);
         }
+        top[r] = max3(top[r], x[r][kt][j], x[r][kt][j + 1]);
+    };
+    const auto join_top = [&](float* top) {
+#pragma unroll
+        for (int r = 0; r < R; r++) top[r] = pair_max(top[r]);
     };
     const auto find_top = [&](f32x16 (*x)[2], float* top) {
 #pragma unroll
@@ -623,35 +639,41 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                 for (int kt = 0; kt < 2; kt++)
 #pragma unroll
                     for (int j = 0; j < 16; j++) x[r][kt][j] += by;
+                if (n > 0) {
 #pragma unroll
-                for (int d = 0; d < DT; d++)
+                    for (int d = 0; d < DT; d++)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) o[r][d][j] *= al;
+                        for (int j = 0; j < 16; j++) o[r][d][j] *= al;
+                }
             }
         }
     };
     frag pw[R][4];
-    const auto weigh = [&](int n) {
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-#pragma unroll
-            for (int g = 0; g < 4; g++) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float e = __builtin_amdgcn_exp2f(s[r][g >> 1][8 * (g & 1) + j]);
-                    if constexpr (FP8 && !EX) sum += e * lds.at[n & 3][16 * g + 8 * (j >> 2) + 4 * h + (j & 3)].inv_v;
-                    else sum += e;
-                    if constexpr (FP8) pw[r][g][j] = (_Float16)e;
-                    else pw[r][g][j] = (__bf16)e;
-                }
-                if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sum, lds.at[n & 3][g].inv_v, l[r]);
-                else l[r] += sum;
-            }
+    float sums[R][4];                                    // of a 16-key group's weights
+    const auto weigh_piece = [&](int n, int piece) {
+        const int r = piece / 16, g = piece % 16 / 4, j = piece % 4 * 2;
+        const float e0 = __builtin_amdgcn_exp2f(s[r][g >> 1][8 * (g & 1) + j]);
+        const float e1 = __builtin_amdgcn_exp2f(s[r][g >> 1][8 * (g & 1) + j + 1]);
+        if constexpr (FP8) {
+            pw[r][g][j] = (_Float16)e0;
+            pw[r][g][j + 1] = (_Float16)e1;
+        } else {
+            pw[r][g][j] = (__bf16)e0;
+            pw[r][g][j + 1] = (__bf16)e1;
+        }
+        float part;
+        if constexpr (FP8 && !EX) {
+            const PageScale* ps = lds.at[n & 3] + 16 * g + 8 * (j >> 2) + 4 * h + (j & 3);
+            part = __builtin_fmaf(e0, ps[0].inv_v, e1 * ps[1].inv_v);
+        } else part = e0 + e1;
+        sums[r][g] = j == 0 ? part : sums[r][g] + part;
+        if (j == 6) {
+            if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sums[r][g], lds.at[n & 3][g].inv_v, l[r]);
+            else l[r] += sums[r][g];
             if constexpr (kSumEarly) asm volatile("" : "+v"(l[r]));
         }
     };
-    const auto add_values = [&](int n) {
+    const auto add_values = [&](int n, auto side) {
         const uint32_t v_at = v_lane + (n & 1) * (int)sizeof(lds.v[0]);
         const auto load_v = [&](int n) {
             const int d = n % DT;
@@ -670,13 +692,13 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
             for (int r = 0; r < R; r++) o[r][n % DT] = T::mma(a, pw[r][n / DT], o[r][n % DT]);
         };
         if constexpr (!CAREFUL) {
-            stream<4 * DT, 4, RawFrag<T>>(load_v, [&](int n, const RawFrag<T>& x) { add(n, operand(x)); });
+            stream<4 * DT, 4, RawFrag<T>>(load_v, [&](int n, const RawFrag<T>& x) { add(n, operand(x)); }, side);
         } else {
             uint32_t odd = 0;
             stream<4 * DT, 2, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
                 odd |= drop_nonfinite(x);
                 add(n, operand(x));
-            });
+            }, side);
             // rows that do see a value that is not finite get an infinity in its dim (the sum is not finite there), the
             // product of two large values
             if constexpr (!FP8) {
@@ -689,7 +711,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                     stream<4 * DT, 2, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
                         keep_nonfinite(x);
                         add(n, operand(x));
-                    });
+                    }, [](int) {});
                 }
             }
         }
@@ -700,10 +722,13 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         tile_ready();
         if (vn < v1) issue_keys(vn, 1);
         if (busy) {
-            multiply_keys<T, KS, L::KB, R>(k_lane, q, s);
+            multiply_keys<T, KS, L::KB, R>(k_lane, q, s, [](int) {});
             float top[R];
-            scale_scores(0, s);
-            find_top(s, top);
+#pragma unroll
+            for (int r = 0; r < R; r++) top[r] = kNegInf;
+#pragma unroll
+            for (int k = 0; k < kPieces; k++) scale_piece(0, s, top, k);
+            join_top(top);
             settle(v, 0, s, top);
         }
     }
@@ -722,12 +747,14 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
             f32x16 x[R][2];
             float top[R];
             if constexpr (kRaise) __builtin_amdgcn_s_setprio(1);
-            multiply_keys<T, KS, L::KB, R>(k_lane + ((n + 1) & 1) * (int)sizeof(lds.k[0]), q, x);
-            weigh(n);
-            add_values(n);
+#pragma unroll
+            for (int r = 0; r < R; r++) top[r] = kNegInf;
+            constexpr int NK = 2 * KS / (FP8 ? 2 : 1), NV = 4 * DT;
+            multiply_keys<T, KS, L::KB, R>(k_lane + ((n + 1) & 1) * (int)sizeof(lds.k[0]), q, x,
+                                           [&](int i) { part_of<NK, kPieces>(i, [&](int k) { weigh_piece(n, k); }); });
+            add_values(n, [&](int i) { part_of<NV, kPieces>(i, [&](int k) { scale_piece(n + 1, x, top, k); }); });
             if constexpr (kRaise) __builtin_amdgcn_s_setprio(0);
-            scale_scores(n + 1, x);
-            find_top(x, top);
+            join_top(top);
             settle(vn, n + 1, x, top);
 #pragma unroll
             for (int r = 0; r < R; r++)
@@ -742,8 +769,9 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     if (v < v1) {
         tile_ready();
         if (busy) {
-            weigh(n);
-            add_values(n);
+#pragma unroll
+            for (int k = 0; k < kPieces; k++) weigh_piece(n, k);
+            add_values(n, [](int) {});
         }
     }
 
@@ -778,7 +806,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     for (int r = 0; r < R; r++) {
         const float ll = pair_sum(l[r]);
         const bool in = row_of[r] >= 0;
-        const int row = max(row_of[r], 0), tl = row / p.group, head = kvh * p.group + row - tl * p.group;
+        const int row = max(row_of[r], 0), tl = row_token(p, row), head = kvh * p.group + row - tl * p.group;
         const int64_t token = t.q0 + tl, id = token * p.hq + head;
         if (partial) {
             if (!in) continue;

@@ -42,6 +42,7 @@ struct AttnParams {
     float* ws_ml;                // [splits, total_q * hq, 2]
     int32_t* ws_chunk;           // [1] key tiles of a split, from the attention kernel to the join
     int32_t row_tile;            // rows of a row tile (set by the launcher, for the join)
+    uint32_t group_mul, group_shift;     // division by group (set by the launcher): see row_token()
 };
 
 // Attention of packed prompts: the same, with keys and values in packed rows.
