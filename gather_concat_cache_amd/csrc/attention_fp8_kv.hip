@@ -18,14 +18,13 @@ namespace gcache {
 template <int DP, bool UNI, bool TREE>
 __global__ __launch_bounds__(kTileWaves * kWave, DP <= 128 ? 2 : 1) void k_fp8_rows(AttnParams p, int64_t wg0) {
     __shared__ StepLds<PagedFp8, DP, DP, UNI> lds;
-    // heads of a unit 8 apart: the same XCD
-    const uint32_t wg = (uint32_t)wg0 + blockIdx.x, per = 8 * (uint32_t)p.hk, set = wg / per, rem = wg - set * per;
-    const int kvh = (int)(rem / 8);
+    uint32_t kvh, unit;
+    if (!head_and_unit(p, (uint32_t)wg0 + blockIdx.x, kvh, unit)) return;
     RowTile t;
-    if (!find_tile<true>(p, set * 8 + rem % 8, kTileRows, t)) return;
+    if (!find_tile<true>(p, unit, kTileRows, t)) return;
     int v0, v1;
     if (!key_range(t, v0, v1)) return;
-    attend_tile<PagedFp8, DP, DP, 1, UNI, TREE>(p, t, kvh, v0, v1, lds);
+    attend_tile<PagedFp8, DP, DP, 1, UNI, TREE>(p, t, (int)kvh, v0, v1, lds);
 }
 
 template <int DP>

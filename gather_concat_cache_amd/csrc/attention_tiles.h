@@ -94,6 +94,7 @@ struct PackedBf16 {
     static constexpr bool kFp8 = false;
     static constexpr int kBytes = 2;
     static constexpr float kShiftUp = 0.0f;              // bf16 weights have binary32's range
+    static constexpr int kDepth = 3;                     // reads in flight (2, 3, 4: 1007, 1019, 1013 TFLOP/s with 128 dims)
     static __device__ __forceinline__ f32x16 mma(const frag& a, const frag& b, const f32x16& c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
     }
@@ -103,6 +104,7 @@ struct PagedFp8 {
     static constexpr bool kFp8 = true;
     static constexpr int kBytes = 1;
     static constexpr float kShiftUp = kShift;
+    static constexpr int kDepth = 2;                     // 2, 3, 4: 520, 535, 540 us for 4 x 2048 tokens over 4096 keys
     static __device__ __forceinline__ f32x16 mma(const frag& a, const frag& b, const f32x16& c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
     }
@@ -315,21 +317,20 @@ struct NoWalk {};
 
 // N fragments with DEPTH reads in flight.  Piece i of `side`, vector work that
 // needs none of them, follows the matrix instructions of fragment i and runs
-// beside them; the barriers keep reads, matrix instructions and pieces in this
-// order (left to the compiler the pieces often come first or last: 929 against
-// 994 TFLOP/s from one build to the next).
-template <int N, int DEPTH, typename F, typename Load, typename Use, typename Side>
+// beside them.  The barriers keep reads and matrix instructions in this order,
+// and with PIN the pieces too.
+template <int N, int DEPTH, bool PIN, typename F, typename Load, typename Use, typename Side>
 __device__ __forceinline__ void stream(Load load, Use use, Side side) {
     F b[DEPTH];
 #pragma unroll
     for (int i = 0; i < DEPTH; i++) b[i] = load(i);
-    __builtin_amdgcn_sched_barrier(0x274);
+    __builtin_amdgcn_sched_barrier(PIN ? 0x274 : 0x676);
 #pragma unroll
     for (int i = 0; i < N; i++) {
         use(i, b[i % DEPTH]);
         if (i + DEPTH < N) b[i % DEPTH] = load(i + DEPTH);
         side(i);
-        __builtin_amdgcn_sched_barrier(0x274);
+        __builtin_amdgcn_sched_barrier(PIN ? 0x274 : 0x676);
     }
 }
 // The i-th of N parts of COUNT pieces: run(piece) for each.
@@ -433,7 +434,7 @@ __device__ __forceinline__ void load_rows_q(const AttnParams& p, const uint16_t*
 
 // Scores of a step: S^T = K Q^T.  A 16-byte read is one step's operand in bf16,
 // two steps' in e4m3.
-template <typename T, int KS, int KB, int R, typename Side>
+template <typename T, int KS, int KB, int R, bool PIN, typename Side>
 __device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::frag (*q)[KS], f32x16 (*s)[2], Side side) {
     constexpr int PER = T::kFp8 ? 2 : 1, J = KS / PER;
 #pragma unroll
@@ -442,7 +443,7 @@ __device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::f
         for (int kt = 0; kt < 2; kt++)
 #pragma unroll
             for (int j = 0; j < 16; j++) s[r][kt][j] = 0.0f;
-    stream<2 * J, 4, u32x4>(
+    stream<2 * J, T::kDepth, PIN, u32x4>(
         [&](int n) { return read_lds<u32x4>(chunk_at<KB / 16>(k_at, 2 * (n % J)) + n / J * 32 * KB); },
         [&](int n, const u32x4& x) {
             const int kt = n / J, st = n % J * PER;
@@ -480,9 +481,12 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     typedef typename T::frag frag;
     constexpr int KS = DK / 16, DT = DV / 32, KC = L::KB / 16, VC = L::VB / 16;
     constexpr bool FP8 = T::kFp8;
-    // Sums of weights where the weights are made: left to the compiler they follow the step, and 32 weights stay in
-    // registers meanwhile.  With 192 dims those spill (724 against 1029 TFLOP/s); e4m3 540 against 557 us for 4 x 2048
-    // tokens over 4096 keys, 64 dims 804 against 782 TFLOP/s, but 128 dims of bf16 946 against 949 and 256 929 against 936.
+    // Pieces of vector work stay between the matrix instructions they are written beside.  Left to the compiler they may
+    // all come last: 192 dims 1071 against 1120 TFLOP/s, 256 681 against 910, 128 929 to 1018 from one build to the next
+    // against 1019; but with e4m3's conversions among them 569 us against 540, and 64 dims 841 against 825.
+    constexpr bool kPin = !FP8 && DK >= 128;
+    // Sums of weights where the weights are made: as late as possible, 32 weights stay in registers, and 192 dims spill
+    // (724 against 1029 TFLOP/s); e4m3 540 against 557 us.
     constexpr bool kSumEarly = FP8 || DK % 128 != 0;
     // A higher wave priority while matrix instructions are issued: 128 dims 963 against 949 TFLOP/s, e4m3 531 against 557
     // us, 192 as before; but 64 dims 761 against 780 and 256 919 against 936.
@@ -585,12 +589,33 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     // ---- logits of a step from its scores: scaled, shifted, the hidden ones -infinity; the running maximum, which the
     // accumulators follow with a lag
     constexpr int kPieces = 16 * R;                      // of a step's logits or weights: two of a row's 32 each
+    // the scales of a step's four groups, read before the products start
+    constexpr int G = FP8 && EX ? 4 : 1;
+    float mul[R][G], plus[R][G], inv[G], inv_next[G];
+    const auto read_scales = [&](int n) {
+        if constexpr (FP8 && EX) {
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const PageScale ps = lds.at[n & 3][g];
+                inv_next[g % G] = ps.inv_v;
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                    mul[r][g % G] = fac[r] * ps.k;
+                    plus[r][g % G] = sub[r] + ps.log2_v;
+                }
+            }
+        }
+    };
     const auto scale_piece = [&](int n, f32x16 (*x)[2], float* top, int piece) {
         const int r = piece / 16, kt = piece % 16 / 8, j = piece % 8 * 2;
-        if constexpr (FP8) {
+        if constexpr (FP8 && EX) {
+            const int g = 2 * kt + j / 8;
+            x[r][kt][j] = __builtin_fmaf(x[r][kt][j], mul[r][g % G], plus[r][g % G]);
+            x[r][kt][j + 1] = __builtin_fmaf(x[r][kt][j + 1], mul[r][g % G], plus[r][g % G]);
+        } else if constexpr (FP8) {
 #pragma unroll
             for (int i = j; i < j + 2; i++) {
-                const PageScale& ps = lds.at[n & 3][EX ? 2 * kt + i / 8 : 32 * kt + 8 * (i >> 2) + 4 * h + (i & 3)];
+                const PageScale& ps = lds.at[n & 3][32 * kt + 8 * (i >> 2) + 4 * h + (i & 3)];
                 x[r][kt][i] = __builtin_fmaf(x[r][kt][i], fac[r] * ps.k, sub[r] + ps.log2_v);
             }
         } else {
@@ -668,7 +693,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         } else part = e0 + e1;
         sums[r][g] = j == 0 ? part : sums[r][g] + part;
         if (j == 6) {
-            if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sums[r][g], lds.at[n & 3][g].inv_v, l[r]);
+            if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sums[r][g], inv[g % G], l[r]);
             else l[r] += sums[r][g];
             if constexpr (kSumEarly) asm volatile("" : "+v"(l[r]));
         }
@@ -692,10 +717,10 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
             for (int r = 0; r < R; r++) o[r][n % DT] = T::mma(a, pw[r][n / DT], o[r][n % DT]);
         };
         if constexpr (!CAREFUL) {
-            stream<4 * DT, 4, RawFrag<T>>(load_v, [&](int n, const RawFrag<T>& x) { add(n, operand(x)); }, side);
+            stream<4 * DT, T::kDepth, kPin, RawFrag<T>>(load_v, [&](int n, const RawFrag<T>& x) { add(n, operand(x)); }, side);
         } else {
             uint32_t odd = 0;
-            stream<4 * DT, 2, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
+            stream<4 * DT, 2, false, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
                 odd |= drop_nonfinite(x);
                 add(n, operand(x));
             }, side);
@@ -708,7 +733,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
 #pragma unroll
                         for (int j = 0; j < 32; j++)
                             pw[r][j >> 3][j & 7] = (__bf16)(s[r][j >> 4][j & 15] != kNegInf ? 0x1p100f : 0.0f);
-                    stream<4 * DT, 2, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
+                    stream<4 * DT, 2, false, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
                         keep_nonfinite(x);
                         add(n, operand(x));
                     }, [](int) {});
@@ -722,13 +747,16 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         tile_ready();
         if (vn < v1) issue_keys(vn, 1);
         if (busy) {
-            multiply_keys<T, KS, L::KB, R>(k_lane, q, s, [](int) {});
+            read_scales(0);
+            multiply_keys<T, KS, L::KB, R, kPin>(k_lane, q, s, [](int) {});
             float top[R];
 #pragma unroll
             for (int r = 0; r < R; r++) top[r] = kNegInf;
 #pragma unroll
             for (int k = 0; k < kPieces; k++) scale_piece(0, s, top, k);
             join_top(top);
+#pragma unroll
+            for (int g = 0; g < G; g++) inv[g] = inv_next[g];
             settle(v, 0, s, top);
         }
     }
@@ -750,11 +778,14 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
 #pragma unroll
             for (int r = 0; r < R; r++) top[r] = kNegInf;
             constexpr int NK = 2 * KS / (FP8 ? 2 : 1), NV = 4 * DT;
-            multiply_keys<T, KS, L::KB, R>(k_lane + ((n + 1) & 1) * (int)sizeof(lds.k[0]), q, x,
+            read_scales(n + 1);
+            multiply_keys<T, KS, L::KB, R, kPin>(k_lane + ((n + 1) & 1) * (int)sizeof(lds.k[0]), q, x,
                                            [&](int i) { part_of<NK, kPieces>(i, [&](int k) { weigh_piece(n, k); }); });
             add_values(n, [&](int i) { part_of<NV, kPieces>(i, [&](int k) { scale_piece(n + 1, x, top, k); }); });
             if constexpr (kRaise) __builtin_amdgcn_s_setprio(0);
             join_top(top);
+#pragma unroll
+            for (int g = 0; g < G; g++) inv[g] = inv_next[g];
             settle(vn, n + 1, x, top);
 #pragma unroll
             for (int r = 0; r < R; r++)
@@ -870,6 +901,22 @@ __device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kv
         __syncthreads();
         attend_once<T, DK, DV, R, EX, TREE, true>(p, t, kvh, v0, v1, lds);
     }
+}
+
+// The kv head and work unit of workgroup wg.  Workgroups of a head get numbers
+// that are equal modulo 8 (or its divisor): one XCD, whose L2 then serves a
+// request's keys to all of its row tiles.
+__device__ __forceinline__ bool head_and_unit(const AttnParams& p, uint32_t wg, uint32_t& kvh, uint32_t& unit) {
+    const uint32_t units = (uint32_t)p.units, hk = (uint32_t)p.hk;
+    if (hk % 8 == 0) {
+        const uint32_t part = wg / (8 * units), in = wg - part * 8 * units;
+        kvh = part * 8 + in % 8;
+        unit = in / 8;
+    } else {
+        unit = wg / hk;
+        kvh = wg - unit * hk;
+    }
+    return kvh < hk;
 }
 
 }  // namespace gcache

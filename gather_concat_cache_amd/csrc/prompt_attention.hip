@@ -7,20 +7,8 @@ namespace gcache {
 template <int DK, int DV, bool EX>
 __global__ __launch_bounds__(kTileWaves * kWave, DK <= 192 ? 2 : 1) void k_prompt(PromptParams p, int64_t wg0) {
     __shared__ StepLds<PackedBf16, DK, DV, EX> lds;
-    // Workgroups of a kv head get numbers that are equal modulo 8 (or its
-    // divisor): one XCD, whose L2 then serves a request's keys to all of its
-    // row tiles.
-    const uint32_t wg = (uint32_t)wg0 + blockIdx.x, units = (uint32_t)p.units, hk = (uint32_t)p.hk;
     uint32_t kvh, unit;
-    if (hk % 8 == 0) {
-        const uint32_t part = wg / (8 * units), in = wg - part * 8 * units;
-        kvh = part * 8 + in % 8;
-        unit = in / 8;
-    } else {
-        unit = wg / hk;
-        kvh = wg - unit * hk;
-    }
-    if (kvh >= hk) return;
+    if (!head_and_unit(p, (uint32_t)wg0 + blockIdx.x, kvh, unit)) return;
     RowTile t;
     if (!find_tile<true>(p, unit, kTileRows, t)) return;
     int v0, v1;
