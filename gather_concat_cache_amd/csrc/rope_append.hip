@@ -348,13 +348,18 @@ __global__ __launch_bounds__(kBlockThreads) void k_rope_append(AppendParams p, i
 hipError_t launch_rope_append(const AppendParams& in, hipStream_t s) {
     AppendParams p = in;
     const int units = p.hs / 16, per = kWave / units;    // (row, head) pairs of a wave
-    p.chunk_heads = p.hk < per ? p.hk : per;
-    p.wave_rows = per / p.chunk_heads;
-    p.head_chunks = (p.hk + p.chunk_heads - 1) / p.chunk_heads;
     // Units: the pages that the requests' tokens can lie in, a bound that the
     // host knows, or the tokens where those are fewer (decoding).
     const int64_t pages = page_unit(p.num_tokens, p.batch, p.div.size);
     p.by_token = p.num_tokens <= pages;
+    // Heads of a workgroup: as many as a wave holds, or for large pages so many
+    // that a page's rows take kKeep rounds (pages of 128 tokens, 8 heads of 128:
+    // 123 us with all heads, whose rows 128 workgroups then read twice).
+    const int64_t rows = p.by_token ? 1 : (p.div.size + kKeep * kWavesPerBlock - 1) / (kKeep * kWavesPerBlock);
+    p.chunk_heads = (int32_t)(per / rows > 1 ? per / rows : 1);
+    if (p.chunk_heads > p.hk) p.chunk_heads = p.hk;
+    p.wave_rows = per / p.chunk_heads;
+    p.head_chunks = (p.hk + p.chunk_heads - 1) / p.chunk_heads;
     p.page_groups = (p.by_token ? p.num_tokens : pages) * p.head_chunks;
     // a wave a token, and more of them for few tokens
     const int most = (p.hq + per - 1) / per;
