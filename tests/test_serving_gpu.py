@@ -55,6 +55,8 @@ APPEND = [  # q heads, kv heads, head size, rot, interleaved, bf16 table, block,
     (16, 16, 128, 64, False, False, 48, "nhd", [60, 1, 47, 2], [70, 48, 47, 50]),
     (1, 1, 48, 16, False, False, 16, "nhd", [1] * 70, list(range(1, 71))),
     (64, 2, 128, 128, False, False, 16, "nhd", [1], [1000]),
+    (2, 8, 128, 128, False, False, 128, "nhd", [150, 1, 129, 0, 3], [160, 129, 129, 4, 131]),
+    (1, 2, 64, 0, False, False, 1024, "nhd", [1100, 1, 30], [1300, 1025, 31]),
 ]
 
 
@@ -395,6 +397,144 @@ def test_cache_on_a_stream_negative_and_zero_scale(g):
     check_cache(g, rng, batch, 1, 2, 64, scale=0.0, window=9, sinks=1)
 
 
+@pytest.mark.parametrize("window,sinks", [(None, 0), (900, 40)])
+@pytest.mark.parametrize("bs", [16, 40])
+def test_cache_long_chunks(g, bs, window, sinks):
+    """Chunks of several row tiles over lengths that differ."""
+    rng = np.random.default_rng(23)
+    batch = Batch(rng, [300, 0, 700, 129], [1100, 5, 1900, 129], bs)
+    check_cache(g, rng, batch, 1, 2, 64, window=window, sinks=sinks)
+
+
+def small_cache(rng, nb, bs, hk, hs):
+    codes = dev(random_codes(rng, (nb, 2, bs, hk, hs)))
+    return codes, dev((2.0 ** rng.uniform(-10, -8, (nb, 2, hk))).astype(np.float32))
+
+
+@pytest.mark.parametrize("bs", [16, 24])
+def test_cache_captured(g, bs):
+    """Append and attention (keys split, so the join is in it) in one graph:
+    every replay gives the eager bits for the inputs of its time."""
+    rng = np.random.default_rng(24)
+    hk, hq, hs, nb = 2, 8, 128, 300
+    cache, scales = small_cache(rng, nb, bs, hk, hs)
+    view = cache.view(torch.float8_e4m3fn)
+    was, was_scales = cache.clone(), scales.clone()
+    table = dev(rng.permutation(nb).astype(np.int32)[:2 * 140].reshape(2, 140))
+    starts, lens = dev(np.array([0, 1, 4], np.int32)), dev(np.array([1800, 2203], np.int32))
+    q, k, v = (ref.bf16(rng.standard_normal((4, h, hs)))[0].cuda() for h in (hq, hk, hk))
+
+    def call():
+        qr, _ = g.rope_append_fp8_kv(q, k, v, view, scales, table, starts, lens, None)
+        return g.attention_fp8_kv(qr, view, scales, table, starts, lens, 2203, 0.09, return_lse=True)
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = call()
+    for i in range(3):
+        for x in (q, k, v):
+            x.mul_(0.5 + i)
+        lens.sub_(dev(np.array([i, 40 * i], np.int32)))
+        cache.copy_(was)
+        scales.copy_(was_scales)
+        want, want_lse = call()
+        state = cache.clone(), scales.clone()
+        cache.copy_(was)
+        scales.copy_(was_scales)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert torch.equal(cache, state[0]) and torch.equal(scales, state[1])
+
+
+@pytest.mark.parametrize("bs", [16, 24])
+def test_cache_behind_4_gib(g, bs):
+    """Pages whose bytes lie behind 2^32 give the bits of pages at the start,
+    in append and in both kinds of attention."""
+    rng = np.random.default_rng(25)
+    hk, hq, hs, nb = 8, 16, 128, 12
+    cache, scales = small_cache(rng, nb, bs, hk, hs)
+    far = (5 << 30) // (2 * bs * hk * hs)
+    big = torch.empty((far + nb, 2, bs, hk, hs), dtype=torch.uint8, device="cuda")
+    big_scales = torch.empty((far + nb, 2, hk), device="cuda")
+    big[far:], big_scales[far:] = cache, scales
+    near = dev(rng.permutation(nb).astype(np.int32).reshape(2, 6))
+    lens = dev(np.array([90, 95], np.int32))
+    for starts in ([0, 1, 3], [0, 70, 101]):
+        T = starts[-1]
+        starts = dev(np.array(starts, np.int32))
+        q, k, v = (ref.bf16(rng.standard_normal((T, h, hs)))[0].cuda() for h in (hq, hk, hk))
+        got = []
+        for c, s, t in ((cache, scales, near), (big, big_scales, near + far)):
+            g.rope_append_fp8_kv(None, k, v, c, s, t, starts, lens, None)
+            got.append(g.attention_fp8_kv(q, c, s, t, starts, lens, 95, 0.09, return_lse=True))
+        assert torch.equal(big[far:], cache) and torch.equal(big_scales[far:], scales)
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_calls_on_two_streams_at_once(g):
+    """Two calls of each attention in flight together, each with its own
+    workspace (allocated by the call), give the bits of one alone."""
+    rng = np.random.default_rng(26)
+    hk, hq, hs, bs, nb = 2, 8, 128, 16, 512
+    cache, scales = small_cache(rng, nb, bs, hk, hs)
+    one, lens = dev(np.array([0, 2], np.int32)), dev(np.array([4000], np.int32))
+    tables = [dev(rng.permutation(nb).astype(np.int32)[None, :256].copy()) for _ in range(2)]
+    qs = [ref.bf16(rng.standard_normal((2, hq, hs)))[0].cuda() for _ in range(2)]
+    k, v = (ref.bf16(rng.standard_normal((4000, hk, hs)))[0].cuda() for _ in range(2))
+
+    def calls(i, stream=None):
+        return [g.attention_fp8_kv(qs[i], cache, scales, tables[i], one, lens, 4000, 0.09, stream=stream),
+                g.prompt_attention(qs[i], k, v, one, dev_keys, 4000, 0.09, stream=stream)]
+
+    dev_keys = dev(np.array([0, 4000], np.int32))
+    want = [calls(i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[calls(i, streams[i]) for i in range(2)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for both in got:
+        for a, b in zip(both, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_argument_refusals(g):
+    """What the binding refuses, with the tensors on the GPU."""
+    x = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    cache, scales = x(3, 2, 16, 2, 64, t=torch.uint8), x(3, 2, 2, t=torch.float32)
+    table, starts, lens = x(1, 4, t=torch.int32), x(2, t=torch.int32), x(1, t=torch.int32)
+    q, k = x(5, 4, 64), x(5, 2, 64)
+    paged = (cache, scales, table, starts, lens)
+    bad = [
+        lambda: g.attention_fp8_kv(q, *paged, 4, 1.0, window=3, tree_mask=x(5, 2, t=torch.bool)),
+        lambda: g.attention_fp8_kv(q, *paged, 4, 1.0, window=0),
+        lambda: g.attention_fp8_kv(x(5, 3, 64), *paged, 4, 1.0),
+        lambda: g.attention_fp8_kv(q, cache, scales[:2], table, starts, lens, 4, 1.0),
+        lambda: g.attention_fp8_kv(q, cache, scales, table, lens, lens, 4, 1.0),
+        lambda: g.attention_fp8_kv(q, *paged, 4, float("nan")),
+        lambda: g.attention_fp8_kv(q, *paged, 4, 1.0, out=x(5, 4, 32)),
+        lambda: g.rope_append_fp8_kv(None, k, k, *paged, None, q_out=q),
+        lambda: g.rope_append_fp8_kv(q, k, k[:4], *paged, None),
+        lambda: g.rope_append_fp8_kv(q, k[..., ::2], k[..., ::2], *paged, None),
+        lambda: g.rope_append_fp8_kv(q, k, k, *paged, x(9, 80, t=torch.float32)),
+        lambda: g.rope_append_fp8_kv(q, k, k, *paged, x(9, 24, t=torch.float32)),
+        lambda: g.rope_append_fp8_kv(q, k, k, *paged, None, positions=x(4, t=torch.int64)),
+        lambda: g.rope_append_fp8_kv(q, k, k, cache[:1].expand(3, -1, -1, -1, -1), *paged[1:], None),
+        lambda: g.prompt_attention(q, k, k, starts, starts, 5, 1.0, accumulate=True),
+        lambda: g.prompt_attention(q, k, k, starts, starts, 5, 1.0, causal=False, window=4),
+        lambda: g.prompt_attention(q, k, k, starts, lens, 5, 1.0),
+        lambda: g.prompt_attention(q, k, k[:4], starts, starts, 5, 1.0),
+        lambda: g.prompt_attention(q, k, k, starts, starts, -1, 1.0),
+        lambda: g.prompt_attention(q, x(5, 3, 64), x(5, 3, 64), starts, starts, 5, 1.0),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, RuntimeError)):
+            call()
+            pytest.fail(f"call {i} was taken")
+
+
 # ---------------------------------------------------------------------------
 # prompts
 # ---------------------------------------------------------------------------
@@ -490,6 +630,28 @@ def test_prompts_over_context(g, hk, group, dk, dv):
 @pytest.mark.parametrize("lens", [[1] * 20, [127, 128, 129], [31, 32, 33, 63, 65], [300], [2] * 70, [0, 0, 5, 0]])
 def test_prompt_lengths(g, lens):
     check_prompt(g, np.random.default_rng(3), lens, lens, 2, 4, 128, 128, fused=True)
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (192, 128), (80, 96)])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (900, 40)])
+def test_prompt_long_batches(g, dk, dv, window, sinks):
+    """Many row tiles, which start with the longest, of lengths that differ."""
+    check_prompt(g, np.random.default_rng(4), [1100, 1, 1900, 700], [1100, 900, 1900, 1030], 1, 2, dk, dv, window=window, sinks=sinks)
+
+
+def test_prompt_rows_behind_4_gib(g):
+    """Rows 2^24 bytes apart give the bits of rows that lie together."""
+    rng = np.random.default_rng(10)
+    n, d = 300, 128
+    q, k, v = (ref.bf16(rng.standard_normal((n, 1, d)))[0].cuda() for _ in range(3))
+    wide = torch.zeros((n, 1 << 23), dtype=torch.bfloat16, device="cuda")
+    far = [wide[:, None, i * d:(i + 1) * d] for i in range(4)]
+    for x, y in zip(far, (q, k, v)):
+        x.copy_(y)
+    starts = dev(np.array([0, 30, n], np.int32))
+    want, lse = g.prompt_attention(q, k, v, starts, starts, n, 0.1, return_lse=True)
+    got, got_lse = g.prompt_attention(*far[:3], starts, starts, n, 0.1, out=far[3], return_lse=True)
+    assert torch.equal(got, want) and torch.equal(got_lse, lse)
 
 
 @pytest.mark.parametrize("dk,dv", [(128, 128), (192, 128), (256, 256)])
