@@ -281,7 +281,8 @@ __device__ __forceinline__ bool find_tile(const P& p, int64_t unit, int RT, RowT
         if (SORTED && per == 1 && !split && p.key_tiles >= kSortTiles) {
             // level of a request's tile j: from + j; count(x) tiles have level x or more
             const int qlen = max(q_last - q_first, 0);
-            const int from = (int)((int64_t)max(first_position(p, keys1, qlen), 0) * p.group / RT);
+            const int64_t far = (int64_t)max(first_position(p, keys1, qlen), 0) * p.group / RT;
+            const int from = (int)min(far, (int64_t)1 << 30);            // (an order only; from + n stays in 32 bits)
             const auto count = [&](int x) {
                 return __builtin_amdgcn_readlane(scan_lanes(n > 0 ? min(max(from + n - x, 0), n) : 0), kWave - 1);
             };

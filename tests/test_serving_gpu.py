@@ -474,6 +474,20 @@ def test_cache_behind_4_gib(g, bs):
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+def test_cache_lengths_behind_the_table(g):
+    """seq_lens that claim up to 2^31 - 1 keys, of which the table has 64: the
+    bits of a sequence that ends there, with many heads a key head."""
+    rng = np.random.default_rng(27)
+    cache, scales = small_cache(rng, 8, 16, 1, 64)
+    table = dev(rng.permutation(8).astype(np.int32).reshape(2, 4))
+    starts = dev(np.array([0, 1, 3], np.int32))
+    q = ref.bf16(rng.standard_normal((3, 256, 64)))[0].cuda()
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    got = [g.attention_fp8_kv(q, cache, scales, table, starts, dev(np.array([n, 40], np.int32)), 4096, 0.1, return_lse=True, workspace=none)
+           for n in (64, 2 ** 31 - 1)]
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_calls_on_two_streams_at_once(g):
     """Two calls of each attention in flight together, each with its own
     workspace (allocated by the call), give the bits of one alone."""
