@@ -1,6 +1,7 @@
 """gather_concat_cache_amd -- quantized paged KV-cache write and gather-upconvert
 for AMD Instinct MI355X (gfx950), with the attention that reads the pages in
-place, the norm and rotation before the write, and the ownership of pages.
+place, the norm and rotation before the write, and the ownership of pages; an
+8-bit paged cache with its append and attention; and the attention of prompts.
 
 The computation lives in libgcache.so (hand-written HIP kernels behind the C
 ABI of the headers in include/); this package only marshals torch tensors (device

@@ -434,36 +434,30 @@ __device__ __forceinline__ void load_rows_q(const AttnParams& p, const uint16_t*
 
 // Scores of a step: S^T = K Q^T.  A 16-byte read is one step's operand in bf16,
 // two steps' in e4m3.
-template <typename T, int KS, int KB, int R, bool PIN, typename Side>
-__device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::frag (*q)[KS], f32x16 (*s)[2], Side side) {
+template <typename T, int KS, int KB, bool PIN, typename Side>
+__device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::frag* q, f32x16* s, Side side) {
     constexpr int PER = T::kFp8 ? 2 : 1, J = KS / PER;
 #pragma unroll
-    for (int r = 0; r < R; r++)
+    for (int kt = 0; kt < 2; kt++)
 #pragma unroll
-        for (int kt = 0; kt < 2; kt++)
-#pragma unroll
-            for (int j = 0; j < 16; j++) s[r][kt][j] = 0.0f;
+        for (int j = 0; j < 16; j++) s[kt][j] = 0.0f;
     stream<2 * J, T::kDepth, PIN, u32x4>(
         [&](int n) { return read_lds<u32x4>(chunk_at<KB / 16>(k_at, 2 * (n % J)) + n / J * 32 * KB); },
         [&](int n, const u32x4& x) {
             const int kt = n / J, st = n % J * PER;
             if constexpr (T::kFp8) {
                 const f16x8 a = fp8_operand(x.x, x.y), b = fp8_operand(x.z, x.w);
-#pragma unroll
-                for (int r = 0; r < R; r++) {
-                    s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
-                    s[r][kt] = T::mma(b, q[r][st + 1], s[r][kt]);
-                }
+                s[kt] = T::mma(a, q[st], s[kt]);
+                s[kt] = T::mma(b, q[st + 1], s[kt]);
             } else {
                 const bf16x8 a = __builtin_bit_cast(bf16x8, x);
-#pragma unroll
-                for (int r = 0; r < R; r++) s[r][kt] = T::mma(a, q[r][st], s[r][kt]);
+                s[kt] = T::mma(a, q[st], s[kt]);
             }
         },
         side);
 }
 
-// One tile of up to 128 R rows over the 32-key tiles [v0, v1).
+// One tile of up to 128 rows over the 32-key tiles [v0, v1).
 // EX: packed prompts with head sizes of exactly DK and DV; a cache whose head
 // size is DK and whose pages are whole 16-key groups within 32 bits.
 // CAREFUL: values of hidden keys may be infinities or NaN, which a weight of 0
@@ -475,7 +469,7 @@ __device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::f
 // The scores of step i + 1 are multiplied while step i's weights are computed,
 // and its values while the next logits are scaled: a wave's matrix instructions
 // and its vector ones are independent, and run side by side.
-template <typename T, int DK, int DV, int R, bool EX, bool TREE, bool CAREFUL, typename P>
+template <typename T, int DK, int DV, bool EX, bool TREE, bool CAREFUL, typename P>
 __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
     typedef StepLds<T, DK, DV, EX> L;
     typedef typename T::frag frag;
@@ -546,22 +540,21 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     }
 
     // ---- query rows
-    frag q[R][KS];
-    float fac[R];
-    int pos[R], tok[R], row_of[R];
-#pragma unroll
-    for (int r = 0; r < R; r++) {
-        const int off = 32 * (R * w + r) + c;
+    frag q[KS];
+    float fac;
+    int pos, tok, row_of;
+    {
+        const int off = 32 * w + c;
         const bool in = off < t.rows;
         const int row = in ? t.row0 + off : t.row0, tl = row_token(p, row), head = kvh * p.group + row - tl * p.group;
-        row_of[r] = in ? row : -1;
-        tok[r] = t.q0 + tl;
-        pos[r] = in ? t.ctx + tl : -1;
-        load_rows_q<DK>(p, p.q + (int64_t)tok[r] * p.q_ts + (int64_t)head * p.q_hs, in, h, q[r], fac[r]);
+        row_of = in ? row : -1;
+        tok = t.q0 + tl;
+        pos = in ? t.ctx + tl : -1;
+        load_rows_q<DK>(p, p.q + (int64_t)tok * p.q_ts + (int64_t)head * p.q_hs, in, h, q, fac);
     }
-    const bool busy = 32 * R * w < t.rows;               // the other waves of a partly filled tile only load
-    const int pos_lo = t.ctx + row_token(p, min(t.row0 + 32 * R * w, t.row0 + t.rows - 1));
-    const int pos_hi = t.ctx + row_token(p, min(t.row0 + 32 * R * (w + 1) - 1, t.row0 + t.rows - 1));
+    const bool busy = 32 * w < t.rows;                   // the other waves of a partly filled tile only load
+    const int pos_lo = t.ctx + row_token(p, min(t.row0 + 32 * w, t.row0 + t.rows - 1));
+    const int pos_hi = t.ctx + row_token(p, min(t.row0 + 32 * (w + 1) - 1, t.row0 + t.rows - 1));
 
     // ---- where a lane reads: K rows c and 32 + c; V rows of its 16-lane group
     const uint32_t k_lane = lds_k + c * L::KB + ((h ^ key_swizzle<KC>(c)) << 4);
@@ -570,69 +563,55 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     const int v_chunk = FP8 ? dim_half : 2 * dim_half + (i >> 1 & 1);
     const uint32_t v_lane = lds_v + v_row * L::VB + ((v_chunk ^ value_swizzle<VC, FP8>(v_row)) << 4) + 8 * (i & 1);
 
-    f32x16 o[R][DT];
+    f32x16 o[DT];
     // weights are exp2(x), x the logits + sub, sub = shift - m (0 before the first visible key); a step whose largest
     // exponent passes lim moves m
-    float m[R], l[R], sub[R], lim[R];
+    float m = kNegInf, l = 0.0f, sub = 0.0f, lim = kNegInf;
 #pragma unroll
-    for (int r = 0; r < R; r++) {
-        m[r] = lim[r] = kNegInf;
-        l[r] = sub[r] = 0.0f;
+    for (int d = 0; d < DT; d++)
 #pragma unroll
-        for (int d = 0; d < DT; d++)
-#pragma unroll
-            for (int j = 0; j < 16; j++) o[r][d][j] = 0.0f;
-    }
-    f32x16 s[R][2];                                      // of the step whose weights come next
+        for (int j = 0; j < 16; j++) o[d][j] = 0.0f;
+    f32x16 s[2];                                         // of the step whose weights come next
     bool seen_all = true;                                // no key of it is hidden
 
     // ---- logits of a step from its scores: scaled, shifted, the hidden ones -infinity; the running maximum, which the
     // accumulators follow with a lag
-    constexpr int kPieces = 16 * R;                      // of a step's logits or weights: two of a row's 32 each
+    constexpr int kPieces = 16;                          // of a step's logits or weights: two of a lane's 32 each
     // the scales of a step's four groups, read before the products start
     constexpr int G = FP8 && EX ? 4 : 1;
-    float mul[R][G], plus[R][G], inv[G], inv_next[G];
+    float mul[G], plus[G], inv[G], inv_next[G];
     const auto read_scales = [&](int n) {
         if constexpr (FP8 && EX) {
 #pragma unroll
             for (int g = 0; g < 4; g++) {
                 const PageScale ps = lds.at[n & 3][g];
                 inv_next[g % G] = ps.inv_v;
-#pragma unroll
-                for (int r = 0; r < R; r++) {
-                    mul[r][g % G] = fac[r] * ps.k;
-                    plus[r][g % G] = sub[r] + ps.log2_v;
-                }
+                mul[g % G] = fac * ps.k;
+                plus[g % G] = sub + ps.log2_v;
             }
         }
     };
-    const auto scale_piece = [&](int n, f32x16 (*x)[2], float* top, int piece) {
-        const int r = piece / 16, kt = piece % 16 / 8, j = piece % 8 * 2;
+    const auto scale_piece = [&](int n, f32x16* x, float& top, int piece) {
+        const int kt = piece / 8, j = piece % 8 * 2;
         if constexpr (FP8 && EX) {
             const int g = 2 * kt + j / 8;
-            x[r][kt][j] = __builtin_fmaf(x[r][kt][j], mul[r][g % G], plus[r][g % G]);
-            x[r][kt][j + 1] = __builtin_fmaf(x[r][kt][j + 1], mul[r][g % G], plus[r][g % G]);
+            x[kt][j] = __builtin_fmaf(x[kt][j], mul[g % G], plus[g % G]);
+            x[kt][j + 1] = __builtin_fmaf(x[kt][j + 1], mul[g % G], plus[g % G]);
         } else if constexpr (FP8) {
 #pragma unroll
             for (int i = j; i < j + 2; i++) {
                 const PageScale& ps = lds.at[n & 3][32 * kt + 8 * (i >> 2) + 4 * h + (i & 3)];
-                x[r][kt][i] = __builtin_fmaf(x[r][kt][i], fac[r] * ps.k, sub[r] + ps.log2_v);
+                x[kt][i] = __builtin_fmaf(x[kt][i], fac * ps.k, sub + ps.log2_v);
             }
         } else {
-            x[r][kt][j] = __builtin_fmaf(x[r][kt][j], fac[r], sub[r]);
-            x[r][kt][j + 1] = __builtin_fmaf(x[r][kt][j + 1], fac[r], sub[r]);
+            x[kt][j] = __builtin_fmaf(x[kt][j], fac, sub);
+            x[kt][j + 1] = __builtin_fmaf(x[kt][j + 1], fac, sub);
         }
-        top[r] = max3(top[r], x[r][kt][j], x[r][kt][j + 1]);
+        top = max3(top, x[kt][j], x[kt][j + 1]);
     };
-    const auto join_top = [&](float* top) {
-#pragma unroll
-        for (int r = 0; r < R; r++) top[r] = pair_max(top[r]);
-    };
-    const auto find_top = [&](f32x16 (*x)[2], float* top) {
-#pragma unroll
-        for (int r = 0; r < R; r++) top[r] = pair_max(fmaxf(max16(x[r][0]), max16(x[r][1])));
-    };
-    const auto settle = [&](int v, int n, f32x16 (*x)[2], float* top) {
+    // (top: over the lane's logits of x)
+    const auto settle = [&](int v, int n, f32x16* x, float top) {
+        top = pair_max(top);
         uint32_t live = after(v) - v == 1 ? 0xFFFFu : ~0u;   // 16 keys of the lane a 32-key tile
         if constexpr (FP8) {
             constexpr int PER = EX ? 8 : 1;
@@ -642,60 +621,53 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         }
         seen_all = __all(live == ~0u && all_seen<TREE>(p, t, pos_lo, pos_hi, step_key(v), kStep));
         if (!seen_all) {
-#pragma unroll
-            for (int r = 0; r < R; r++) hide_step<TREE>(p, t, pos[r], tok[r], step_key(v) + 4 * h, live, x[r]);
-            find_top(x, top);
+            hide_step<TREE>(p, t, pos, tok, step_key(v) + 4 * h, live, x);
+            top = pair_max(fmaxf(max16(x[0]), max16(x[1])));
         }
-        bool late = false;
+        if (__builtin_expect(__any(top > lim), 0)) {      // wave-uniform, rare after the first steps
+            const float mn = fmaxf(m, top - sub);
+            const bool any = mn != kNegInf;
+            const float al = any ? __builtin_amdgcn_exp2f(m - mn) : 1.0f;
+            const float to = any ? T::kShiftUp - mn : 0.0f, by = to - sub;
+            m = mn;
+            sub = to;
+            lim = any ? T::kShiftUp + kLag : kNegInf;
+            l *= al;
 #pragma unroll
-        for (int r = 0; r < R; r++) late = late || top[r] > lim[r];
-        if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first steps
+            for (int kt = 0; kt < 2; kt++)
 #pragma unroll
-            for (int r = 0; r < R; r++) {
-                const float mn = fmaxf(m[r], top[r] - sub[r]);
-                const bool any = mn != kNegInf;
-                const float al = any ? __builtin_amdgcn_exp2f(m[r] - mn) : 1.0f;
-                const float to = any ? T::kShiftUp - mn : 0.0f, by = to - sub[r];
-                m[r] = mn;
-                sub[r] = to;
-                lim[r] = any ? T::kShiftUp + kLag : kNegInf;
-                l[r] *= al;
+                for (int j = 0; j < 16; j++) x[kt][j] += by;
+            if (n > 0) {
 #pragma unroll
-                for (int kt = 0; kt < 2; kt++)
+                for (int d = 0; d < DT; d++)
 #pragma unroll
-                    for (int j = 0; j < 16; j++) x[r][kt][j] += by;
-                if (n > 0) {
-#pragma unroll
-                    for (int d = 0; d < DT; d++)
-#pragma unroll
-                        for (int j = 0; j < 16; j++) o[r][d][j] *= al;
-                }
+                    for (int j = 0; j < 16; j++) o[d][j] *= al;
             }
         }
     };
-    frag pw[R][4];
-    float sums[R][4];                                    // of a 16-key group's weights
+    frag pw[4];
+    float sums[4];                                       // of a 16-key group's weights
     const auto weigh_piece = [&](int n, int piece) {
-        const int r = piece / 16, g = piece % 16 / 4, j = piece % 4 * 2;
-        const float e0 = __builtin_amdgcn_exp2f(s[r][g >> 1][8 * (g & 1) + j]);
-        const float e1 = __builtin_amdgcn_exp2f(s[r][g >> 1][8 * (g & 1) + j + 1]);
+        const int g = piece / 4, j = piece % 4 * 2;
+        const float e0 = __builtin_amdgcn_exp2f(s[g >> 1][8 * (g & 1) + j]);
+        const float e1 = __builtin_amdgcn_exp2f(s[g >> 1][8 * (g & 1) + j + 1]);
         if constexpr (FP8) {
-            pw[r][g][j] = (_Float16)e0;
-            pw[r][g][j + 1] = (_Float16)e1;
+            pw[g][j] = (_Float16)e0;
+            pw[g][j + 1] = (_Float16)e1;
         } else {
-            pw[r][g][j] = (__bf16)e0;
-            pw[r][g][j + 1] = (__bf16)e1;
+            pw[g][j] = (__bf16)e0;
+            pw[g][j + 1] = (__bf16)e1;
         }
         float part;
         if constexpr (FP8 && !EX) {
             const PageScale* ps = lds.at[n & 3] + 16 * g + 8 * (j >> 2) + 4 * h + (j & 3);
             part = __builtin_fmaf(e0, ps[0].inv_v, e1 * ps[1].inv_v);
         } else part = e0 + e1;
-        sums[r][g] = j == 0 ? part : sums[r][g] + part;
+        sums[g] = j == 0 ? part : sums[g] + part;
         if (j == 6) {
-            if constexpr (FP8 && EX) l[r] = __builtin_fmaf(sums[r][g], inv[g % G], l[r]);
-            else l[r] += sums[r][g];
-            if constexpr (kSumEarly) asm volatile("" : "+v"(l[r]));
+            if constexpr (FP8 && EX) l = __builtin_fmaf(sums[g], inv[g % G], l);
+            else l += sums[g];
+            if constexpr (kSumEarly) asm volatile("" : "+v"(l));
         }
     };
     const auto add_values = [&](int n, auto side) {
@@ -712,10 +684,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
             }
             return x;
         };
-        const auto add = [&](int n, const frag& a) {
-#pragma unroll
-            for (int r = 0; r < R; r++) o[r][n % DT] = T::mma(a, pw[r][n / DT], o[r][n % DT]);
-        };
+        const auto add = [&](int n, const frag& a) { o[n % DT] = T::mma(a, pw[n / DT], o[n % DT]); };
         if constexpr (!CAREFUL) {
             stream<4 * DT, T::kDepth, kPin, RawFrag<T>>(load_v, [&](int n, const RawFrag<T>& x) { add(n, operand(x)); }, side);
         } else {
@@ -729,10 +698,8 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
             if constexpr (!FP8) {
                 if (__any(odd != 0)) {
 #pragma unroll
-                    for (int r = 0; r < R; r++)
-#pragma unroll
-                        for (int j = 0; j < 32; j++)
-                            pw[r][j >> 3][j & 7] = (__bf16)(s[r][j >> 4][j & 15] != kNegInf ? 0x1p100f : 0.0f);
+                    for (int j = 0; j < 32; j++)
+                        pw[j >> 3][j & 7] = (__bf16)(s[j >> 4][j & 15] != kNegInf ? 0x1p100f : 0.0f);
                     stream<4 * DT, 2, false, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
                         keep_nonfinite(x);
                         add(n, operand(x));
@@ -748,13 +715,10 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         if (vn < v1) issue_keys(vn, 1);
         if (busy) {
             read_scales(0);
-            multiply_keys<T, KS, L::KB, R, kPin>(k_lane, q, s, [](int) {});
-            float top[R];
-#pragma unroll
-            for (int r = 0; r < R; r++) top[r] = kNegInf;
+            multiply_keys<T, KS, L::KB, kPin>(k_lane, q, s, [](int) {});
+            float top = kNegInf;
 #pragma unroll
             for (int k = 0; k < kPieces; k++) scale_piece(0, s, top, k);
-            join_top(top);
 #pragma unroll
             for (int g = 0; g < G; g++) inv[g] = inv_next[g];
             settle(v, 0, s, top);
@@ -772,25 +736,20 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         if (vp < v1) issue_keys(vp, n + 2);
         issue_values(vn, n + 1);
         if (busy) {                                      // wave-uniform
-            f32x16 x[R][2];
-            float top[R];
+            f32x16 x[2];
+            float top = kNegInf;
             if constexpr (kRaise) __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-            for (int r = 0; r < R; r++) top[r] = kNegInf;
             constexpr int NK = 2 * KS / (FP8 ? 2 : 1), NV = 4 * DT;
             read_scales(n + 1);
-            multiply_keys<T, KS, L::KB, R, kPin>(k_lane + ((n + 1) & 1) * (int)sizeof(lds.k[0]), q, x,
-                                           [&](int i) { part_of<NK, kPieces>(i, [&](int k) { weigh_piece(n, k); }); });
+            multiply_keys<T, KS, L::KB, kPin>(k_lane + ((n + 1) & 1) * (int)sizeof(lds.k[0]), q, x,
+                                        [&](int i) { part_of<NK, kPieces>(i, [&](int k) { weigh_piece(n, k); }); });
             add_values(n, [&](int i) { part_of<NV, kPieces>(i, [&](int k) { scale_piece(n + 1, x, top, k); }); });
             if constexpr (kRaise) __builtin_amdgcn_s_setprio(0);
-            join_top(top);
 #pragma unroll
             for (int g = 0; g < G; g++) inv[g] = inv_next[g];
             settle(vn, n + 1, x, top);
 #pragma unroll
-            for (int r = 0; r < R; r++)
-#pragma unroll
-                for (int kt = 0; kt < 2; kt++) s[r][kt] = x[r][kt];
+            for (int kt = 0; kt < 2; kt++) s[kt] = x[kt];
         }
         v = vn;
         vn = vp;
@@ -809,11 +768,9 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     if constexpr (!CAREFUL) {
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // a NaN anywhere makes one here
 #pragma unroll
-        for (int r = 0; r < R; r++)
+        for (int d = 0; d < DT; d++)
 #pragma unroll
-            for (int d = 0; d < DT; d++)
-#pragma unroll
-                for (int j = 0; j < 16; j++) sum[j & 3] += o[r][d][j];
+            for (int j = 0; j < 16; j++) sum[j & 3] += o[d][j];
         const float any = (sum[0] + sum[1]) + (sum[2] + sum[3]);
         // a place that the last step does not use, nor the output rows below
         uint32_t* flag;
@@ -833,73 +790,69 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     static_assert(kTileWaves * 32 * 16 * OC <= sizeof(lds.k) + (FP8 ? sizeof(lds.v) : 0), "rows of all waves fit");
     const uint32_t mine = lds_k + w * 32 * 16 * OC;
     if (CAREFUL) tile_ready();
-#pragma unroll
-    for (int r = 0; r < R; r++) {
-        const float ll = pair_sum(l[r]);
-        const bool in = row_of[r] >= 0;
-        const int row = max(row_of[r], 0), tl = row_token(p, row), head = kvh * p.group + row - tl * p.group;
-        const int64_t token = t.q0 + tl, id = token * p.hq + head;
-        if (partial) {
-            if (!in) continue;
-            if (h == 0) {
-                float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
-                ml[0] = m[r] - T::kShiftUp + kShift;     // the join takes kShift off
-                ml[1] = ll;
-            }
-            float* dst = p.ws_o + ((int64_t)t.split * p.total_q * p.hq + id) * p.hs + 4 * h;
-#pragma unroll
-            for (int d = 0; d < DT; d++)
-#pragma unroll
-                for (int a = 0; a < 4; a++)
-                    if (EX || 32 * d + 8 * a + 4 * h < p.hs)
-                        *reinterpret_cast<f32x4*>(dst + 32 * d + 8 * a) =
-                            f32x4{o[r][d][4 * a], o[r][d][4 * a + 1], o[r][d][4 * a + 2], o[r][d][4 * a + 3]};
-            continue;
+    const float ll = pair_sum(l);
+    const bool in = row_of >= 0;
+    const int row = max(row_of, 0), tl = row_token(p, row), head = kvh * p.group + row - tl * p.group;
+    const int64_t token = t.q0 + tl, id = token * p.hq + head;
+    if (partial) {
+        if (!in) return false;
+        if (h == 0) {
+            float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
+            ml[0] = m - T::kShiftUp + kShift;         // the join takes kShift off
+            ml[1] = ll;
         }
-        RowEnd end{0.0f, 0.0f, 0.0f};
-        if (in) {
-            end = row_end_shifted<T>(p, token, head, m[r], ll);
-            if (h == 0 && p.lse) p.lse[token * p.lse_ts + head] = end.lse;
-        }
-        uint16_t* dst = p.out + token * p.o_ts + (int64_t)head * p.o_hs;
-        if (accumulates(p)) {
-            if (!in) continue;
-#pragma unroll
-            for (int d = 0; d < DT; d++)
-#pragma unroll
-                for (int a = 0; a < 4; a++)
-                    if (EX || 32 * d + 8 * a + 4 * h < p.hs)
-                        write_dims(p, end, dst + 32 * d + 8 * a + 4 * h, o[r][d][4 * a], o[r][d][4 * a + 1], o[r][d][4 * a + 2],
-                                   o[r][d][4 * a + 3]);
-            continue;
-        }
-        if (!busy) continue;                             // wave-uniform
+        float* dst = p.ws_o + ((int64_t)t.split * p.total_q * p.hq + id) * p.hs + 4 * h;
 #pragma unroll
         for (int d = 0; d < DT; d++)
 #pragma unroll
             for (int a = 0; a < 4; a++)
-                write_lds(mine + c * 16 * OC + (((4 * d + a) ^ (c & (OW - 1))) << 4) + 8 * h,
-                          u32x2{pack_bf16x2(o[r][d][4 * a] * end.scale, o[r][d][4 * a + 1] * end.scale),
-                                pack_bf16x2(o[r][d][4 * a + 2] * end.scale, o[r][d][4 * a + 3] * end.scale)});
-        const uint64_t to = in ? reinterpret_cast<uint64_t>(dst) : 0;
-        wave_lds_ready();
+                if (EX || 32 * d + 8 * a + 4 * h < p.hs)
+                    *reinterpret_cast<f32x4*>(dst + 32 * d + 8 * a) =
+                        f32x4{o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2], o[d][4 * a + 3]};
+        return false;
+    }
+    RowEnd end{0.0f, 0.0f, 0.0f};
+    if (in) {
+        end = row_end_shifted<T>(p, token, head, m, ll);
+        if (h == 0 && p.lse) p.lse[token * p.lse_ts + head] = end.lse;
+    }
+    uint16_t* dst = p.out + token * p.o_ts + (int64_t)head * p.o_hs;
+    if (accumulates(p)) {
+        if (!in) return false;
 #pragma unroll
-        for (int k = 0; k < 32 * OC / kWave; k++) {
-            const int from = (k * kWave + lane) / OC, chunk = (k * kWave + lane) % OC;
-            const u32x4 x = read_lds<u32x4>(mine + from * 16 * OC + ((chunk ^ (from & (OW - 1))) << 4));
-            const uint64_t at = (uint64_t)(uint32_t)__shfl((int)(to >> 32), from) << 32 | (uint32_t)__shfl((int)to, from);
-            if (at != 0 && (EX || 8 * chunk < p.hs)) *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(at) + 8 * chunk) = x;
-        }
-        wave_lds_ready();
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+            for (int a = 0; a < 4; a++)
+                if (EX || 32 * d + 8 * a + 4 * h < p.hs)
+                    write_dims(p, end, dst + 32 * d + 8 * a + 4 * h, o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2],
+                               o[d][4 * a + 3]);
+        return false;
+    }
+    if (!busy) return false;                             // wave-uniform
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+        for (int a = 0; a < 4; a++)
+            write_lds(mine + c * 16 * OC + (((4 * d + a) ^ (c & (OW - 1))) << 4) + 8 * h,
+                      u32x2{pack_bf16x2(o[d][4 * a] * end.scale, o[d][4 * a + 1] * end.scale),
+                            pack_bf16x2(o[d][4 * a + 2] * end.scale, o[d][4 * a + 3] * end.scale)});
+    const uint64_t to = in ? reinterpret_cast<uint64_t>(dst) : 0;
+    wave_lds_ready();
+#pragma unroll
+    for (int k = 0; k < 32 * OC / kWave; k++) {
+        const int from = (k * kWave + lane) / OC, chunk = (k * kWave + lane) % OC;
+        const u32x4 x = read_lds<u32x4>(mine + from * 16 * OC + ((chunk ^ (from & (OW - 1))) << 4));
+        const uint64_t at = (uint64_t)(uint32_t)__shfl((int)(to >> 32), from) << 32 | (uint32_t)__shfl((int)to, from);
+        if (at != 0 && (EX || 8 * chunk < p.hs)) *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(at) + 8 * chunk) = x;
     }
     return false;
 }
 
-template <typename T, int DK, int DV, int R, bool EX, bool TREE, typename P>
+template <typename T, int DK, int DV, bool EX, bool TREE, typename P>
 __device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
-    if (attend_once<T, DK, DV, R, EX, TREE, false>(p, t, kvh, v0, v1, lds)) {
+    if (attend_once<T, DK, DV, EX, TREE, false>(p, t, kvh, v0, v1, lds)) {
         __syncthreads();
-        attend_once<T, DK, DV, R, EX, TREE, true>(p, t, kvh, v0, v1, lds);
+        attend_once<T, DK, DV, EX, TREE, true>(p, t, kvh, v0, v1, lds);
     }
 }
 

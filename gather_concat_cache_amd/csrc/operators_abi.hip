@@ -1,6 +1,7 @@
 // operators_abi.hip -- the extern "C" entry points of gcache_attention.h,
-// gcache_fp8_kv.h, gcache_prompt.h and gcache_pages.h: host checks, then one short sequence of launches on the
-// caller's stream.  Nothing here allocates, frees or synchronizes.
+// gcache_fp8_kv.h, gcache_prompt.h and gcache_pages.h: host checks, then one
+// short sequence of launches on the caller's stream.  Nothing here allocates,
+// frees or synchronizes.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
