@@ -59,16 +59,20 @@ constexpr int kMaxSplits = 256;
 // token of 16 heads over 65536 latent keys 34 us against 54 with a wave a row, 8
 // x 1 over 32768 48 against 54; but 2048 rows of 3 splits 46 against 44.
 constexpr int kWideRows = 2048, kWideSplits = 32;
+// Dims that half a wave's lanes hold, and the splits that they reduce.
+constexpr int kHalfDims = 128, kHalfSplits = 32;
 
 // WIDE: the four waves of a workgroup share a row, each with every fourth
 // split, so a single token's many splits are not read in one wave's sequence.
-template <bool WIDE, typename P>
+// HALF: a row takes half a wave (the same sums in the same order).
+template <bool WIDE, bool HALF, typename P>
 __global__ __launch_bounds__(kBlockThreads) void k_attention_join(P p, int64_t wg0) {
-    __shared__ float s_w[kWavesPerBlock][kMaxSplits];
+    constexpr int LANES = HALF ? kWave / 2 : kWave, SPLITS = HALF ? kHalfSplits : kMaxSplits, PER = kWave / LANES;
+    __shared__ float s_w[kWavesPerBlock * PER][SPLITS];
     __shared__ f32x4 s_acc[WIDE ? kWavesPerBlock : 1][WIDE ? kNope / 4 : 1];
-    const int lane = lane_id();
+    const int lane = lane_id() % LANES, part = wave_id() * PER + lane_id() / LANES;
     const int RT = p.row_tile;
-    const int64_t id = WIDE ? wg0 + blockIdx.x : (wg0 + blockIdx.x) * kWavesPerBlock + wave_id();
+    const int64_t id = WIDE ? wg0 + blockIdx.x : (wg0 + blockIdx.x) * (kWavesPerBlock * PER) + part;
     const int64_t rows = (int64_t)p.total_q * p.hq;
     if (id >= rows) return;
     const int token = (int)(id / p.hq), head = (int)(id % p.hq);
@@ -92,11 +96,11 @@ __global__ __launch_bounds__(kBlockThreads) void k_attention_join(P p, int64_t w
     const int chunk = *p.ws_chunk;
     if (t.total <= chunk) return;                        // written by its only workgroup
     const int n = min((t.total - 1) / chunk + 1, request_splits(request_work(p, t.b), chunk));
-    float* wts = s_w[wave_id()];                         // this wave's own
-    float mk[kMaxSplits / kWave], lk[kMaxSplits / kWave], mm = kNegInf, ll = 0.0f;
+    float* wts = s_w[part];                              // this row's own (WIDE: this wave's)
+    float mk[SPLITS / LANES], lk[SPLITS / LANES], mm = kNegInf, ll = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / kWave; i++) {
-        const int k = i * kWave + lane;
+    for (int i = 0; i < SPLITS / LANES; i++) {
+        const int k = i * LANES + lane;
         mk[i] = kNegInf;
         lk[i] = 0.0f;
         if (k < n) {
@@ -107,22 +111,22 @@ __global__ __launch_bounds__(kBlockThreads) void k_attention_join(P p, int64_t w
         mm = fmaxf(mm, mk[i]);
     }
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
+    for (int d = 1; d < LANES; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / kWave; i++) {
+    for (int i = 0; i < SPLITS / LANES; i++) {
         const float wt = mk[i] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(mk[i] - mm);
         ll = __builtin_fmaf(wt, lk[i], ll);
-        if (i * kWave + lane < n) wts[i * kWave + lane] = wt;
+        if (i * LANES + lane < n) wts[i * LANES + lane] = wt;
     }
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) ll += __shfl_xor(ll, d);
+    for (int d = 1; d < LANES; d <<= 1) ll += __shfl_xor(ll, d);
     const RowEnd end = row_end(p, token, head, mm, ll, p.gscale[1] ? *p.gscale[1] : 1.0f);
     __builtin_amdgcn_wave_barrier();
     constexpr int STEP = WIDE ? kWavesPerBlock : 1;
     const auto write = [&](int d, const f32x4& x) {
         write_dims(p, end, p.out + (int64_t)token * p.o_ts + (int64_t)head * p.o_hs + d, x[0], x[1], x[2], x[3]);
     };
-    for (int d = 4 * lane; d < p.hs; d += 4 * kWave) {
+    for (int d = 4 * lane; d < p.hs; d += 4 * LANES) {
         f32x4 acc = {0, 0, 0, 0};
         const float* src = p.ws_o + id * p.hs + d;
         int k = WIDE ? wave_id() : 0;
@@ -170,8 +174,11 @@ hipError_t launch_parts(void (*kernel)(P, int64_t), int waves, int row_tile, con
     const hipError_t e = launch_span(kernel, (units + 7) / 8 * 8 * p.hk, waves * kWave, s, true, !join, p);
     if (e != hipSuccess || !join) return e;
     const int64_t rows = (int64_t)p.total_q * p.hq;
-    if (rows <= kWideRows && p.splits >= kWideSplits) return launch_span(k_attention_join<true, P>, rows, kBlockThreads, s, false, true, p);
-    return launch_span(k_attention_join<false, P>, (rows + kWavesPerBlock - 1) / kWavesPerBlock, kBlockThreads, s, false, true, p);
+    if (rows <= kWideRows && p.splits >= kWideSplits) return launch_span(k_attention_join<true, false, P>, rows, kBlockThreads, s, false, true, p);
+    const bool half = p.hs <= kHalfDims && p.splits <= kHalfSplits;
+    const int64_t per = kWavesPerBlock * (half ? 2 : 1);
+    return launch_span(half ? k_attention_join<false, true, P> : k_attention_join<false, false, P>, (rows + per - 1) / per,
+                       kBlockThreads, s, false, true, p);
 }
 
 }  // namespace gcache
