@@ -22,7 +22,8 @@ AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, 
 }
 
 AttnPlan plan_attention_rows(int row_tiles, int64_t slots, int64_t total_q, int32_t batch, int32_t hq, int32_t hk,
-                             int32_t dv, int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail) {
+                             int32_t dv, int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail,
+                             bool even) {
     AttnPlan a;
     const int64_t group = hq / hk, rows = total_q * group;
     const int64_t mean = (rows + batch - 1) / batch;     // rows of a request and kv head
@@ -45,6 +46,8 @@ AttnPlan plan_attention_rows(int row_tiles, int64_t slots, int64_t total_q, int3
     // 12, 32 and 96 tiles for many rows give 589, 499 and 503 us for 32 x 32
     // latent tokens over 8192 keys, 235, 215 and 216 for 16 x 64 per-head ones;
     // 6 and 20 for few rows 130 and 121 for 128 x 1 latent tokens.
+    // even: all row tiles see about as many keys, so the ragged end is a quarter.
+    const int64_t ragged = even ? 4 : 2;
     const int64_t groups = (mean + rt - 1) / rt * batch * hk;
     const bool few = a.row_tiles <= 2;
     const int64_t extra = few ? 24 : 40;
@@ -56,10 +59,10 @@ AttnPlan plan_attention_rows(int row_tiles, int64_t slots, int64_t total_q, int3
     int64_t most = top;
     if (most > 8 * slots / groups) most = 8 * slots / groups;   // eight rounds are even enough
     if (!counts_requests(batch, hk)) most = 1;
-    int64_t splits = 1, best = rounds(groups) * kt + kt / 2;
+    int64_t splits = 1, best = rounds(groups) * kt + kt / ragged;
     for (int64_t n = 2; n <= most; n += n < 16 ? 1 : n / 16) {
         const int64_t c = ((kt + n - 1) / n + 3) / 4 * 4, m = (kt + c - 1) / c;
-        const int64_t cost = rounds(groups * m) * (c + extra) + c / 2;
+        const int64_t cost = rounds(groups * m) * (c + extra) + c / ragged;
         if (cost < best) {
             best = cost;
             splits = m;

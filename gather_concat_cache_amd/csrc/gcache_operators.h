@@ -67,11 +67,12 @@ struct AttnPlan {
 AttnPlan plan_attention(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t dp, int32_t dv,
                         int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail);
 AttnPlan plan_attention_rows(int row_tiles, int64_t slots, int64_t total_q, int32_t batch, int32_t hq, int32_t hk,
-                             int32_t dv, int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail);
+                             int32_t dv, int64_t max_seq_len, int32_t window, int32_t sinks, int64_t ws_floats_avail,
+                             bool even = false);
 AttnPlan plan_attention_fp8(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t hs, int64_t max_seq_len,
                             int32_t window, int32_t sinks, int64_t ws_floats_avail);
 AttnPlan plan_attention_prompt(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t dk, int32_t dv,
-                               int64_t max_key_len, int32_t window, int32_t sinks, int64_t ws_floats_avail);
+                               int64_t max_key_len, int32_t window, int32_t sinks, int64_t ws_floats_avail, bool even);
 hipError_t launch_attention_fp8(const AttnParams& p, int row_tiles, hipStream_t s);
 hipError_t launch_attention_prompt(const PromptParams& p, hipStream_t s);
 hipError_t launch_attention_kv(const AttnParams& p, int row_tiles, hipStream_t s);

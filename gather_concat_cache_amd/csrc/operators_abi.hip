@@ -573,8 +573,11 @@ int gcache_prompt_attention(const gcache_prompt_args* a, hipStream_t stream) {
     p.causal = a->causal != 0;
     p.accumulate = a->accumulate != 0;
     p.div = make_div(1);
+    // Chunks of context whose lengths are near the longest: 3 of 5264 to 7222 keys, 2784 queries of 16 heads, take 215 us
+    // without a split against 239 with the one that batches of unknown lengths get.
+    const bool even = !a->causal && a->max_key_len <= 4 * a->total_k / (3 * (int64_t)a->batch_size);
     const AttnPlan plan = plan_attention_prompt(p.total_q, p.batch, p.hq, p.hk, p.dk, p.hs, a->max_key_len, p.window, p.sinks,
-                                                workspace_floats(a->workspace, a->workspace_bytes));
+                                                workspace_floats(a->workspace, a->workspace_bytes), even);
     use_plan(plan, a->workspace, &p);
     if (((int64_t)p.units + 7) * p.hk > INT32_MAX) return GCACHE_ERR_SHAPE;  // workgroups are numbered in 32 bits
     return launched(launch_attention_prompt(p, stream));
@@ -587,7 +590,7 @@ int64_t gcache_prompt_workspace_bytes(int64_t total_q, int32_t batch_size, int32
         key_size <= 0 || value_size <= 0 || max_key_len < 0 || window < 0 || num_sinks < 0 || total_q > kMaxRows / num_q_heads)
         return 0;
     return plan_attention_prompt(total_q, batch_size, num_q_heads, num_kv_heads, key_size, value_size, max_key_len, window,
-                                 num_sinks, INT64_MAX).ws_floats * (int64_t)sizeof(float);
+                                 num_sinks, INT64_MAX, false).ws_floats * (int64_t)sizeof(float);
 }
 
 int64_t gcache_pages_workspace_bytes(int64_t num_blocks, int32_t num_rows, int64_t num_requests) {

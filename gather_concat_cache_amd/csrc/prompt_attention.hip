@@ -38,9 +38,10 @@ hipError_t launch_attention_prompt(const PromptParams& p, hipStream_t s) {
 }
 
 AttnPlan plan_attention_prompt(int64_t total_q, int32_t batch, int32_t hq, int32_t hk, int32_t dk, int32_t dv,
-                               int64_t max_key_len, int32_t window, int32_t sinks, int64_t ws_floats_avail) {
+                               int64_t max_key_len, int32_t window, int32_t sinks, int64_t ws_floats_avail, bool even) {
     const int64_t slots = 256 * (dk <= 192 && dv <= 128 ? 2 : 1);
-    return plan_attention_rows(kTileRows / 16, slots, total_q, batch, hq, hk, dv, max_key_len, window, sinks, ws_floats_avail);
+    return plan_attention_rows(kTileRows / 16, slots, total_q, batch, hq, hk, dv, max_key_len, window, sinks, ws_floats_avail,
+                               even);
 }
 
 }  // namespace gcache

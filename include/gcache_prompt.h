@@ -36,8 +36,8 @@ extern "C" {
  * Rows outside [query_starts[0], query_starts[batch]) are left as they were.
  * query_starts and key_starts must be non-decreasing (values are clamped to
  * [0, total_q] and [0, total_k]; otherwise rows belong to unspecified requests).
- *   max_key_len: the most keys of a request the caller expects; it only sizes
- *   the split of the keys.  The split follows the lengths of the whole batch:
+ *   max_key_len: the most keys of a request the caller expects; it (and total_k,
+ *   which tells even lengths) only sizes the split of the keys.  The split follows the lengths of the whole batch:
  *   equal calls give equal bits, but the last bits of a row may change with the
  *   other requests.
  *   workspace: gcache_prompt_workspace_bytes() bytes, 16-byte aligned, or less,
