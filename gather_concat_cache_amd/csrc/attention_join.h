@@ -50,10 +50,11 @@ __device__ __forceinline__ void write_dims(const PromptParams& p, const RowEnd& 
     *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
 }
 
-// Join the key splits of a row: one wave per (token, head).  The splits'
-// maxima and sums are read by a lane each and reduced across the wave; the
-// weighted rows follow with four loads in flight.  Bound by memory: the parts
-// of 761 tokens of 32 heads of 128, seven each on average, take 26 us.
+// Join the key splits of a row: a wave, or half of one, per (token, head).  The
+// splits' maxima and sums are read by a lane each and reduced across the wave;
+// the weighted rows follow with four loads in flight.  Bound by the latency of a
+// chain of dependent loads, so by rows in flight: the parts of 761 tokens of 32
+// heads of 128, seven each on average, take 14 us, and 22 with a wave a row.
 constexpr int kMaxSplits = 256;
 // Rows and planned splits (half of the bound p.splits) for a workgroup a row: 1
 // token of 16 heads over 65536 latent keys 34 us against 54 with a wave a row, 8
