@@ -699,6 +699,26 @@ def test_prompt_chunks_of_context(g):
     assert float((out.float() - whole.float()).abs().max()) < bound
 
 
+@pytest.mark.parametrize("tokens", [1, 8, 9])
+def test_prompt_many_splits(g, tokens):
+    """Dozens of key splits a row, for the joins of few rows and of more than
+    2048: against the call that does not split.  Values are positive and grow
+    along the keys, so that outputs (1 .. 3) are off by less than four roundings
+    of 2^-8 to bf16 (weights and outputs, both calls); an lse of about 10 by the
+    rounding of sums, 2^-24 a step of 512 and of the parts."""
+    rng = np.random.default_rng(11)
+    n, hq = 32768, 256
+    q, k = (ref.bf16(rng.standard_normal((m, h, 64)))[0].cuda() for m, h in ((tokens, hq), (n, 1)))
+    v = (1 + torch.arange(n, device="cuda") / n)[:, None, None].expand(n, 1, 64) + torch.rand(n, 1, 64, device="cuda")
+    v = v.to(torch.bfloat16)
+    qs, ks = dev(np.array([0, tokens], np.int32)), dev(np.array([0, n], np.int32))
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    one, one_lse = g.prompt_attention(q, k, v, qs, ks, n, 0.125, return_lse=True, workspace=none)
+    out, lse = g.prompt_attention(q, k, v, qs, ks, n, 0.125, return_lse=True)
+    assert float((lse - one_lse).abs().max()) < 1e-3
+    assert float(((out.float() - one.float()) / one.float()).abs().max()) < 4 * 2.0 ** -8
+
+
 def test_prompt_values_that_are_hidden(g):
     """Infinities and NaN in keys and values reach the rows that see them and
     no other, not those of the same tile or of the next sequence."""
