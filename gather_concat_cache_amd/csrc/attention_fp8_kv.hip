@@ -7,10 +7,13 @@
 //     P_j = exp2(s_j + log2 vscale_j - m),  o = sum P_j code_j / sum P_j / vscale_j,
 // which keeps the weights that meet the codes within binary16 whatever the
 // scales are.  The scales are constant over the keys of a page, so this costs
-// no operation a weight.  Scores are binary32 sums of exact products of
-// binary16 (an e4m3 value is exact there, a query row is scaled by a power of
-// two); only the weights are rounded, to 11 bits, shifted up so that they stay
-// normal down to 2^-20 of the largest.
+// no operation a weight.  Where value scales are so far apart that sum P_j /
+// vscale_j would leave binary32 (far_scale()), the row's sum goes on apart, as
+// sum exp2(s_j - M) with the maximum M of the logits alone, and
+//     o = sum P_j code_j 2^(m - M) / sum exp2(s_j - M).
+// Scores are binary32 sums of exact products of binary16 (an e4m3 value is exact
+// there, a query row is scaled by a power of two); only the weights are rounded,
+// to 11 bits, shifted up so that they stay normal down to 2^-20 of the largest.
 #include "attention_tiles.h"
 
 namespace gcache {
@@ -79,6 +82,7 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
     static_assert(kFew * 16 * OROW * 4 <= kFew * 4 * SIDE, "the join fits the ring");
     __shared__ __attribute__((aligned(256))) uint8_t s_ring[kFew][4][SIDE];      // K, V of two tiles
     __shared__ float s_m[kFew][16], s_l[kFew][16];
+    __shared__ FarSum s_far[kFew][R][kWave];             // in LDS, because few rows ever use it
 
     // heads of a unit 8 apart: the same XCD
     const uint32_t wg = (uint32_t)wg0 + blockIdx.x, per = 8 * (uint32_t)p.hk, set = wg / per, rem = wg - set * per;
@@ -158,6 +162,17 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
         }
     }
 
+    // The rows see a far page: s_far holds their sums then, l does not.  One row
+    // tile looks in every 32-key tile (64 x 1 over 8192 keys 229 us against 235);
+    // two look at all pages first and have a loop for either answer, because that
+    // loop has no registers left (16 x 8 tokens 64 us against 65, pages of 24 108
+    // against 117).
+    bool far = R > 1 && sees_far(p, t, kvh, v0, v1);
+    if (far) {
+#pragma unroll
+        for (int r = 0; r < R; r++) s_far[w][r][lane] = FarSum{kNegInf, 0.0f};
+    }
+
     // ---- query rows, the dims as the K reads hold them
     f16x8 q[R][KS];
     float fac[R];
@@ -195,136 +210,156 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
         for (int d = 0; d < DT; d++) o[r][d] = f32x4{0, 0, 0, 0};
     }
 
-    for (int slot = 0; v < v1; v += kFew, slot ^= 1) {
-        const bool one = v + kFew < v1, two = v + 2 * kFew < v1;
-        const int key0 = tile_key(v);
-        const uint32_t k_at = ring + 2 * slot * SIDE + k_lane, v_at = ring + (2 * slot + 1) * SIDE + v_lane;
-        if (one) wait_loads<2 * N>();                    // the tile ahead stays in flight
-        else wait_loads<0>();
-        // ---- S^T = K Q^T
-        f32x4 s[R][2];
-        u32x4 raw[2][KS / 2];
+    // apart: whether a far page is there, or (R = 1) may be
+    const auto loop = [&](auto apart) {
+        for (int slot = 0; v < v1; v += kFew, slot ^= 1) {
+            const bool one = v + kFew < v1, two = v + 2 * kFew < v1;
+            const int key0 = tile_key(v);
+            const uint32_t k_at = ring + 2 * slot * SIDE + k_lane, v_at = ring + (2 * slot + 1) * SIDE + v_lane;
+            if (one) wait_loads<2 * N>();                    // the tile ahead stays in flight
+            else wait_loads<0>();
+            // ---- S^T = K Q^T
+            f32x4 s[R][2];
+            u32x4 raw[2][KS / 2];
 #pragma unroll
-        for (int kt = 0; kt < 2; kt++)
+            for (int kt = 0; kt < 2; kt++)
 #pragma unroll
-            for (int j = 0; j < KS / 2; j++)
-                raw[kt][j] = read_lds<u32x4>(chunk_at<NC>(k_at, 4 * j) + kt * 16 * DP);
-#pragma unroll
-        for (int kt = 0; kt < 2; kt++) {
-#pragma unroll
-            for (int r = 0; r < R; r++) s[r][kt] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < KS / 2; j++) {
-                const f16x8 a = fp8_operand(raw[kt][j].x, raw[kt][j].y), b = fp8_operand(raw[kt][j].z, raw[kt][j].w);
-#pragma unroll
-                for (int r = 0; r < R; r++) {
-                    s[r][kt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][2 * j], s[r][kt], 0, 0, 0);
-                    s[r][kt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, q[r][2 * j + 1], s[r][kt], 0, 0, 0);
-                }
-            }
-        }
-        // ---- K's place takes the tile two ahead
-        Pages x = next;
-        Scales sc_two;
-        if (two) {
-            next = find(v + 3 * kFew);
-            sc_two = scales(x);
-            reads_done();
-            issue(x, slot, 0);
-        }
-        // ---- logits with the scales of their pages
-        uint32_t live;
-        float inv[UNI ? 2 : 8];
-        if constexpr (UNI) {
-            live = 0;
+                for (int j = 0; j < KS / 2; j++)
+                    raw[kt][j] = read_lds<u32x4>(chunk_at<NC>(k_at, 4 * j) + kt * 16 * DP);
 #pragma unroll
             for (int kt = 0; kt < 2; kt++) {
-                const PageScale ps = scale_of(sc.raw[kt], sc.live[kt]);
-                live |= sc.live[kt] ? 0xFu << (4 * kt) : 0u;
-                inv[kt] = ps.inv_v;
 #pragma unroll
-                for (int r = 0; r < R; r++) {
-                    const float f = fac[r] * ps.k;
+                for (int r = 0; r < R; r++) s[r][kt] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < 4; i++) s[r][kt][i] = __builtin_fmaf(s[r][kt][i], f, ps.log2_v);
+                for (int j = 0; j < KS / 2; j++) {
+                    const f16x8 a = fp8_operand(raw[kt][j].x, raw[kt][j].y), b = fp8_operand(raw[kt][j].z, raw[kt][j].w);
+#pragma unroll
+                    for (int r = 0; r < R; r++) {
+                        s[r][kt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[r][2 * j], s[r][kt], 0, 0, 0);
+                        s[r][kt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, q[r][2 * j + 1], s[r][kt], 0, 0, 0);
+                    }
                 }
             }
-        } else {
-            const PageScale ps = scale_of(sc.raw[0], sc.live[0]);
-            const uint64_t bits = __ballot(sc.live[0]);
-            live = (uint32_t)(bits >> (4 * g) & 0xF) | (uint32_t)(bits >> (16 + 4 * g) & 0xF) << 4;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int from = 16 * (j >> 2) + 4 * g + (j & 3);
-                const float ks = __shfl(ps.k, from), lv = __shfl(ps.log2_v, from);
-                inv[j] = __shfl(ps.inv_v, from);
-#pragma unroll
-                for (int r = 0; r < R; r++) s[r][j >> 2][j & 3] = __builtin_fmaf(s[r][j >> 2][j & 3], fac[r] * ks, lv);
+            // ---- K's place takes the tile two ahead
+            Pages x = next;
+            Scales sc_two;
+            if (two) {
+                next = find(v + 3 * kFew);
+                sc_two = scales(x);
+                reads_done();
+                issue(x, slot, 0);
             }
-        }
-        const bool all = __all(live == 0xFFu && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kTileKeys));
-        if (!all) {
+            // ---- logits with the scales of their pages
+            uint32_t live;
+            float inv[UNI ? 2 : 8];
+            bool odd = false;                                // a page of the tile is far
+            if constexpr (UNI) {
+                live = 0;
 #pragma unroll
-            for (int r = 0; r < R; r++) hide<TREE, 2>(p, t, pos[r], tok[r], key0 + 4 * g, live, s[r]);
-        }
-        // ---- running maximum; the accumulators follow it with a lag
-        float top[R];
-        bool late = false;
+                for (int kt = 0; kt < 2; kt++) {
+                    const PageScale ps = scale_of(sc.raw[kt], sc.live[kt]);
+                    odd = odd || (R == 1 && far_page(t, sc.raw[kt], sc.live[kt], key0 + 16 * kt));
+                    live |= sc.live[kt] ? 0xFu << (4 * kt) : 0u;
+                    inv[kt] = ps.inv_v;
 #pragma unroll
-        for (int r = 0; r < R; r++) {
-            top[r] = group_max(max8(s[r][0], s[r][1]));
-            late = late || top[r] > m[r] + kLag;
-        }
-        if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first tiles
+                    for (int r = 0; r < R; r++) {
+                        const float f = fac[r] * ps.k;
+#pragma unroll
+                        for (int i = 0; i < 4; i++) s[r][kt][i] = __builtin_fmaf(s[r][kt][i], f, ps.log2_v);
+                    }
+                }
+            } else {
+                const PageScale ps = scale_of(sc.raw[0], sc.live[0]);
+                odd = R == 1 && far_page(t, sc.raw[0], sc.live[0], key0 + (lane & 31));
+                const uint64_t bits = __ballot(sc.live[0]);
+                live = (uint32_t)(bits >> (4 * g) & 0xF) | (uint32_t)(bits >> (16 + 4 * g) & 0xF) << 4;
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int from = 16 * (j >> 2) + 4 * g + (j & 3);
+                    const float ks = __shfl(ps.k, from), lv = __shfl(ps.log2_v, from);
+                    inv[j] = __shfl(ps.inv_v, from);
+#pragma unroll
+                    for (int r = 0; r < R; r++) s[r][j >> 2][j & 3] = __builtin_fmaf(s[r][j >> 2][j & 3], fac[r] * ks, lv);
+                }
+            }
+            const bool all = __all(live == 0xFFu && all_seen<TREE>(p, t, pos_lo, pos_hi, key0, kTileKeys));
+            if (!all) {
+#pragma unroll
+                for (int r = 0; r < R; r++) hide<TREE, 2>(p, t, pos[r], tok[r], key0 + 4 * g, live, s[r]);
+            }
+            // ---- running maximum; the accumulators follow it with a lag
+            float top[R];
+            bool late = apart.value && (far || odd);
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                const float mn = fmaxf(m[r], top[r]);
-                const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
-                m[r] = mn;
-                l[r] *= al;
-#pragma unroll
-                for (int d = 0; d < DT; d++) o[r][d] *= al;
+                top[r] = group_max(max8(s[r][0], s[r][1]));
+                late = late || top[r] > m[r] + kLag;
             }
-        }
-        f16x8 pw[R];
+            if (__builtin_expect(__any(late), 0)) {          // wave-uniform, rare after the first tiles
+                const bool now = apart.value && (far || __any(odd));
 #pragma unroll
-        for (int r = 0; r < R; r++) {
-            const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
+                for (int r = 0; r < R; r++) {
+                    const float mn = fmaxf(m[r], top[r]);
+                    const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
+                    m[r] = mn;
+                    l[r] *= al;
 #pragma unroll
-            for (int kt = 0; kt < 2; kt++) {
-                float sum = 0.0f;
+                    for (int d = 0; d < DT; d++) o[r][d] *= al;
+                    if (now) {                               // (l holds the tiles before this one)
+                        FarSum fs = far ? s_far[w][r][lane] : FarSum{m[r], l[r]};
+                        const auto logit = [&](int j) { return s[r][j >> 2][j & 3] + __builtin_log2f(inv[UNI ? j >> 2 : j]); };
+                        float most = kNegInf;
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float e = __builtin_amdgcn_exp2f(s[r][kt][i] + sub);
-                    if constexpr (UNI) sum += e;
-                    else sum = __builtin_fmaf(e, inv[4 * kt + i], sum);
-                    pw[r][4 * kt + i] = (_Float16)e;
+                        for (int j = 0; j < 8; j++) most = fmaxf(most, logit(j));
+                        far_add<8>(fs, group_max(most), kShift, logit);
+                        s_far[w][r][lane] = fs;
+                    }
                 }
-                l[r] = UNI ? __builtin_fmaf(sum, inv[UNI ? kt : 0], l[r]) : l[r] + sum;
+                far = now;
             }
-        }
-        // ---- O^T += V^T P^T
-        const auto multiply = [&](auto fix) {
-            u32x2 vr[DT];
+            f16x8 pw[R];
 #pragma unroll
-            for (int d = 0; d < DT; d++)
-                vr[d] = __builtin_bit_cast(u32x2, read_transposed8(chunk_at<NC>(v_at, d)));
+            for (int r = 0; r < R; r++) {
+                const float sub = m[r] == kNegInf ? 0.0f : kShift - m[r];
 #pragma unroll
-            for (int d = 0; d < DT; d++) {
-                const f16x8 a = fp8_operand(fix(vr[d].x), fix(vr[d].y));
+                for (int kt = 0; kt < 2; kt++) {
+                    float sum = 0.0f;
 #pragma unroll
-                for (int r = 0; r < R; r++) o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw[r], o[r][d], 0, 0, 0);
+                    for (int i = 0; i < 4; i++) {
+                        const float e = __builtin_amdgcn_exp2f(s[r][kt][i] + sub);
+                        if constexpr (UNI) sum += e;
+                        else sum = __builtin_fmaf(e, inv[4 * kt + i], sum);
+                        pw[r][4 * kt + i] = (_Float16)e;
+                    }
+                    l[r] = UNI ? __builtin_fmaf(sum, inv[UNI ? kt : 0], l[r]) : l[r] + sum;
+                }
             }
-        };
-        if (all) multiply([](uint32_t x) { return x; });
-        else multiply([](uint32_t x) { return drop_nan_e4m3x4(x); });    // hidden codes may be NaN
-        if (two) {
-            reads_done();
-            issue(x, slot, 1);
+            // ---- O^T += V^T P^T
+            const auto multiply = [&](auto fix) {
+                u32x2 vr[DT];
+#pragma unroll
+                for (int d = 0; d < DT; d++)
+                    vr[d] = __builtin_bit_cast(u32x2, read_transposed8(chunk_at<NC>(v_at, d)));
+#pragma unroll
+                for (int d = 0; d < DT; d++) {
+                    const f16x8 a = fp8_operand(fix(vr[d].x), fix(vr[d].y));
+#pragma unroll
+                    for (int r = 0; r < R; r++) o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, pw[r], o[r][d], 0, 0, 0);
+                }
+            };
+            if (all) multiply([](uint32_t x) { return x; });
+            else multiply([](uint32_t x) { return drop_nan_e4m3x4(x); });    // hidden codes may be NaN
+            if (two) {
+                reads_done();
+                issue(x, slot, 1);
+            }
+            sc = sc_next;
+            if (two) sc_next = sc_two;
         }
-        sc = sc_next;
-        if (two) sc_next = sc_two;
-    }
+
+    };
+    if (R == 1 || far) loop(std::true_type{});
+    else loop(std::false_type{});
 
     // ---- join the four waves, 16 rows at a time
     float* s_o = reinterpret_cast<float*>(&s_ring[0][0][0]);
@@ -332,7 +367,14 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
     const int jr = threadIdx.x >> 4, jc = threadIdx.x & 15;   // the row and dim column this thread writes
 #pragma unroll
     for (int r = 0; r < R; r++) {
-        const float lw = group_sum(l[r]);
+        float lw = group_sum(l[r]);
+        if (__builtin_expect(far, 0)) {
+            const FarSum fs = s_far[w][r][lane];
+            lw = group_sum(fs.l);
+            const float mean = far_end(fs, m[r], lw);
+#pragma unroll
+            for (int d = 0; d < DT; d++) o[r][d] *= mean;
+        }
         __syncthreads();                                 // the other waves' reads of the ring, or of the last rows
         if (g == 0) {
             s_m[w][c] = m[r];

@@ -313,6 +313,60 @@ struct PageWalk {
         if (UNI ? lane == 0 : lane < 16) to[UNI ? wave : 16 * wave + lane] = s;
     }
 };
+// Rows that see a far page hold the sum of their weights with a maximum of its
+// own, that of their logits alone: 2^(top - shift) l.
+struct FarSum {
+    float top, l;
+};
+// Adds N weights; logit(j) in log2 units, `most` their maximum over the lanes of the row.
+template <int N, typename Logit>
+__device__ __forceinline__ void far_add(FarSum& f, float most, float shift, Logit logit) {
+    const float to = fmaxf(f.top, most);
+    if (to == kNegInf) return;
+    const float by = shift - to;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; j++) sum += __builtin_amdgcn_exp2f(logit(j) + by);
+    f.l = __builtin_fmaf(f.l, __builtin_amdgcn_exp2f(f.top - to), sum);
+    f.top = to;
+}
+// The row's end in the form that joins have: the factor that makes its weighted
+// values their mean, with m and a sum of 1 (0 where nothing was seen) beside it.
+// l: over the lanes of the row.
+__device__ __forceinline__ float far_end(const FarSum& f, float& m, float& l) {
+    if (l == 0.0f) return 1.0f;
+    const float mean = __builtin_amdgcn_exp2f(m - f.top) / l;
+    m = f.top + __builtin_log2f(l);
+    l = 1.0f;
+    return mean;
+}
+
+// Whether the page of `key` is far; scales behind the last key may be anything.
+__device__ __forceinline__ bool far_page(const RowTile& t, const RawScale& r, bool exists, int key) {
+    return exists && key < t.kv_len && far_scale(page_scale(r.v));
+}
+// Whether a page with keys of the 32-key tiles [v0, v1) is far: the workgroup's
+// lanes look at a page each, before the tile begins.  (4 x 2048 tokens over 4096
+// keys: 1 per cent; looking in every step instead 5.)
+__device__ __forceinline__ bool sees_far(const AttnParams& p, const RowTile& t, int kvh, int v0, int v1) {
+    const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
+    const float* scales = p.gscale[0] + p.L.scale_offset + kvh * p.L.scale_head_stride;
+    bool far = false;
+    const auto look = [&](int key0, int key1) {          // keys [key0, key1)
+        int first, last, off;
+        split_position(p, key0, first, off);
+        split_position(p, max(min(key1, t.kv_len), key0 + 1) - 1, last, off);
+        for (uint32_t i = first + threadIdx.x; i <= (uint32_t)last; i += kTileWaves * kWave) {
+            const PageAt at{bt_row[i], 0};
+            if (page_exists(p, at)) far = far || far_scale(page_scale(scales[(int64_t)at.blk * p.L.scale_token_stride]));
+        }
+    };
+    const int sinks = min(t.sink_tiles, v1), from = max(v0, t.sink_tiles);
+    if (v0 < sinks) look(v0 * kTileKeys, sinks * kTileKeys);
+    if (from < v1) look((from - t.sink_tiles + t.win_tile0) * kTileKeys, (v1 - t.sink_tiles + t.win_tile0) * kTileKeys);
+    return __syncthreads_or(far);
+}
+
 struct NoWalk {};
 
 // N fragments with DEPTH reads in flight.  Piece i of `side`, vector work that
@@ -469,8 +523,10 @@ __device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::f
 // The scores of step i + 1 are multiplied while step i's weights are computed,
 // and its values while the next logits are scaled: a wave's matrix instructions
 // and its vector ones are independent, and run side by side.
+// apart: the tile sees far pages and sums its weights apart (FarSum; CAREFUL only).
 template <typename T, int DK, int DV, bool EX, bool TREE, bool CAREFUL, typename P>
-__device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
+__device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kvh, int v0, int v1, bool apart,
+                                            StepLds<T, DK, DV, EX>& lds) {
     typedef StepLds<T, DK, DV, EX> L;
     typedef typename T::frag frag;
     constexpr int KS = DK / 16, DT = DV / 32, KC = L::KB / 16, VC = L::VB / 16;
@@ -573,6 +629,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         for (int j = 0; j < 16; j++) o[d][j] = 0.0f;
     f32x16 s[2];                                         // of the step whose weights come next
     bool seen_all = true;                                // no key of it is hidden
+    FarSum fs{kNegInf, 0.0f};                            // apart: the row's sum, in place of l
 
     // ---- logits of a step from its scores: scaled, shifted, the hidden ones -infinity; the running maximum, which the
     // accumulators follow with a lag
@@ -642,6 +699,17 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                 for (int d = 0; d < DT; d++)
 #pragma unroll
                     for (int j = 0; j < 16; j++) o[d][j] *= al;
+            }
+        }
+        if constexpr (FP8 && CAREFUL) {
+            if (apart) {
+                const auto logit = [&](int j) {
+                    return x[j >> 4][j & 15] - (sub + lds.at[n & 3][EX ? j >> 3 : 8 * (j >> 2) + 4 * h + (j & 3)].log2_v);
+                };
+                float most = kNegInf;
+#pragma unroll
+                for (int j = 0; j < 32; j++) most = fmaxf(most, logit(j));
+                far_add<32>(fs, pair_max(most), T::kShiftUp, logit);
             }
         }
     };
@@ -790,7 +858,17 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     static_assert(kTileWaves * 32 * 16 * OC <= sizeof(lds.k) + (FP8 ? sizeof(lds.v) : 0), "rows of all waves fit");
     const uint32_t mine = lds_k + w * 32 * 16 * OC;
     if (CAREFUL) tile_ready();
-    const float ll = pair_sum(l);
+    float ll = pair_sum(l);
+    if constexpr (FP8 && CAREFUL) {
+        if (apart) {
+            ll = pair_sum(fs.l);
+            const float mean = far_end(fs, m, ll);
+#pragma unroll
+            for (int d = 0; d < DT; d++)
+#pragma unroll
+                for (int j = 0; j < 16; j++) o[d][j] *= mean;
+        }
+    }
     const bool in = row_of >= 0;
     const int row = max(row_of, 0), tl = row_token(p, row), head = kvh * p.group + row - tl * p.group;
     const int64_t token = t.q0 + tl, id = token * p.hq + head;
@@ -850,9 +928,11 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
 
 template <typename T, int DK, int DV, bool EX, bool TREE, typename P>
 __device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
-    if (attend_once<T, DK, DV, EX, TREE, false>(p, t, kvh, v0, v1, lds)) {
+    bool apart = false;
+    if constexpr (T::kFp8) apart = sees_far(p, t, kvh, v0, v1);
+    if (apart || attend_once<T, DK, DV, EX, TREE, false>(p, t, kvh, v0, v1, false, lds)) {
         __syncthreads();
-        attend_once<T, DK, DV, EX, TREE, true>(p, t, kvh, v0, v1, lds);
+        attend_once<T, DK, DV, EX, TREE, true>(p, t, kvh, v0, v1, apart, lds);
     }
 }
 

@@ -11,6 +11,14 @@ namespace gcache {
 constexpr float kLeastScale = 0x1p-100f, kLargestScale = 0x1p121f;
 __device__ __forceinline__ float page_scale(float s) { return fminf(fmaxf(s, kLeastScale), kLargestScale); }
 
+// Value scales that the attention's sums take as they come: a row's weights carry
+// their pages' value scales, P = exp2(s + log2 scale - m), and its sum adds P /
+// scale.  Between these bounds that stays below 2^14 2^40 a key, and a P that
+// exp2 flushes to 0 is a weight below 2^-68 of the row's largest.  Scales outside
+// are far: rows that see one sum their weights apart (an append of zeros makes
+// the least scale).
+__device__ __forceinline__ bool far_scale(float s) { return s < 0x1p-40f || s > 0x1p24f; }
+
 // The scale that values up to `largest` need.
 __device__ __forceinline__ float append_need(float largest) { return fminf(fmaxf(largest / 448.0f, kLeastScale), 0x1p120f); }
 
