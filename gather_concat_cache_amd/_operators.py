@@ -1,5 +1,5 @@
-"""ctypes binding of the operators around the cache (include/gcache_attention.h
-and include/gcache_pages.h): attention over the quantized pages, query/key
+"""ctypes binding of the operators around the cache (include/gcache_attention.h,
+include/gcache_pages.h and include/gcache_page_sets.h): attention over the quantized pages, query/key
 norms with the position rotation, and page ownership.
 
 Argument marshalling only, as in _native: checks of dtype, device and layout,
@@ -56,6 +56,12 @@ _SIGS = {
     "gcache_compact_pages": (C.c_int, [_STATE, _CACHES, _P, _P, _I64, _P]),
 }
 
+_SET_SIGS = {
+    "gcache_copy_page_sets": (C.c_int, [_CACHES, _I32, _I64, _P, _P, _I64, _P]),
+    "gcache_fork_page_sets": (C.c_int, [_STATE, _CACHES, _I32, _P, _P, _I64, _P, _P, _I64, _P]),
+    "gcache_compact_page_sets": (C.c_int, [_STATE, _CACHES, _I32, _P, _P, _I64, _P]),
+}
+
 _INT32_MAX = 2 ** 31 - 1
 _lib = None
 
@@ -64,7 +70,7 @@ def _load():
     global _lib
     if _lib is None:
         lib = load()
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in {**_SIGS, **_SET_SIGS}.items():
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
         _lib = lib
@@ -381,27 +387,48 @@ def tree_attention_nvfp4_ds_mla(q, kv_cache, block_table, query_starts, seq_lens
 # pages
 # ---------------------------------------------------------------------------
 def _page_caches(caches):
-    """One cache or a sequence of them (one a layer), dim 0 the pages, all of
-    one geometry -> (PageCaches and what it points to, num_blocks, device)."""
+    """One cache or a sequence of them (one a layer, or codes and scales of each),
+    dim 0 the pages -> (pointer to a PageCaches for each geometry, their
+    number, what they point to, num_blocks, device)."""
     caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
     if not caches:
         raise ValueError("caches must name at least one cache")
+    pc, array, nb, dev, rest = _one_geometry(caches)
+    if not rest:
+        return C.byref(pc), 1, array, nb, dev
+    sets, keep = [pc], [array]
+    while rest:
+        pc, array, pages, device, rest = _one_geometry(rest)
+        if pages != nb or device != dev:
+            raise ValueError("caches must be GPU tensors on one device, of the same number of pages")
+        sets.append(pc)
+        keep.append(array)
+    return (PageCaches * len(sets))(*sets), len(sets), keep, nb, dev
+
+
+def _one_geometry(caches):
+    """PageCaches of those caches that are like the first, what it points to,
+    their pages and device, and the other caches."""
     first = caches[0]
     if not isinstance(first, torch.Tensor) or first.device.type != "cuda":
         raise ValueError("caches must be GPU tensors on one device")
     shape, strides, dtype, dev = first.shape, first.stride(), first.dtype, first.device
     if len(shape) < 2:
         raise ValueError("a cache must be [num_blocks, ...]")
+    like, rest = caches, []
     for c in caches:
         if c.shape != shape or c.stride() != strides or c.dtype is not dtype or c.device != dev:
-            raise ValueError("caches must be GPU tensors on one device, of one shape, strides and dtype")
+            rest.append(c)
+    if rest:
+        other = set(map(id, rest))
+        like = [c for c in caches if id(c) not in other]
     item = first.element_size()
     page = 0 if 0 in shape[1:] else item * (1 + sum((n - 1) * s for n, s in zip(shape[1:], strides[1:])))
     stride = strides[0] * item if shape[0] > 1 else max(page, strides[0] * item)
     if page > stride:
         raise ValueError("the pages of a cache must not overlap")
-    array = (C.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
-    return PageCaches(C.addressof(array), len(caches), stride, page), array, shape[0], dev
+    array = (C.c_void_p * len(like))(*[c.data_ptr() for c in like])
+    return PageCaches(C.addressof(array), len(like), stride, page), array, shape[0], dev, rest
 
 
 def _page_state(block_size, block_table, seq_lens, ref_counts, dev=None):
@@ -437,16 +464,17 @@ def _status(status, n, dev):
 
 def copy_pages(caches, src, dst, stream=None):
     """Copy pages src[i] -> dst[i] (int32 vectors) in every cache: a tensor
-    [num_blocks, ...] or a sequence of such tensors of one geometry.  A page
-    goes from its first element to its last, padding between them included
-    (for forks and compaction too); bytes between pages stay.  Destinations
-    are distinct and none is a source."""
-    pc, _keep, nb, dev = _page_caches(caches)
+    [num_blocks, ...] or a sequence of such tensors, of one geometry or several
+    (the 8-bit cache and its kv_scales, which a page needs both; for forks and
+    compaction too).  A page goes from its first element to its last, padding
+    between them included; bytes between pages stay.  Destinations are distinct
+    and none is a source."""
+    pc, sets, _keep, nb, dev = _page_caches(caches)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return copy_pages(caches, src, dst)
     n = _requests(("src", "dst"), (src, dst), dev)
-    _check(_load().gcache_copy_pages(C.byref(pc), nb, src.data_ptr(), dst.data_ptr(), n, _raw_stream(dev.index)),
+    _check(_load().gcache_copy_page_sets(pc, sets, nb, src.data_ptr(), dst.data_ptr(), n, _raw_stream(dev.index)),
            "gcache_copy_pages")
 
 
@@ -457,7 +485,7 @@ def fork_requests(caches, block_size, block_table, seq_lens, ref_counts, parent_
     cache.  State: block_table int32 [rows, max_blocks], seq_lens int32 [rows],
     ref_counts int32 [num_blocks] (0: free).  Returns status int32: 1, or 0
     where the fork was refused (gcache_pages.h says when)."""
-    pc, _keep, nb, dev = _page_caches(caches)
+    pc, sets, _keep, nb, dev = _page_caches(caches)
     ps, dev = _page_state(block_size, block_table, seq_lens, ref_counts, dev)
     if nb != ref_counts.numel():
         raise ValueError("ref_counts must hold one count per page of the caches")
@@ -470,8 +498,8 @@ def fork_requests(caches, block_size, block_table, seq_lens, ref_counts, parent_
     if n:
         lib = _load()
         ws, nbytes = _scratch(workspace, lib.gcache_pages_workspace_bytes(nb, ps.num_rows, n), dev)
-        _check(lib.gcache_fork_requests(C.byref(ps), C.byref(pc), parent_rows.data_ptr(), child_rows.data_ptr(), n,
-                                        status.data_ptr(), _ptr(ws), nbytes, _raw_stream(dev.index)),
+        _check(lib.gcache_fork_page_sets(C.byref(ps), pc, sets, parent_rows.data_ptr(), child_rows.data_ptr(), n,
+                                         status.data_ptr(), _ptr(ws), nbytes, _raw_stream(dev.index)),
                "gcache_fork_requests")
     return status
 
@@ -509,7 +537,7 @@ def compact_pages(caches, block_size, block_table, seq_lens, ref_counts, page_ma
     """Move the live pages into the lowest page ids, in every cache, and rename
     them in the tables.  Returns page_map int32 [num_blocks]: the new id of
     each page, -1 for free ones."""
-    pc, _keep, nb, dev = _page_caches(caches)
+    pc, sets, _keep, nb, dev = _page_caches(caches)
     ps, dev = _page_state(block_size, block_table, seq_lens, ref_counts, dev)
     if nb != ref_counts.numel():
         raise ValueError("ref_counts must hold one count per page of the caches")
@@ -523,6 +551,6 @@ def compact_pages(caches, block_size, block_table, seq_lens, ref_counts, page_ma
         raise ValueError("page_map must hold one entry per page")
     lib = _load()
     ws, nbytes = _scratch(workspace, lib.gcache_pages_workspace_bytes(nb, ps.num_rows, 0), dev)
-    _check(lib.gcache_compact_pages(C.byref(ps), C.byref(pc), page_map.data_ptr(), _ptr(ws), nbytes,
-                                    _raw_stream(dev.index)), "gcache_compact_pages")
+    _check(lib.gcache_compact_page_sets(C.byref(ps), pc, sets, page_map.data_ptr(), _ptr(ws), nbytes,
+                                        _raw_stream(dev.index)), "gcache_compact_pages")
     return page_map

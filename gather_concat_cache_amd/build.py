@@ -30,7 +30,7 @@ BENCH_SOURCES = ["bench_ceiling.hip"]
 HEADERS = ["gcache_device.h", "gcache_internal.h"]
 OPERATOR_HEADERS = ["gcache_operators.h", "attention_device.h", "attention_join.h", "attention_few.h", "attention_tiles.h",
                     "fp8_scale.h"]
-PUBLIC_HEADERS = ["gcache.h", "gcache_attention.h", "gcache_fp8_kv.h", "gcache_prompt.h", "gcache_pages.h"]
+PUBLIC_HEADERS = ["gcache.h", "gcache_attention.h", "gcache_fp8_kv.h", "gcache_prompt.h", "gcache_pages.h", "gcache_page_sets.h"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

@@ -1,6 +1,6 @@
 // operators_abi.hip -- the extern "C" entry points of gcache_attention.h,
-// gcache_fp8_kv.h, gcache_prompt.h and gcache_pages.h: host checks, then one
-// short sequence of launches on the caller's stream.  Nothing here allocates,
+// gcache_fp8_kv.h, gcache_prompt.h, gcache_pages.h and gcache_page_sets.h: host
+// checks, then one short sequence of launches on the caller's stream.  Nothing here allocates,
 // frees or synchronizes.
 #include <algorithm>
 #include <atomic>
@@ -10,6 +10,7 @@
 
 #include "../../include/gcache_attention.h"
 #include "../../include/gcache_fp8_kv.h"
+#include "../../include/gcache_page_sets.h"
 #include "../../include/gcache_pages.h"
 #include "../../include/gcache_prompt.h"
 #include "gcache_operators.h"
@@ -244,6 +245,16 @@ int check_caches(const gcache_page_caches* c, int64_t num_blocks) {
     return GCACHE_OK;
 }
 
+int check_sets(const gcache_page_caches* sets, int32_t num_sets, int64_t num_blocks) {
+    if (num_sets < 0) return GCACHE_ERR_SHAPE;
+    if (num_sets > 0 && !sets) return GCACHE_ERR_NULL;
+    for (int i = 0; i < num_sets; i++)
+        if (const int rc = check_caches(sets + i, num_blocks)) return rc;
+    return GCACHE_OK;
+}
+// Caches of a set that have bytes to move.
+int moved_caches(const gcache_page_caches& c) { return c.page_bytes > 0 ? c.num_caches : 0; }
+
 // The caches from `at` on that one launch carries.
 CacheList cache_list(const gcache_page_caches* c, int64_t num_blocks, int at) {
     CacheList l;
@@ -253,6 +264,21 @@ CacheList cache_list(const gcache_page_caches* c, int64_t num_blocks, int at) {
     l.block_stride = c->block_stride;
     l.page_bytes = c->page_bytes;
     return l;
+}
+
+// run(list, first, last) for each launch's caches, of all sets.
+template <typename Run>
+void each_list(const gcache_page_caches* sets, int32_t num_sets, int64_t num_blocks, Run run) {
+    int64_t left = 0, done = 0;
+    for (int i = 0; i < num_sets; i++) left += moved_caches(sets[i]);
+    for (int i = 0; i < num_sets; i++) {
+        const int n = moved_caches(sets[i]);
+        for (int at = 0; at < n; at += kMaxCaches) {
+            const CacheList l = cache_list(sets + i, num_blocks, at);
+            run(l, done == 0, done + l.n == left);
+            done += l.n;
+        }
+    }
 }
 
 int grant_params(const PageTable& t, const int32_t* a, const int32_t* b, int64_t n, int32_t* status, void* ws,
@@ -603,37 +629,54 @@ int64_t gcache_pages_workspace_bytes(int64_t num_blocks, int32_t num_rows, int64
 
 int gcache_copy_pages(const gcache_page_caches* caches, int64_t num_blocks, const int32_t* src, const int32_t* dst,
                       int64_t num_pairs, hipStream_t stream) {
+    return gcache_copy_page_sets(caches, 1, num_blocks, src, dst, num_pairs, stream);
+}
+
+int gcache_copy_page_sets(const gcache_page_caches* sets, int32_t num_sets, int64_t num_blocks, const int32_t* src,
+                          const int32_t* dst, int64_t num_pairs, hipStream_t stream) {
     if (num_pairs < 0 || num_pairs > kMaxRequests || num_blocks < 0 || num_blocks > INT32_MAX) return GCACHE_ERR_SHAPE;
-    int rc = check_caches(caches, num_blocks);
+    int rc = check_sets(sets, num_sets, num_blocks);
     if (rc) return rc;
-    if (num_pairs == 0 || caches->num_caches == 0 || caches->page_bytes == 0 || num_blocks == 0) return GCACHE_OK;
+    bool any = false;
+    for (int i = 0; i < num_sets; i++) any = any || moved_caches(sets[i]) > 0;
+    if (num_pairs == 0 || !any || num_blocks == 0) return GCACHE_OK;
     if (!src || !dst) return GCACHE_ERR_NULL;
     if (!aligned(src, 4) || !aligned(dst, 4)) return GCACHE_ERR_ALIGN;
     if ((rc = check_device())) return rc;
-    for (int at = 0; at < caches->num_caches; at += kMaxCaches) {
-        const hipError_t e = launch_copy_pages(cache_list(caches, num_blocks, at), src, dst, num_pairs, stream, at == 0,
-                                               at + kMaxCaches >= caches->num_caches);
-        if (e != hipSuccess) return GCACHE_ERR_LAUNCH;
-    }
-    return GCACHE_OK;
+    hipError_t e = hipSuccess;
+    each_list(sets, num_sets, num_blocks, [&](const CacheList& l, bool first, bool last) {
+        if (e == hipSuccess) e = launch_copy_pages(l, src, dst, num_pairs, stream, first, last);
+    });
+    return launched(e);
 }
 
 int gcache_fork_requests(const gcache_page_state* state, const gcache_page_caches* caches, const int32_t* parent_rows,
                          const int32_t* child_rows, int64_t num_forks, int32_t* status, void* workspace,
                          int64_t workspace_bytes, hipStream_t stream) {
+    return gcache_fork_page_sets(state, caches, 1, parent_rows, child_rows, num_forks, status, workspace, workspace_bytes,
+                                 stream);
+}
+
+int gcache_fork_page_sets(const gcache_page_state* state, const gcache_page_caches* sets, int32_t num_sets,
+                          const int32_t* parent_rows, const int32_t* child_rows, int64_t num_forks, int32_t* status,
+                          void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     if (num_forks < 0) return GCACHE_ERR_SHAPE;
     PageTable t;
     int rc = check_state(state, &t);
     if (rc) return rc;
-    if ((rc = check_caches(caches, t.num_blocks))) return rc;
+    if ((rc = check_sets(sets, num_sets, t.num_blocks))) return rc;
     if (num_forks == 0) return GCACHE_OK;
     GrantParams g;
     if ((rc = grant_params(t, parent_rows, child_rows, num_forks, status, workspace, workspace_bytes, &g))) return rc;
     if ((rc = check_device())) return rc;
     hipError_t e = launch_fork_plan(g, stream);
-    const int n = caches->page_bytes > 0 ? caches->num_caches : 0;
-    for (int at = 0; (at < n || at == 0) && e == hipSuccess; at += kMaxCaches)
-        e = launch_fork_apply(g, cache_list(caches, n ? t.num_blocks : 0, at), at == 0, stream, at + kMaxCaches >= n);
+    // the first launch does the rows too, also where no cache has bytes to move
+    bool rows = true;
+    each_list(sets, num_sets, t.num_blocks, [&](const CacheList& l, bool first, bool last) {
+        rows = false;
+        if (e == hipSuccess) e = launch_fork_apply(g, l, first, stream, last);
+    });
+    if (rows && e == hipSuccess) e = launch_fork_apply(g, CacheList{}, true, stream, true);
     return launched(e);
 }
 
@@ -666,10 +709,15 @@ int gcache_free_requests(const gcache_page_state* state, const int32_t* rows, in
 
 int gcache_compact_pages(const gcache_page_state* state, const gcache_page_caches* caches, int32_t* page_map,
                          void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+    return gcache_compact_page_sets(state, caches, 1, page_map, workspace, workspace_bytes, stream);
+}
+
+int gcache_compact_page_sets(const gcache_page_state* state, const gcache_page_caches* sets, int32_t num_sets,
+                             int32_t* page_map, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     PageTable t;
     int rc = check_state(state, &t);
     if (rc) return rc;
-    if ((rc = check_caches(caches, t.num_blocks))) return rc;
+    if ((rc = check_sets(sets, num_sets, t.num_blocks))) return rc;
     if (!page_map || !workspace) return GCACHE_ERR_NULL;
     if (workspace_bytes < gcache_pages_workspace_bytes(t.num_blocks, t.num_rows, 0)) return GCACHE_ERR_SHAPE;
     if (!aligned(page_map, 4) || !aligned(workspace, 4)) return GCACHE_ERR_ALIGN;
@@ -678,9 +726,9 @@ int gcache_compact_pages(const gcache_page_state* state, const gcache_page_cache
     const int64_t groups = t.num_blocks / kCompactIds + 1;
     CompactParams c{t, page_map, w, w + groups, w + groups + t.num_blocks, w + groups + 2 * (int64_t)t.num_blocks};
     hipError_t e = launch_compact_plan(c, stream);
-    const int n = caches->page_bytes > 0 ? caches->num_caches : 0;
-    for (int at = 0; at < n && e == hipSuccess; at += kMaxCaches)
-        e = launch_compact_move(c, cache_list(caches, t.num_blocks, at), stream);
+    each_list(sets, num_sets, t.num_blocks, [&](const CacheList& l, bool, bool) {
+        if (e == hipSuccess) e = launch_compact_move(c, l, stream);
+    });
     if (e == hipSuccess) e = launch_compact_finish(c, stream);
     return launched(e);
 }

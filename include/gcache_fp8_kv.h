@@ -16,6 +16,10 @@
  *                 + head * scale_head_stride],      side 0: keys, 1: values.
  * A scale counts as the nearest number within 2^-100 .. 2^121 (what is not a
  * positive number as 2^-100).
+ * A page is its codes and its scales: what copies, forks or compacts pages has to
+ * move both (gcache_page_sets.h, with a set for kv_cache and one for kv_scales),
+ * or the scales lie within the page's bytes: kv_scales = kv_cache + the bytes of a
+ * page's codes, scale_block_stride = block_stride / 4.
  */
 #ifndef GCACHE_FP8_KV_H
 #define GCACHE_FP8_KV_H

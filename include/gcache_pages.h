@@ -12,7 +12,8 @@
  *   caches       HOST array of num_caches device pointers (one cache a layer,
  *                any format), read during the call; all with the same
  *                num_blocks, block_stride and page_bytes (the bytes of a page
- *                that are copied, <= block_stride)
+ *                that are copied, <= block_stride); pages that lie in arrays of
+ *                several geometries go through gcache_page_sets.h
  * A page that a row fills only partly belongs to that row alone: a fork shares
  * the full pages and copies the partial one, so rows may append without
  * looking at counts.

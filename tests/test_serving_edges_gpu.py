@@ -6,9 +6,10 @@ import numpy as np
 import pytest
 import torch
 
+import operator_refs as pages_ref
 import serving_refs as ref
-from gpu_util import dev
-from test_operators_gpu import Batch, close
+from gpu_util import dev, host
+from test_operators_gpu import Batch, check_pages, close, random_state
 from test_serving_gpu import cache_view, g, random_codes  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -114,3 +115,102 @@ def test_cache_least_scales_alone(g, qlens):  # noqa: F811
     scales = np.full((batch.nb, 2, 1), 2.0 ** -9, np.float32)
     scales[:, 1] = (2.0 ** -rng.integers(96, 101, (batch.nb, 1))).astype(np.float32)
     check_scaled(g, batch, 1, 4, 64, codes, scales, rng.standard_normal((batch.T, 4, 64)), 0.125)
+
+
+# ---------------------------------------------------------------------------
+# pages of codes and scales
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("sizes", [[(96, np.uint8), (24, np.float32)], [(40, np.uint8), (7, np.uint8), (16, np.uint8)], [(3, np.float32)] * 2])
+@pytest.mark.parametrize("rows,nb,bs,stride", [(5, 20, 4, 6), (40, 200, 16, 9), (300, 3000, 1, 30)])
+def test_pages_of_several_geometries(g, sizes, rows, nb, bs, stride):  # noqa: F811
+    """Copies, forks and compactions of pages whose bytes lie in arrays of
+    different sizes and types, several of each, against the plain model."""
+    rng = np.random.default_rng(rows + len(sizes))
+    state = random_state(rng, rows, nb, bs, stride)
+    caches = [rng.integers(0, 100, (nb, n)).astype(t) for n, t in sizes + sizes[::-1]]
+    n = rows + 5
+    parents, children = (rng.integers(-2, rows + 2, n).astype(np.int32) for _ in range(2))
+    gpu = [dev(c) for c in caches]
+    src, dst = np.arange(nb, dtype=np.int32)[:nb // 2], np.arange(nb, dtype=np.int32)[nb // 2:][:nb // 2]
+    g.copy_pages(gpu, dev(src), dev(dst))
+    for c, x in zip(gpu, caches):
+        x[dst] = x[src]
+        assert np.array_equal(host(c), x)
+    state = check_pages(lambda t, l, r, c: g.fork_requests(c, bs, t, l, r, dev(parents), dev(children)),
+                        lambda t, l, r, c: pages_ref.fork(t, l, r, parents, children, bs, c), state, caches)
+    gone = rng.integers(-1, rows + 1, rows // 2).astype(np.int32)
+    state = check_pages(lambda t, l, r, c: g.free_requests(bs, t, l, r, dev(gone)),
+                        lambda t, l, r, c: pages_ref.free(t, l, r, gone, bs), state, caches)
+    check_pages(lambda t, l, r, c: g.compact_pages(c, bs, t, l, r), lambda t, l, r, c: pages_ref.compact(t, l, r, bs, c), state, caches)
+
+
+def test_pages_of_several_geometries_refusals(g):  # noqa: F811
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a, b = torch.zeros(4, 8, device="cuda"), torch.zeros(5, 16, device="cuda")
+    for bad in ([a, b], [a, torch.zeros(4, 16)], [a, torch.zeros(4, 16, device="cuda").expand(2, 4, 16)[0], b[:4].t().contiguous().t()], []):
+        with pytest.raises(ValueError):
+            g.copy_pages(bad, i, i)
+
+
+@pytest.mark.parametrize("inside", [False, True])
+def test_cache_pages_fork_and_compact(g, inside):  # noqa: F811
+    """Forked and compacted pages of the 8-bit cache keep their values, with the
+    scales as a second array or inside the pages; the fork's appends leave its
+    parent alone; all of it in a captured graph too."""
+    rng = np.random.default_rng(41)
+    hq, hk, hs, bs, nb = 4, 2, 64, 16, 24
+    codes = 2 * bs * hk * hs
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    if inside:
+        pool = torch.full((nb, codes + 16 * hk), 0xFF, dtype=torch.uint8, device="cuda")
+        cache = pool[:, :codes].unflatten(1, (2, bs, hk, hs))
+        scales = pool[:, codes:codes + 8 * hk].view(torch.float32).unflatten(1, (2, hk))
+        moved = pool
+    else:
+        cache = torch.full((nb, 2, bs, hk, hs), 0xFF, dtype=torch.uint8, device="cuda")
+        scales = torch.full((nb, 2, hk), float("nan"), device="cuda")
+        moved = [cache, scales]
+    table = torch.full((4, 6), -1, dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(nb, dtype=torch.int32, device="cuda")
+    state = (bs, table, lens, refs)
+
+    def append(row, n, size):
+        old = int(lens[row])
+        assert int(g.extend_requests(*state, i32(row), i32(old + n))) == 1
+        k, v = (ref.bf16(size * rng.standard_normal((n, hk, hs)))[0].cuda() for _ in range(2))
+        g.rope_append_fp8_kv(None, k, v, cache, scales, table[row:row + 1], i32(0, n), lens[row:row + 1], None)
+
+    q = ref.bf16(rng.standard_normal((1, hq, hs)))[0].cuda()
+
+    def attend(row):
+        return g.attention_fp8_kv(q, cache, scales, table[row:row + 1], i32(0, 1), lens[row:row + 1], 96, 0.125, return_lse=True)
+
+    append(3, 40, 1.0)                                       # to be freed: a hole
+    append(0, 37, 5.0)
+    want = attend(0)
+    assert g.fork_requests(moved, *state, i32(0, 0), i32(1, 2)).tolist() == [1, 1]
+    for row in (1, 2):
+        assert all(torch.equal(a, b) for a, b in zip(attend(row), want))
+    append(1, 3, 100.0)                                      # the fork's partial page gets scales of its own
+    forked = attend(1)
+    assert not torch.equal(forked[0], want[0])
+    for row in (0, 2):
+        assert all(torch.equal(a, b) for a, b in zip(attend(row), want))
+    g.free_requests(*state, i32(3))
+    before = [x.clone() for x in (cache, scales, table, lens, refs)]
+    g.compact_pages(moved, *state)
+    for row, w in ((0, want), (1, forked), (2, want)):
+        assert all(torch.equal(a, b) for a, b in zip(attend(row), w))
+    after = [x.clone() for x in (cache, scales, table, lens, refs)]
+    assert int(table.max()) < int(before[2].max())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.compact_pages(moved, *state)
+    for _ in range(3):
+        for x, y in zip((cache, scales, table, lens, refs), before):
+            x.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(table, after[2]) and torch.equal(refs, after[4])
+        live = refs > 0
+        assert torch.equal(cache[live], after[0][live]) and torch.equal(scales[live], after[1][live])
