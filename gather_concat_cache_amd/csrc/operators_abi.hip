@@ -446,7 +446,7 @@ int gcache_rope_append_fp8_kv(const gcache_append_args* a, void* kv_cache, float
         if (sides[i] && !rows_apart(a->num_tokens, i == 3 ? a->num_q_heads : a->num_kv_heads, st[2 * i], st[2 * i + 1], a->head_size))
             return GCACHE_ERR_SHAPE;
     if (!aligned(a->query_starts, 4) || !aligned(a->seq_lens, 4) || !aligned(a->block_table, 4) ||
-        !aligned(a->positions, 8) || !aligned(a->cos_sin, a->cos_sin_bf16 ? 2 : 4))
+        (a->rot > 0 && (!aligned(a->positions, 8) || !aligned(a->cos_sin, a->cos_sin_bf16 ? 2 : 4))))
         return GCACHE_ERR_ALIGN;
     int rc = check_fp8_layout(L, kv_cache, kv_scales, a->num_blocks, true, a->num_kv_heads, a->head_size, a->block_size);
     if (rc) return rc;
@@ -481,8 +481,8 @@ int gcache_rope_append_fp8_kv(const gcache_append_args* a, void* kv_cache, float
     p.block_table = a->block_table;
     p.bt_stride = a->block_table_stride;
     p.num_blocks = a->num_blocks;
-    p.positions = a->positions;
-    p.cos_sin = a->cos_sin;
+    p.positions = a->rot > 0 ? a->positions : nullptr;   // (without a rotation neither is read)
+    p.cos_sin = a->rot > 0 ? a->cos_sin : nullptr;
     p.max_pos = a->max_position;
     p.cs_stride = a->cos_sin_stride;
     p.cs_bf16 = a->cos_sin_bf16 != 0;

@@ -55,3 +55,19 @@ def test_page_set_refusals(lib):  # noqa: F811
         assert f(sets(), -1) == -2 and f(None, 1) == -1
     assert fork(sets(), 2, 0) == 0 and copy(sets(), 2, 0) == 0 and copy(None, 0) == 0
     assert copy(sets(page_bytes=0), 0) == 0
+
+
+# ---------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------
+def test_append_without_rotation_looks_at_no_table(lib):  # noqa: F811
+    """rot 0: positions and cos_sin may be anything.  The calls are refused for
+    their layout, which is checked behind the pointers."""
+    from gather_concat_cache_amd._serving import AppendArgs, Fp8KvLayout
+    bad = Fp8KvLayout(**{**LAYOUT, "block_stride": 1 << 62})
+    for change in (dict(positions=A16 + 4), dict(cos_sin=A16 + 2), dict(cos_sin=A16 + 1, cos_sin_bf16=1, max_position=-1, cos_sin_stride=-5)):
+        a = AppendArgs(**{**APPEND, "rot": 0, **change})
+        assert lib.gcache_rope_append_fp8_kv(C.byref(a), A16, A16, C.byref(bad), None) == -2, change
+        if "max_position" not in change:
+            a.rot = 16
+            assert lib.gcache_rope_append_fp8_kv(C.byref(a), A16, A16, C.byref(bad), None) == -3, change
