@@ -46,11 +46,11 @@ __device__ __forceinline__ void load_lds(uint32_t lds, const void* base, uint32_
     const uint64_t s = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 |
                        (uint32_t)__builtin_amdgcn_readfirstlane((int)b);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 : : "s"(lds), "v"(offset), "s"(s) : "memory");
+                 : : "s"(lds), "v"(offset), "s"(s) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds(uint32_t lds, const void* lane_address) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                 : : "s"(lds), "v"(lane_address) : "memory");
+                 : : "s"(lds), "v"(lane_address) : "memory", "m0");
 }
 // Every wave's loads have landed and every wave's reads are done.
 __device__ __forceinline__ void tile_ready() {

@@ -71,3 +71,19 @@ def test_append_without_rotation_looks_at_no_table(lib):  # noqa: F811
         if "max_position" not in change:
             a.rot = 16
             assert lib.gcache_rope_append_fp8_kv(C.byref(a), A16, A16, C.byref(bad), None) == -3, change
+
+
+# ---------------------------------------------------------------------------
+# inline assembly
+# ---------------------------------------------------------------------------
+def test_assembly_that_writes_m0_says_so():
+    """The compiler keeps values in m0 over a statement that does not name it."""
+    import glob
+    import re
+    found = 0
+    for path in glob.glob(os.path.join(ROOT, "gather_concat_cache_amd", "csrc", "*.h*")):
+        for asm in re.findall(r"\basm\b[^;]*?\((.*?)\);", open(path).read(), flags=re.S):
+            if re.search(r"s_mov_b32 m0", asm):
+                found += 1
+                assert '"m0"' in asm.split(":")[-1], (path, asm)
+    assert found
