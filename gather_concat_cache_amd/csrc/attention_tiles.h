@@ -441,13 +441,15 @@ __device__ __forceinline__ uint32_t drop_nonfinite(RawFrag<PagedFp8>& r) {
     r.w.y = drop_nan_e4m3x4(x.y);
     return (r.w.x ^ x.x) | (r.w.y ^ x.y);
 }
-// What is not finite as bf16's largest value, the rest as 0.
-__device__ __forceinline__ void keep_nonfinite(RawFrag<PackedBf16>& r) {
+// What is NaN or an infinity of one sign (0 or 0x8000) as bf16's largest value of
+// that sign, the rest as 0.
+__device__ __forceinline__ uint32_t keep_nonfinite(uint32_t x, uint32_t sign) {      // a value in the lower half
+    const bool keep = (x & 0x7F80u) == 0x7F80u && ((x & 0x7Fu) != 0 || (x & 0x8000u) == sign);
+    return keep ? 0x7F7Fu | sign : 0u;
+}
+__device__ __forceinline__ void keep_nonfinite(RawFrag<PackedBf16>& r, uint32_t sign) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const uint32_t x = r.w[i];
-        r.w[i] = ((x & 0x7F80u) == 0x7F80u ? 0x7F7Fu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0x7F7F0000u : 0u);
-    }
+    for (int i = 0; i < 4; i++) r.w[i] = keep_nonfinite(r.w[i] & 0xFFFFu, sign) | keep_nonfinite(r.w[i] >> 16, sign) << 16;
 }
 
 // row_end for weights shifted by T's shift (row_lse takes kShift off).
@@ -761,17 +763,19 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                 odd |= drop_nonfinite(x);
                 add(n, operand(x));
             }, side);
-            // rows that do see a value that is not finite get an infinity in its dim (the sum is not finite there), the
-            // product of two large values
+            // rows that do see a value that is not finite get it in its dim: an infinity as the product of two large
+            // values, a NaN as one of each sign (in two passes: of one instruction's products the large ones might cancel)
             if constexpr (!FP8) {
                 if (__any(odd != 0)) {
 #pragma unroll
                     for (int j = 0; j < 32; j++)
                         pw[j >> 3][j & 7] = (__bf16)(s[j >> 4][j & 15] != kNegInf ? 0x1p100f : 0.0f);
-                    stream<4 * DT, 2, false, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
-                        keep_nonfinite(x);
-                        add(n, operand(x));
-                    }, [](int) {});
+#pragma unroll 1
+                    for (uint32_t sign = 0; sign <= 0x8000u; sign += 0x8000u)
+                        stream<4 * DT, 2, false, RawFrag<T>>(load_v, [&](int n, RawFrag<T> x) {
+                            keep_nonfinite(x, sign);
+                            add(n, operand(x));
+                        }, [](int) {});
                 }
             }
         }

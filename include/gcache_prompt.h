@@ -32,7 +32,9 @@ extern "C" {
  *   of its keys) and get the attention over both; a part whose lse is -infinity
  *   does not count, whatever its row holds.
  * Keys and values that a row does not see cannot reach it, infinities and NaN
- * among them; a row that sees a value that is not finite gets one.
+ * among them; a row that sees a value that is not finite gets one in its dim (the
+ * infinity, or a NaN where it sees a NaN, infinities of both signs, or one whose
+ * weight is 0 in binary32), and one that sees a NaN key NaNs in all.
  * Rows outside [query_starts[0], query_starts[batch]) are left as they were.
  * query_starts and key_starts must be non-decreasing (values are clamped to
  * [0, total_q] and [0, total_k]; otherwise rows belong to unspecified requests).

@@ -214,3 +214,84 @@ def test_cache_pages_fork_and_compact(g, inside):  # noqa: F811
         assert torch.equal(table, after[2]) and torch.equal(refs, after[4])
         live = refs > 0
         assert torch.equal(cache[live], after[0][live]) and torch.equal(scales[live], after[1][live])
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite, in every form of the prompt kernel
+# ---------------------------------------------------------------------------
+def seen_specials(see, v):
+    """What the weighted sum of each row and dim is where it sees values that are
+    not finite (positive weights): +-infinity, or NaN of a NaN or of both."""
+    up, down, nan = ((see.astype(float) @ x.astype(float)) > 0 for x in (v == np.inf, v == -np.inf, np.isnan(v)))
+    some = up | down | nan
+    return some, np.where(nan | (up & down), np.nan, np.where(up, np.inf, -np.inf))
+
+
+FORMS = [(128, 128), (64, 64), (192, 128), (256, 256), (80, 80), (200, 136), (40, 64)]
+
+
+@pytest.mark.parametrize("dk,dv", FORMS)
+@pytest.mark.parametrize("qlens,klens,kw", [
+    ([64, 40, 30], [64, 40, 30], {}), ([64, 40, 30], [64, 40, 30], dict(window=7, num_sinks=1)), ([90, 9], [70, 130], dict(causal=False)),
+    ([3, 40], [2100, 900], {}), ([3, 40], [2100, 900], dict(causal=False)), ([33, 20], [64, 50], dict(accumulate=True)),
+    ([3, 40], [2100, 900], dict(accumulate=True)),
+])
+def test_prompt_values_that_are_not_finite(g, dk, dv, qlens, klens, kw):  # noqa: F811
+    """Rows that see an infinity get it with its sign, those that see a NaN or
+    both signs a NaN, and no other row or dim changes; lse counts them as any
+    key.  Keys split, joined with an earlier part, and behind a window."""
+    rng = np.random.default_rng(dk + dv + sum(klens))
+    hk, group, hq = 2, 2, 4
+    qs, ks = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (qlens, klens))
+    q, k = (ref.bf16(0.5 * rng.standard_normal((n, h, dk)))[0].cuda() for n, h in ((qs[-1], hq), (ks[-1], hk)))
+    v, v64 = ref.bf16(rng.standard_normal((ks[-1], hk, dv)))
+    kw = dict(kw)
+    accumulate = kw.pop("accumulate", False)
+    if accumulate:
+        kw["causal"] = False
+        old = ref.bf16(rng.standard_normal((qs[-1], hq, dv)))[0].cuda(), torch.zeros(int(qs[-1]), hq, device="cuda")
+
+    def call(v):
+        more = dict(out=old[0].clone(), lse=old[1].clone(), accumulate=True) if accumulate else {}
+        return g.prompt_attention(q, k, v, dev(qs), dev(ks), max(klens), dk ** -0.5, return_lse=True, **kw, **more)
+
+    want, want_lse = (x.double().cpu().numpy() for x in call(v.cuda()))
+    for values in ((-np.inf,), (np.inf,), (np.nan,), (np.inf, -np.inf, np.nan)):
+        x = v.clone()
+        for at in rng.integers(0, ks[-1], 6):
+            x[int(at), int(rng.integers(hk)), int(rng.integers(dv))] = float(rng.choice(values))
+        for b in range(len(klens)):                          # where some rows see it, others not
+            x[int(ks[b]) + klens[b] - qlens[b] // 2 - 1, b % hk, 3 + b] = float(values[-1])
+            x[int(ks[b]) + klens[b] - qlens[b] // 2, b % hk, 3 + b] = float(values[0])
+        x64 = x.double().numpy()
+        out, lse = (y.double().cpu().numpy() for y in call(x.cuda()))
+        for b, (n, m) in enumerate(zip(qlens, klens)):
+            see = ref.causal(n, m, kw.get("window"), kw.get("num_sinks", 0)) if kw.get("causal", True) else np.ones((n, m), bool)
+            rows, keys = slice(qs[b], qs[b + 1]), slice(ks[b], ks[b + 1])
+            for h in range(hq):
+                some, what = seen_specials(see, x64[keys, h // group])
+                got = out[rows, h]
+                assert np.array_equal(got[some], what[some], equal_nan=True), (values, b, h)
+                # a finite sum elsewhere: two calls differ by their roundings of weights (2^-8, where the tile is computed
+                # another way) and of the output
+                near = 2.0 ** -6 * (np.abs(want[rows, h]) + 1)
+                close(got[~some], want[rows, h][~some], near[~some], f"{values} request {b} head {h}")
+        close(lse, want_lse, 1e-5 * (np.abs(np.where(np.isfinite(want_lse), want_lse, 0)) + 1), f"{values} lse")
+
+
+def test_prompt_rows_that_see_a_nan(g):  # noqa: F811
+    """A NaN row of keys or values reaches every dim of every row that sees it."""
+    rng = np.random.default_rng(9)
+    for dk, dv in FORMS:
+        q, k, v = (ref.bf16(rng.standard_normal((70, 2, d)))[0].cuda() for d in (dk, dk, dv))
+        starts = dev(np.array([0, 40, 70], np.int32))
+        want, lse = g.prompt_attention(q, k, v, starts, starts, 40, dk ** -0.5, return_lse=True)
+        see = torch.zeros(70, dtype=torch.bool, device="cuda")
+        see[30:40] = True
+        for x in (k, v):
+            y = x.clone()
+            y[30] = float("nan")
+            got, got_lse = g.prompt_attention(q, y if x is k else k, y if x is v else v, starts, starts, 40, dk ** -0.5, return_lse=True)
+            assert torch.isnan(got[see]).all() and torch.equal(got[~see], want[~see]), (dk, dv)
+            assert torch.isnan(got_lse[see]).all() if x is k else torch.equal(got_lse, lse), (dk, dv)
+            assert torch.equal(got_lse[~see], lse[~see])
