@@ -132,6 +132,8 @@ def rope_append_fp8_kv(q, k, v, kv_cache, kv_scales, block_table, query_starts, 
         with _on(dev, stream):
             return rope_append_fp8_kv(q, k, v, kv_cache, kv_scales, block_table, query_starts, seq_lens, cos_sin, positions,
                                       interleaved, q_out, k_out, return_k)
+    if hk == 0:
+        raise ValueError("the cache must have heads")
     ks = _head_rows(k, "k", dev, None, hk, hs)
     T = k.shape[0]
     vs = _head_rows(v, "v", dev, T, hk, hs)
@@ -178,7 +180,7 @@ def rope_append_fp8_kv(q, k, v, kv_cache, kv_scales, block_table, query_starts, 
         pos_ptr = positions.data_ptr()
     if T > _INT32_MAX or B > _INT32_MAX or hq > _INT32_MAX:
         raise ValueError("tokens, requests and heads must be within int32")
-    if T and B and hk:
+    if T and B:
         a = AppendArgs(q_ptr if hq else None, k.data_ptr(), v.data_ptr(), qo_ptr if hq else None, _ptr(k_out), *qs, *ks, *vs,
                        *qos, *kos, query_starts.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
                        block_table.shape[1], pos_ptr, cs_ptr, max_pos, cs_stride, T, nb, B, hq, hk, hs, bs, rot,

@@ -295,3 +295,15 @@ def test_prompt_rows_that_see_a_nan(g):  # noqa: F811
             assert torch.isnan(got[see]).all() and torch.equal(got[~see], want[~see]), (dk, dv)
             assert torch.isnan(got_lse[see]).all() if x is k else torch.equal(got_lse, lse), (dk, dv)
             assert torch.equal(got_lse[~see], lse[~see])
+
+
+# ---------------------------------------------------------------------------
+# refusals
+# ---------------------------------------------------------------------------
+def test_append_refuses_a_cache_without_heads(g):  # noqa: F811
+    """No kernel would write the queries that the call returns."""
+    x = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    cache, scales = x(3, 2, 16, 0, 64, t=torch.uint8), x(3, 2, 0, t=torch.float32)
+    with pytest.raises(ValueError):
+        g.rope_append_fp8_kv(x(5, 4, 64), x(5, 0, 64), x(5, 0, 64), cache, scales, x(1, 4, t=torch.int32), x(2, t=torch.int32),
+                             x(1, t=torch.int32), None)
