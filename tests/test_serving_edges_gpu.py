@@ -10,7 +10,7 @@ import operator_refs as pages_ref
 import serving_refs as ref
 from gpu_util import dev, host
 from test_operators_gpu import Batch, check_pages, close, random_state
-from test_serving_gpu import cache_view, g, random_codes  # noqa: F401
+from test_serving_gpu import cache_view, check_cache, g, random_codes  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -307,3 +307,38 @@ def test_append_refuses_a_cache_without_heads(g):  # noqa: F811
     with pytest.raises(ValueError):
         g.rope_append_fp8_kv(x(5, 4, 64), x(5, 0, 64), x(5, 0, 64), cache, scales, x(1, 4, t=torch.int32), x(2, t=torch.int32),
                              x(1, t=torch.int32), None)
+
+
+# ---------------------------------------------------------------------------
+# every form that a call's sizes select
+# ---------------------------------------------------------------------------
+FORM_CASES = [  # rows of a tile, query lengths, lengths, group, head size
+    (16, [1, 2, 1], [60, 45, 300], 4, 64), (16, [1, 2, 1], [60, 45, 300], 4, 128), (16, [5, 9, 2], [60, 45, 300], 2, 256),
+    (32, [4, 7, 3], [60, 45, 300], 4, 64), (32, [4, 7, 3], [60, 45, 300], 4, 128), (32, [4, 7, 3], [60, 45, 300], 4, 96),
+    (128, [33, 9, 70], [60, 9, 200], 2, 64), (128, [33, 9, 70], [60, 9, 200], 4, 256), (128, [33, 9, 70], [60, 9, 200], 2, 176),
+    (128, [33, 9, 140], [60, 9, 900], 2, 256), (128, [33, 9, 70], [60, 9, 200], 4, 128), (128, [33, 9, 70], [60, 9, 200], 4, 80),
+]
+
+
+@pytest.mark.parametrize("kind", ["causal", "window", "tree"])
+@pytest.mark.parametrize("bs", [16, 24])
+@pytest.mark.parametrize("rows,qlens,lens,group,hs", FORM_CASES)
+def test_cache_every_form(g, rows, qlens, lens, group, hs, bs, kind):  # noqa: F811
+    """Both kernels at all their head sizes, over whole pages and others, causal,
+    behind a window and with a tree mask."""
+    rng = np.random.default_rng(rows + hs + bs)
+    batch = Batch(rng, qlens, lens, bs)
+    assert rows_kernel(batch.T + 2, len(qlens), group, hs) == rows
+    mask = None
+    if kind == "tree":
+        mask = rng.random((batch.T, max(qlens))) < 0.4
+        mask[int(batch.starts[1]) + 1] = False               # a row that sees its context alone, if there is any
+    w, s = (40, 6) if kind == "window" else (None, 0)
+    check_cache(g, rng, batch, 2, group, hs, "nhd", w, s, mask=mask)
+
+
+def test_cache_every_form_is_there():
+    """All head sizes of both kernels are among the cases above."""
+    padded = lambda hs: 64 if hs <= 64 else 128 if hs <= 128 else 256  # noqa: E731
+    assert {(r, padded(hs)) for r, _, _, _, hs in FORM_CASES} == {(16, 64), (16, 128), (16, 256), (32, 64), (32, 128), (128, 64), (128, 128),
+                                                                  (128, 256)}
