@@ -599,8 +599,13 @@ int gcache_prompt_attention(const gcache_prompt_args* a, hipStream_t stream) {
     p.causal = a->causal != 0;
     p.accumulate = a->accumulate != 0;
     p.div = make_div(1);
-    // Chunks of context whose lengths are near the longest: 3 of 5264 to 7222 keys, 2784 queries of 16 heads, take 215 us
-    // without a split against 239 with the one that batches of unknown lengths get.
+    // Chunks of context whose mean is at least 3/4 of the longest are split as if all were alike.  Against the split that
+    // batches of unknown lengths get, us, 192 / 128 dims: 176 and 256 row tiles over 2048 keys 52 and 53 against 57 and
+    // 66, 272 and 336 over 4096 121 and 130 against 125 and 139, 224 and 256 over 16384 301 and 328 against 313 and 339, 384
+    // over 8192 268 against 290; 128 dims, 336 over 4096 105 against 121, 480 and 512 alike.  Lengths that differ, 384
+    // tiles: 7200, 5800 and 5400 keys 222 against 240; twice 8192 and 2048 225 against 237; but one of three long, 8192 and
+    // twice 5120 241 against 235, and 128 dims, 4096, 2500 and 2900 100 against 93.  The lengths are on the device, so the
+    // host cannot tell the last two from the others.
     const bool even = !a->causal && a->max_key_len <= 4 * a->total_k / (3 * (int64_t)a->batch_size);
     const AttnPlan plan = plan_attention_prompt(p.total_q, p.batch, p.hq, p.hk, p.dk, p.hs, a->max_key_len, p.window, p.sinks,
                                                 workspace_floats(a->workspace, a->workspace_bytes), even);
