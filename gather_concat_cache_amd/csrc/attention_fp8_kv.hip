@@ -299,14 +299,15 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
                 const bool now = apart.value && (far || __any(odd));
 #pragma unroll
                 for (int r = 0; r < R; r++) {
+                    FarSum fs{m[r], l[r]};               // (before a large scale's m flushes l; l holds the tiles before)
                     const float mn = fmaxf(m[r], top[r]);
                     const float al = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[r] - mn);
                     m[r] = mn;
                     l[r] *= al;
 #pragma unroll
                     for (int d = 0; d < DT; d++) o[r][d] *= al;
-                    if (now) {                               // (l holds the tiles before this one)
-                        FarSum fs = far ? s_far[w][r][lane] : FarSum{m[r], l[r]};
+                    if (now) {
+                        if (far) fs = s_far[w][r][lane];
                         const auto logit = [&](int j) { return s[r][j >> 2][j & 3] + __builtin_log2f(inv[UNI ? j >> 2 : j]); };
                         float most = kNegInf;
 #pragma unroll

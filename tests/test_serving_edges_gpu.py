@@ -107,6 +107,24 @@ def test_cache_scales_over_their_range(g, qlens, group, hs, bs, kind):  # noqa: 
         check_scaled(g, batch, 2, group, hs, codes, scales, q, hs ** -0.5, w, s, mask, ws)
 
 
+@pytest.mark.parametrize("order", ["rising", "falling"])
+@pytest.mark.parametrize("qlen,bs", [(1, 16), (1, 24), (4, 64), (8, 16), (8, 24), (40, 16), (40, 24)])
+def test_cache_scales_in_order(g, qlen, bs, order):  # noqa: F811
+    """Value scales that rise or fall page by page from one end of their range to
+    the other: no jump loses the sum of the pages before it."""
+    rng = np.random.default_rng(bs + qlen)
+    batch = Batch(rng, [qlen], [700], bs)
+    codes = random_codes(rng, (batch.nb, 2, bs, 1, 64))
+    scales = np.full((batch.nb, 2, 1), 2.0 ** -9, np.float32)
+    pages = -(-700 // bs)
+    for ends in ((-100, 110), (-39, 110), (-39, 20)):
+        steps = np.array([ends[0], ends[1]])[(np.arange(pages) >= pages // 2).astype(int)], np.linspace(*ends, pages)
+        for step in steps:
+            scales[batch.table[0, :pages], 1, 0] = 2.0 ** (step if order == "rising" else step[::-1])
+            check_scaled(g, batch, 1, 4, 64, codes, scales, rng.standard_normal((qlen, 4, 64)), 0.125,
+                         workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+
+
 @pytest.mark.parametrize("qlens", [[1, 2], [5, 6], [40, 30]])
 def test_cache_least_scales_alone(g, qlens):  # noqa: F811
     rng = np.random.default_rng(1)
