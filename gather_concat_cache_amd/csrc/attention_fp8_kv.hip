@@ -79,6 +79,12 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
     constexpr int NC = DP / 16, LR = kWave / NC, N = kTileKeys / LR;    // chunks of a row, rows of a load, loads of a side
     constexpr int SIDE = kTileKeys * DP;                 // bytes
     constexpr int OROW = DP + 4;
+    // Far pages are looked for in every 32-key tile (64 x 1 over 8192 keys 229 us
+    // against 235 with a look before the first, 32 requests of 2 to 8 tokens behind
+    // a window 70 against 74).  Two row tiles over other pages than whole 16-key
+    // groups have no registers for that and look first, with a loop for either
+    // answer (16 x 8 tokens, pages of 24, 108 against 117).
+    constexpr bool kLook = R > 1 && !UNI;
     static_assert(kFew * 16 * OROW * 4 <= kFew * 4 * SIDE, "the join fits the ring");
     __shared__ __attribute__((aligned(256))) uint8_t s_ring[kFew][4][SIDE];      // K, V of two tiles
     __shared__ float s_m[kFew][16], s_l[kFew][16];
@@ -147,10 +153,13 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
     int v = v0 + w;
     Pages next;                                          // of the tile two ahead
     Scales sc, sc_next;
+    FarLook look;
+    if constexpr (kLook) look.find(p, t, kvh, v0, v1);
     if (v < v1) {
         Pages x = find(v);
         next = find(v + kFew);
         sc = scales(x);
+        if constexpr (kLook) look.load(p);
         issue(x, 0, 0);
         issue(x, 0, 1);
         if (v + kFew < v1) {
@@ -160,18 +169,10 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
             issue(x, 1, 0);
             issue(x, 1, 1);
         }
-    }
+    } else if constexpr (kLook) look.load(p);
 
-    // The rows see a far page: s_far holds their sums then, l does not.  One row
-    // tile looks in every 32-key tile (64 x 1 over 8192 keys 229 us against 235);
-    // two look at all pages first and have a loop for either answer, because that
-    // loop has no registers left (16 x 8 tokens 64 us against 65, pages of 24 108
-    // against 117).
-    bool far = R > 1 && sees_far(p, t, kvh, v0, v1);
-    if (far) {
-#pragma unroll
-        for (int r = 0; r < R; r++) s_far[w][r][lane] = FarSum{kNegInf, 0.0f};
-    }
+    // The rows see a far page: s_far holds their sums then, l does not.
+    bool far = false;
 
     // ---- query rows, the dims as the K reads hold them
     f16x8 q[R][KS];
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
         for (int d = 0; d < DT; d++) o[r][d] = f32x4{0, 0, 0, 0};
     }
 
-    // apart: whether a far page is there, or (R = 1) may be
+    // apart: whether a far page is there, or (without a look) may be
     const auto loop = [&](auto apart) {
         for (int slot = 0; v < v1; v += kFew, slot ^= 1) {
             const bool one = v + kFew < v1, two = v + 2 * kFew < v1;
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
 #pragma unroll
                 for (int kt = 0; kt < 2; kt++) {
                     const PageScale ps = scale_of(sc.raw[kt], sc.live[kt]);
-                    odd = odd || (R == 1 && far_page(t, sc.raw[kt], sc.live[kt], key0 + 16 * kt));
+                    odd = odd || (!kLook && far_page(t, sc.raw[kt], sc.live[kt], key0 + 16 * kt));
                     live |= sc.live[kt] ? 0xFu << (4 * kt) : 0u;
                     inv[kt] = ps.inv_v;
 #pragma unroll
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
                 }
             } else {
                 const PageScale ps = scale_of(sc.raw[0], sc.live[0]);
-                odd = R == 1 && far_page(t, sc.raw[0], sc.live[0], key0 + (lane & 31));
+                odd = !kLook && far_page(t, sc.raw[0], sc.live[0], key0 + (lane & 31));
                 const uint64_t bits = __ballot(sc.live[0]);
                 live = (uint32_t)(bits >> (4 * g) & 0xF) | (uint32_t)(bits >> (16 + 4 * g) & 0xF) << 4;
 #pragma unroll
@@ -359,7 +360,14 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
         }
 
     };
-    if (R == 1 || far) loop(std::true_type{});
+    if constexpr (kLook) {
+        far = __syncthreads_or(look.far(p));
+        if (far) {
+#pragma unroll
+            for (int r = 0; r < R; r++) s_far[w][r][lane] = FarSum{kNegInf, 0.0f};
+        }
+    }
+    if (!kLook || far) loop(std::true_type{});
     else loop(std::false_type{});
 
     // ---- join the four waves, 16 rows at a time

@@ -346,27 +346,64 @@ __device__ __forceinline__ bool far_page(const RowTile& t, const RawScale& r, bo
     return exists && key < t.kv_len && far_scale(page_scale(r.v));
 }
 // Whether a page with keys of the 32-key tiles [v0, v1) is far: the workgroup's
-// lanes look at a page each, before the tile begins.  (4 x 2048 tokens over 4096
-// keys: 1 per cent; looking in every step instead 5.)
-__device__ __forceinline__ bool sees_far(const AttnParams& p, const RowTile& t, int kvh, int v0, int v1) {
-    const int32_t* bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
-    const float* scales = p.gscale[0] + p.L.scale_offset + kvh * p.L.scale_head_stride;
-    bool far = false;
-    const auto look = [&](int key0, int key1) {          // keys [key0, key1)
-        int first, last, off;
-        split_position(p, key0, first, off);
-        split_position(p, max(min(key1, t.kv_len), key0 + 1) - 1, last, off);
-        for (uint32_t i = first + threadIdx.x; i <= (uint32_t)last; i += kTileWaves * kWave) {
-            const PageAt at{bt_row[i], 0};
-            if (page_exists(p, at)) far = far || far_scale(page_scale(scales[(int64_t)at.blk * p.L.scale_token_stride]));
-        }
-    };
-    const int sinks = min(t.sink_tiles, v1), from = max(v0, t.sink_tiles);
-    if (v0 < sinks) look(v0 * kTileKeys, sinks * kTileKeys);
-    if (from < v1) look((from - t.sink_tiles + t.win_tile0) * kTileKeys, (v1 - t.sink_tiles + t.win_tile0) * kTileKeys);
-    return __syncthreads_or(far);
-}
+// lanes look at a page each, two at once.
+struct FarLook {
+    static constexpr int N = 2, THREADS = kTileWaves * kWave;
+    const int32_t* bt_row;
+    const float* scales;
+    int first[2], pages[2];      // of the sinks and of the window
+    int id[N];
+    float scale[N];
 
+    __device__ __forceinline__ int page_id(uint32_t i) const {       // of the i-th page, -1 behind the last
+        const bool sink = i < (uint32_t)pages[0];
+        const uint32_t k = sink ? i : i - pages[0];
+        return k < (uint32_t)pages[sink ? 0 : 1] ? bt_row[first[sink ? 0 : 1] + k] : -1;
+    }
+    // (a page that does not exist counts as ordinary)
+    __device__ __forceinline__ float scale_of_page(const AttnParams& p, int blk) const {
+        return page_exists(p, PageAt{blk, 0}) ? scales[(int64_t)blk * p.L.scale_token_stride] : 1.0f;
+    }
+    __device__ __forceinline__ void find(const AttnParams& p, const RowTile& t, int kvh, int v0, int v1) {
+        bt_row = p.block_table + (int64_t)t.b * p.bt_stride;
+        scales = p.gscale[0] + p.L.scale_offset + kvh * p.L.scale_head_stride;
+        const int from[2] = {v0, max(v0, t.sink_tiles) - t.sink_tiles + t.win_tile0};
+        const int to[2] = {min(v1, t.sink_tiles), v1 - t.sink_tiles + t.win_tile0};      // 32-key tiles
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int key0 = from[k] * kTileKeys, key1 = min(to[k] * kTileKeys, t.kv_len);
+            int last = 0, off;
+            first[k] = pages[k] = 0;
+            if (key0 < key1) {
+                split_position(p, key0, first[k], off);
+                split_position(p, key1 - 1, last, off);
+                pages[k] = last + 1 - first[k];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < N; n++) id[n] = page_id(threadIdx.x + n * THREADS);
+    }
+    __device__ __forceinline__ void load(const AttnParams& p) {
+#pragma unroll
+        for (int n = 0; n < N; n++) scale[n] = scale_of_page(p, id[n]);
+    }
+    __device__ __forceinline__ bool far(const AttnParams& p) const {         // the lane's pages
+        bool x = false;
+#pragma unroll
+        for (int n = 0; n < N; n++) x = x || far_scale(page_scale(scale[n]));
+        const uint32_t all = (uint32_t)pages[0] + (uint32_t)pages[1];
+        for (uint32_t i = threadIdx.x + N * THREADS; i < all; i += THREADS) x = x || far_scale(page_scale(scale_of_page(p, page_id(i))));
+        return x;
+    }
+};
+
+// The lane's part of it, in one go.
+__device__ __forceinline__ bool sees_far(const AttnParams& p, const RowTile& t, int kvh, int v0, int v1) {
+    FarLook look;
+    look.find(p, t, kvh, v0, v1);
+    look.load(p);
+    return look.far(p);
+}
 struct NoWalk {};
 
 // N fragments with DEPTH reads in flight.  Piece i of `side`, vector work that
@@ -518,17 +555,25 @@ __device__ __forceinline__ void multiply_keys(uint32_t k_at, const typename T::f
 // size is DK and whose pages are whole 16-key groups within 32 bits.
 // CAREFUL: values of hidden keys may be infinities or NaN, which a weight of 0
 // would let through: looked for in every step with a mask.  Without it such a
-// value makes a NaN, and the tile is computed again with it.  Returns whether
-// there is a NaN in the workgroup's tile, when not CAREFUL; nothing is written
-// then.
+// value makes a NaN, and the tile is computed again with it.  When not CAREFUL,
+// returns kSawNan and kSawFar where there is a NaN in the workgroup's tile or a far
+// page among its keys; nothing is written then.
+// apart: sum the weights apart (FarSum; CAREFUL only).
 //
 // The scores of step i + 1 are multiplied while step i's weights are computed,
 // and its values while the next logits are scaled: a wave's matrix instructions
 // and its vector ones are independent, and run side by side.
-// apart: the tile sees far pages and sums its weights apart (FarSum; CAREFUL only).
+constexpr uint32_t kSawNan = 1, kSawFar = 2;
+// A tile of many rows looks for far pages behind its last step, when the scales
+// are in L2 (3 chunks over 2 k to 6 k keys 441 us, 438 without a look; before the
+// first step 453, in every step 460); with 256 dims before the first (4 x 2048
+// tokens over 4096 keys 460 us, 548 behind the last, 530 without: the compiler
+// then spills fewer registers).
+template <int DK>
+constexpr bool kLookFirst = DK > 128;
 template <typename T, int DK, int DV, bool EX, bool TREE, bool CAREFUL, typename P>
-__device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kvh, int v0, int v1, bool apart,
-                                            StepLds<T, DK, DV, EX>& lds) {
+__device__ __forceinline__ uint32_t attend_once(const P& p, const RowTile& t, int kvh, int v0, int v1, bool apart,
+                                                StepLds<T, DK, DV, EX>& lds) {
     typedef StepLds<T, DK, DV, EX> L;
     typedef typename T::frag frag;
     constexpr int KS = DK / 16, DT = DV / 32, KC = L::KB / 16, VC = L::VB / 16;
@@ -848,11 +893,12 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         uint32_t* flag;
         if constexpr (FP8) flag = reinterpret_cast<uint32_t*>(lds.at[(n + 1) & 3]);
         else flag = reinterpret_cast<uint32_t*>(lds.v[(n + 1) & 1]);
-        if (lane == 0) flag[w] = 0;
-        wave_lds_ready();
-        if (busy && any != any) flag[w] = 1;
+        uint32_t saw = __any(busy && any != any) ? kSawNan : 0;
+        if constexpr (FP8 && !kLookFirst<DK>) saw |= __any(sees_far(p, t, kvh, v0, v1)) ? kSawFar : 0;
+        if (lane == 0) flag[w] = saw;
         __syncthreads();
-        if (flag[0] | flag[1] | flag[2] | flag[3]) return true;
+        saw = flag[0] | flag[1] | flag[2] | flag[3];
+        if (saw) return saw;
     }
 
     // ---- each lane holds runs of four dims of its rows.  They go through LDS, so that a store writes whole rows (16 bytes
@@ -877,7 +923,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     const int row = max(row_of, 0), tl = row_token(p, row), head = kvh * p.group + row - tl * p.group;
     const int64_t token = t.q0 + tl, id = token * p.hq + head;
     if (partial) {
-        if (!in) return false;
+        if (!in) return 0;
         if (h == 0) {
             float* ml = p.ws_ml + 2 * ((int64_t)t.split * p.total_q * p.hq + id);
             ml[0] = m - T::kShiftUp + kShift;         // the join takes kShift off
@@ -891,7 +937,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                 if (EX || 32 * d + 8 * a + 4 * h < p.hs)
                     *reinterpret_cast<f32x4*>(dst + 32 * d + 8 * a) =
                         f32x4{o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2], o[d][4 * a + 3]};
-        return false;
+        return 0;
     }
     RowEnd end{0.0f, 0.0f, 0.0f};
     if (in) {
@@ -900,7 +946,7 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
     }
     uint16_t* dst = p.out + token * p.o_ts + (int64_t)head * p.o_hs;
     if (accumulates(p)) {
-        if (!in) return false;
+        if (!in) return 0;
 #pragma unroll
         for (int d = 0; d < DT; d++)
 #pragma unroll
@@ -908,9 +954,9 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
                 if (EX || 32 * d + 8 * a + 4 * h < p.hs)
                     write_dims(p, end, dst + 32 * d + 8 * a + 4 * h, o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2],
                                o[d][4 * a + 3]);
-        return false;
+        return 0;
     }
-    if (!busy) return false;                             // wave-uniform
+    if (!busy) return 0;                             // wave-uniform
 #pragma unroll
     for (int d = 0; d < DT; d++)
 #pragma unroll
@@ -927,16 +973,17 @@ __device__ __forceinline__ bool attend_once(const P& p, const RowTile& t, int kv
         const uint64_t at = (uint64_t)(uint32_t)__shfl((int)(to >> 32), from) << 32 | (uint32_t)__shfl((int)to, from);
         if (at != 0 && (EX || 8 * chunk < p.hs)) *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(at) + 8 * chunk) = x;
     }
-    return false;
+    return 0;
 }
 
 template <typename T, int DK, int DV, bool EX, bool TREE, typename P>
 __device__ __forceinline__ void attend_tile(const P& p, const RowTile& t, int kvh, int v0, int v1, StepLds<T, DK, DV, EX>& lds) {
-    bool apart = false;
-    if constexpr (T::kFp8) apart = sees_far(p, t, kvh, v0, v1);
-    if (apart || attend_once<T, DK, DV, EX, TREE, false>(p, t, kvh, v0, v1, false, lds)) {
+    uint32_t saw = 0;
+    if constexpr (T::kFp8 && kLookFirst<DK>) saw = __syncthreads_or(sees_far(p, t, kvh, v0, v1)) ? kSawFar : 0;
+    if (!saw) saw = attend_once<T, DK, DV, EX, TREE, false>(p, t, kvh, v0, v1, false, lds);
+    if (saw) {
         __syncthreads();
-        attend_once<T, DK, DV, EX, TREE, true>(p, t, kvh, v0, v1, apart, lds);
+        attend_once<T, DK, DV, EX, TREE, true>(p, t, kvh, v0, v1, (saw & kSawFar) != 0, lds);
     }
 }
 

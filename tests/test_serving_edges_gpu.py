@@ -360,3 +360,50 @@ def test_cache_every_form_is_there():
     padded = lambda hs: 64 if hs <= 64 else 128 if hs <= 128 else 256  # noqa: E731
     assert {(r, padded(hs)) for r, _, _, _, hs in FORM_CASES} == {(16, 64), (16, 128), (16, 256), (32, 64), (32, 128), (128, 64), (128, 128),
                                                                   (128, 256)}
+
+
+# ---------------------------------------------------------------------------
+# other calls that the headers allow
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_without_any_keys(g, causal):  # noqa: F811
+    """No key in the whole batch: zeros with lse -infinity, or what an earlier
+    part left."""
+    rng = np.random.default_rng(2)
+    q = ref.bf16(rng.standard_normal((40, 4, 128)))[0].cuda()
+    k = torch.empty(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    qs, ks = dev(np.array([0, 7, 40], np.int32)), torch.zeros(3, dtype=torch.int32, device="cuda")
+    out, lse = g.prompt_attention(q, k, k, qs, ks, 0, 0.1, causal=causal, return_lse=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    part, part_lse = ref.bf16(rng.standard_normal((40, 4, 128)))[0].cuda(), dev(rng.standard_normal((40, 4)).astype(np.float32))
+    out, lse = part.clone(), part_lse.clone()
+    g.prompt_attention(q, k, k, qs, ks, 0, 0.1, causal=causal, out=out, lse=lse, accumulate=True)
+    assert torch.equal(out, part) and torch.equal(lse, part_lse)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("bs", [16, 128, 1024])
+def test_append_in_place_whatever_the_page(g, bs, inter):  # noqa: F811
+    """k_out=k where a page's rows stay in registers and where they are read
+    twice: the bits of a call with outputs of its own."""
+    rng = np.random.default_rng(bs)
+    hq, hk, hs, rot, lens = 4, 3, 64, 48, [1100, 40, 300]
+    T, pages = sum(lens), [-(-n // bs) for n in lens]
+    table = np.full((3, max(pages)), -1, np.int32)
+    order = rng.permutation(sum(pages))
+    for b, n in enumerate(pages):
+        table[b, :n] = order[sum(pages[:b]):sum(pages[:b + 1])]
+    qkv = ref.bf16(rng.standard_normal((T, hq + 2 * hk, hs)))[0].cuda()
+    cs = dev(rng.standard_normal((1200, rot)).astype(np.float32))
+    got = []
+    for own in (True, False):
+        x = qkv.clone()
+        q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+        cache = torch.zeros(sum(pages), 2, bs, hk, hs, dtype=torch.uint8, device="cuda")
+        scales = torch.zeros(sum(pages), 2, hk, device="cuda")
+        starts = dev(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+        out = g.rope_append_fp8_kv(q, k, v, cache, scales, dev(table), starts, dev(np.array(lens, np.int32)), cs, interleaved=inter,
+                                   return_k=True, **({} if own else dict(q_out=q, k_out=k)))
+        got.append((*out, cache, scales, v.clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(got[0][4], qkv[:, hq + hk:])
