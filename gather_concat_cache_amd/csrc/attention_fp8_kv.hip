@@ -20,8 +20,8 @@ namespace gcache {
 
 // Many query rows.  Bound by instruction issue: e4m3's conversions and the
 // exponentials beside the products.  4 x 2048 tokens over 4096 keys, 32 / 8 heads
-// of 128: 515 us, 800 TFLOP/s; with 256 dims (a workgroup a CU: registers) 770.
-// Other pages than whole 16-key groups look up a page and a scale a key: 600.
+// of 128: 497 us, 830 TFLOP/s; with 256 dims (a workgroup a CU: registers) 895.
+// Other pages than whole 16-key groups look up a page and a scale a key: 620.
 template <int DP, bool UNI, bool TREE>
 __global__ __launch_bounds__(kTileWaves * kWave, DP <= 128 ? 2 : 1) void k_fp8_rows(AttnParams p, int64_t wg0) {
     __shared__ StepLds<PagedFp8, DP, DP, UNI> lds;

@@ -93,7 +93,8 @@ struct PackedBf16 {
     typedef bf16x8 frag;
     static constexpr bool kFp8 = false;
     static constexpr int kBytes = 2;
-    static constexpr float kShiftUp = 0.0f;              // bf16 weights have binary32's range
+    // Weights become bf16, the values' type, because a product takes both operands in one; a row's sum has them unrounded.
+    static constexpr float kShiftUp = 0.0f;              // (they have binary32's range)
     static constexpr int kDepth = 3;                     // reads in flight (2, 3, 4: 1007, 1019, 1013 TFLOP/s with 128 dims)
     static __device__ __forceinline__ f32x16 mma(const frag& a, const frag& b, const f32x16& c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);

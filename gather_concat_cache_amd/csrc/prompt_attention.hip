@@ -3,7 +3,7 @@
 //
 // Bound by the matrix and vector instructions of two waves a SIMD that do not
 // fully overlap.  4 x 4096 tokens, not causal, TFLOP/s: 128 dims 1000, keys of
-// 192 and values of 128 1105, 256 dims 915 (one workgroup a CU: its accumulators
+// 192 and values of 128 1105, 256 dims 905 (one workgroup a CU: its accumulators
 // fill the registers), 64 800 (as many exponentials for half the products).
 // Head sizes between run in the next larger form with a test a chunk (80: 687
 // of its own operations).

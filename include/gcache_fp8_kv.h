@@ -102,8 +102,13 @@ int gcache_rope_append_fp8_kv(const gcache_append_args* args, void* kv_cache, fl
  * gcache_tree_attention_nvfp4_kv (window 0 then).  An e4m3 NaN code (no write
  * makes one) that a row does not see cannot reach it; a row that sees one may
  * take it as a NaN or as 0.
+ * Any value scale is right; rows that see one outside 2^-40 .. 2^24 (of pages of
+ * zeros, for instance) may take up to three times as long where a request has
+ * more than 32 rows a kv head.
  * Requirements: as there, head_size a multiple of 16 up to 256; the layout's
- * strides as above.  Workspace: gcache_attention_fp8_kv_workspace_bytes().
+ * strides as above; fewer than 2^31 workgroups, which is certain when (batch_size
+ * + 8) * num_kv_heads <= 2^30 (more: GCACHE_ERR_SHAPE).  Workspace:
+ * gcache_attention_fp8_kv_workspace_bytes().
  */
 int gcache_attention_fp8_kv(const gcache_attention_args* args, const void* kv_cache, const float* kv_scales,
                             const gcache_fp8_kv_layout* layout, int32_t num_kv_heads, int32_t head_size,

@@ -50,7 +50,9 @@ extern "C" {
  * 8; everything 16-byte aligned; token strides of k and v at most 2^23
  * (larger: GCACHE_ERR_UNSUPPORTED); no two rows of out share an element, and
  * out must not overlap the inputs; num_q_heads a multiple of num_kv_heads;
- * total_q * num_q_heads <= 2^31 - 128; total_q + total_k <= 2^31 - 256.
+ * total_q * num_q_heads <= 2^31 - 128; total_q + total_k <= 2^31 - 256; fewer than
+ * 2^31 workgroups, which is certain when (batch_size + 8) * num_kv_heads <= 2^30
+ * (more: GCACHE_ERR_SHAPE).
  */
 typedef struct {
     const void* q;               /* bf16 [total_q, num_q_heads, key_size] */
