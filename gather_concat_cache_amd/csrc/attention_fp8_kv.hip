@@ -358,7 +358,6 @@ __global__ __launch_bounds__(kFew * kWave, DP <= 128 ? 2 : 1) void k_fp8_few(Att
             sc = sc_next;
             if (two) sc_next = sc_two;
         }
-
     };
     if constexpr (kLook) {
         far = __syncthreads_or(look.far(p));
